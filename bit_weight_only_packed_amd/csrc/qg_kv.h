@@ -1,0 +1,112 @@
+// qg_kv.h -- the paged key-value cache as its kernels see it: the device view of
+// a cache, the rows of a call, and the launchers (host code: qgkv.hip).  The
+// kernels: qg_kv_pages.h (page operations, append), qg_attn_step.h (attention of
+// few rows), qg_attn_rows.h (attention of many rows).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace qg {
+
+constexpr int KV_MAX_SEQS = 1024;
+
+// one layer of a cache
+struct KvDev {
+  const uint16_t* pool;  // this layer's keys of page 0
+  const int32_t* tables;
+  const int32_t* lens;
+  int64_t page_stride;   // elements from a page to the next
+  int64_t v_off;         // elements from a page's keys to its values
+  int pages, max_pages, max_seqs, page_shift, kv_heads;
+  int cap;               // max_pages * page_size
+};
+
+struct KvRows {
+  const uint16_t* ptr;
+  int64_t row, head;     // strides in elements
+};
+
+struct KvBatchDev {
+  const int32_t* seqs;       // or NULL
+  const int32_t* row_start;  // or NULL
+  int n, rows, max_rows;     // entries, rows in all, rows of an entry at most
+};
+
+// entry j of a call: slot, length, first row, rows.  Everything that comes from
+// device memory is cut to what the cache and the call's operands hold.
+struct KvEntry {
+  int slot, len, row0, rows;
+};
+__device__ __forceinline__ KvEntry kv_entry(const KvDev& c, const KvBatchDev& b, int j) {
+  KvEntry e;
+  int s = b.seqs ? b.seqs[j] : j;
+  const bool ok = (unsigned)s < (unsigned)c.max_seqs;
+  e.slot = ok ? s : 0;
+  const int len = c.lens[e.slot];
+  e.len = ok ? min(max(len, 0), c.cap) : 0;
+  if (b.row_start) {
+    e.row0 = min(max(b.row_start[j], 0), b.rows);
+    const int end = min(max(b.row_start[j + 1], e.row0), b.rows);
+    e.rows = min(end - e.row0, b.max_rows);
+  } else {
+    e.row0 = j * b.max_rows;
+    e.rows = b.max_rows;
+  }
+  return e;
+}
+
+// page that a table names, or page 0 where it names none of the pool
+__device__ __forceinline__ int kv_page(const KvDev& c, int id) { return (unsigned)id < (unsigned)c.pages ? id : 0; }
+
+// 16 bytes = 8 elements
+typedef uint32_t kv_u4 __attribute__((ext_vector_type(4)));
+typedef uint32_t kv_u2 __attribute__((ext_vector_type(2)));
+
+// ---- page operations ---------------------------------------------------------
+struct KvPool {
+  uint16_t* pool;
+  int32_t *tables, *lens, *refs, *info;
+  int64_t page_bytes;
+  int pages, max_seqs, max_pages, page_shift;
+  // workspace: [0] copies to make, [1] first id that moves (compact), then the
+  // lists of source and destination pages and the moved pages' new ids
+  int32_t* head;
+  int32_t *from, *to, *place;
+};
+
+hipError_t launch_kv_fork(const KvPool& p, const int32_t* src, const int32_t* dst, int n, hipStream_t st);
+hipError_t launch_kv_trim(const KvPool& p, const int32_t* seqs, const int32_t* keep, int n, hipStream_t st);
+hipError_t launch_kv_extend(const KvPool& p, const int32_t* n_new, int cus, hipStream_t st);
+hipError_t launch_kv_compact(const KvPool& p, int cus, hipStream_t st);
+hipError_t launch_kv_append(const KvDev& c, const KvBatchDev& b, const KvRows& k, const KvRows& v, int D, hipStream_t st);
+
+// ---- attention ---------------------------------------------------------------
+struct AttnArgs {
+  KvDev c;
+  KvBatchDev b;
+  KvRows q, out;
+  int G;               // q heads per kv head
+  float scale_log2;    // scale * log2(e)
+  int window, sinks;   // window 0: none
+  float* partial;      // see the kernels
+  int* counters;       // zero between launches
+  int workers;         // few rows: workgroups that share the tiles
+  int splits;          // many rows: workgroups that may share a block's tiles
+};
+
+// rows of one kv head that the few-row kernel takes: (new rows) * (q heads per
+// kv head); wide heads hold fewer for lack of registers
+__host__ __device__ constexpr int step_max_rows(int D) { return D == 256 ? 32 : 64; }
+constexpr int STEP_WORKERS_PER_CU = 2;
+// fp32 words of one partial of MT row tiles: o, then (max, sum) of each row
+__host__ __device__ constexpr size_t step_slot(int MT, int D) { return (size_t)MT * 16 * (D + 2); }
+hipError_t launch_attn_step(const AttnArgs& a, int D, bool bf16, int MT, hipStream_t st);
+
+constexpr int ROWS_BM = 128;  // rows of a block of the many-row kernel
+__host__ __device__ constexpr size_t rows_slot(int D) { return (size_t)ROWS_BM * (D + 2); }
+hipError_t launch_attn_rows(const AttnArgs& a, int D, bool bf16, unsigned blocks, hipStream_t st);
+hipError_t attn_step_allow_lds();
+hipError_t attn_rows_allow_lds();
+
+}  // namespace qg

@@ -17,13 +17,16 @@
 #include <vector>
 
 #include "../../include/qgemv.h"
+#include "qg_error.h"
 #include "qg_launch.h"
 
 using namespace qg;
 
 namespace {
-
 thread_local std::string g_err;
+}  // namespace
+
+namespace qg {
 
 qg_status fail(qg_status st, const char* fmt, ...) {
   char buf[512];
@@ -34,6 +37,23 @@ qg_status fail(qg_status st, const char* fmt, ...) {
   g_err = buf;
   return st;
 }
+
+void clear_error() { g_err.clear(); }
+
+qg_status check_device(int* dev) {
+  int d = 0;
+  if (hipGetDevice(&d) != hipSuccess) return fail(QG_ERR_UNSUPPORTED, "no HIP device available");
+  hipDeviceProp_t prop;
+  if (hipGetDeviceProperties(&prop, d) != hipSuccess) return fail(QG_ERR_UNSUPPORTED, "cannot query HIP device");
+  if (std::strncmp(prop.gcnArchName, "gfx950", 6) != 0)
+    return fail(QG_ERR_UNSUPPORTED, "device %d is %s; this library is built for gfx950 only", d, prop.gcnArchName);
+  *dev = d;
+  return QG_OK;
+}
+
+}  // namespace qg
+
+namespace {
 
 #define QG_HIP(call)                                                                   \
   do {                                                                                 \
@@ -389,17 +409,6 @@ qg_status size_workspace(qg_plan* h, size_t* floats) {
       if (!p.fx) need = std::max(need, xs_partial_need(p, dual ? 2 : 1));
     }
   *floats = need;
-  return QG_OK;
-}
-
-qg_status check_device(int* dev) {
-  int d = 0;
-  if (hipGetDevice(&d) != hipSuccess) return fail(QG_ERR_UNSUPPORTED, "no HIP device available");
-  hipDeviceProp_t prop;
-  if (hipGetDeviceProperties(&prop, d) != hipSuccess) return fail(QG_ERR_UNSUPPORTED, "cannot query HIP device");
-  if (std::strncmp(prop.gcnArchName, "gfx950", 6) != 0)
-    return fail(QG_ERR_UNSUPPORTED, "device %d is %s; this library is built for gfx950 only", d, prop.gcnArchName);
-  *dev = d;
   return QG_OK;
 }
 
