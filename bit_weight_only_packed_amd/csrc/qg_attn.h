@@ -52,37 +52,50 @@ template <int H> __device__ __forceinline__ uint32_t at_halves(uint32_t a, uint3
 
 // Non-finite values.  A weight of 0 does not keep a NaN or infinity out of a sum
 // of products, so where a tile holds tokens that some of its rows see and others
-// do not, its values are looked at, and where one is not finite the products run
-// over the values with 0 in its place, and the rows that do see it (a product of
-// indicators) get it added: +inf, -inf, or both for a NaN.
+// do not, its values are looked at.  One that is not finite is taken out (0) and
+// noted, a bit for +inf or NaN and a bit for -inf or NaN; after the products each
+// row that does see the token gets the infinity added, or both.
 template <bool BF> __device__ __forceinline__ uint32_t at_exp_mask() { return BF ? 0x7F80u : 0x7C00u; }
 template <bool BF> __device__ __forceinline__ bool at_odd1(uint32_t h) { return (h & at_exp_mask<BF>()) == at_exp_mask<BF>(); }
-template <bool BF> __device__ __forceinline__ bool at_odd(uint32_t w) { return at_odd1<BF>(w) || at_odd1<BF>(w >> 16); }
-template <bool BF> __device__ __forceinline__ uint32_t at_one() { return BF ? 0x3F80u : 0x3C00u; }
-// one half: finite part, and indicators of +inf-or-NaN and -inf-or-NaN
-template <bool BF> __device__ __forceinline__ uint32_t at_fin1(uint32_t h) { return at_odd1<BF>(h) ? 0u : h & 0xFFFFu; }
-template <bool BF> __device__ __forceinline__ uint32_t at_ind1(uint32_t h, bool neg) {
-  const bool nan = (h & 0x7FFFu) > at_exp_mask<BF>();
-  return at_odd1<BF>(h) && (nan || ((h & 0x8000u) != 0) == neg) ? at_one<BF>() : 0u;
+template <bool BF> __device__ __forceinline__ bool at_odd(uint32_t w) {
+  return (int)at_odd1<BF>(w) | (int)at_odd1<BF>(w >> 16);
 }
-template <bool BF> __device__ __forceinline__ uint32_t at_fin(uint32_t w) {
-  return at_fin1<BF>(w) | at_fin1<BF>(w >> 16) << 16;
+// take what is not finite out of two values; bits `at` and `at` + 1 of pos and neg note it
+template <bool BF> __device__ __forceinline__ uint32_t at_take(uint32_t w, int at, uint32_t& pos, uint32_t& neg) {
+  asm volatile("" : "+v"(w));  // its classification is not carried over from the check: registers are dearer here
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t h = (w >> (16 * i)) & 0xFFFFu;
+    const uint32_t odd = at_odd1<BF>(h), nan = (h & 0x7FFFu) > at_exp_mask<BF>(), sign = h >> 15;
+    pos |= (odd & (nan | (sign ^ 1u))) << (at + i);
+    neg |= (odd & (nan | sign)) << (at + i);
+    if (odd) w &= ~(0xFFFFu << (16 * i));
+  }
+  return w;
 }
-template <bool BF> __device__ __forceinline__ uint32_t at_ind(uint32_t w, bool neg) {
-  return at_ind1<BF>(w, neg) | at_ind1<BF>(w >> 16, neg) << 16;
-}
-// what a row that sees p values of +inf or NaN and n of -inf or NaN has to add
-__device__ __forceinline__ float at_add_odd(float p, float n) {
+// what bits p and n of a noted value add to the output of a row that sees it
+__device__ __forceinline__ float at_noted(uint32_t p, uint32_t n) {
   const float inf = __builtin_inff();
-  return (p > 0.0f ? inf : 0.0f) + (n > 0.0f ? -inf : 0.0f);
+  return ((p & 1) ? inf : 0.0f) + ((n & 1) ? -inf : 0.0f);
 }
 
-// Partials go past the per-XCD L2 caches (agent scope), as in qg_common.h.
-__device__ __forceinline__ void at_st(float* p, float v) {
-  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// Partials go past the per-XCD L2 caches (agent scope), as in qg_common.h, here
+// 16 bytes at a time: buffer accesses with the cache policy of an agent-scope atomic.
+constexpr int AT_AGENT = 16;  // sc1
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t at_slots(float* p, size_t floats) {
+  return __builtin_amdgcn_make_buffer_rsrc(p, 0, (int)(floats * 4), 0x00020000);
 }
-__device__ __forceinline__ float at_ld(const float* p) {
-  return __hip_atomic_load(const_cast<float*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+__device__ __forceinline__ void at_st4(__amdgpu_buffer_rsrc_t r, uint32_t at, at_f4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(kv_u4, v), r, (int)(at * 4), 0, AT_AGENT);
+}
+__device__ __forceinline__ void at_st2(__amdgpu_buffer_rsrc_t r, uint32_t at, float x, float y) {
+  __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(kv_u2, at_f2{x, y}), r, (int)(at * 4), 0, AT_AGENT);
+}
+__device__ __forceinline__ at_f4 at_ld4(__amdgpu_buffer_rsrc_t r, uint32_t lane_at, uint32_t slot) {
+  return __builtin_bit_cast(at_f4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(lane_at * 4), (int)(slot * 4), AT_AGENT));
+}
+__device__ __forceinline__ at_f2 at_ld2(__amdgpu_buffer_rsrc_t r, uint32_t lane_at, uint32_t slot) {
+  return __builtin_bit_cast(at_f2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)(lane_at * 4), (int)(slot * 4), AT_AGENT));
 }
 
 // The workgroup's arrival at a counter of n, after its partial: true in the one
@@ -120,42 +133,44 @@ __device__ __forceinline__ void at_store(const AttnArgs& a, const KvEntry& e, in
 }
 
 // Join n partials of rows r0 .. r0 + nrows - 1 of (entry, head) in the order 0, 1,
-// ...; slot(k) is the k-th: [ld][D] fp32, then (m, l) of each row.  The loads of
-// eight partials are in flight at once.
+// ...; slot(k) is where the k-th lies (in floats): [ld][D] fp32, then (m, l) of each
+// row.  The loads of eight partials are in flight at once.
 template <bool BF, int D, class F>
-__device__ __forceinline__ void at_join(const AttnArgs& a, const KvEntry& e, int head, int r0, int nrows, int ld, int n, F slot) {
+__device__ __forceinline__ void at_join(const AttnArgs& a, __amdgpu_buffer_rsrc_t rs, const KvEntry& e, int head, int r0,
+                                        int nrows, int ld, int n, F slot) {
   constexpr int NB = 8;
   for (int it = threadIdx.x; it < nrows * (D / 4); it += blockDim.x) {
     const int r = it / (D / 4), c = (it % (D / 4)) * 4;
-    float M = -__builtin_inff(), L = 0.0f, o[4] = {0, 0, 0, 0};
+    const uint32_t at_o = (uint32_t)r * D + c, at_m = (uint32_t)ld * D + 2 * r;
+    float M = -__builtin_inff(), L = 0.0f;
+    at_f4 o = {0, 0, 0, 0};
     for (int k0 = 0; k0 < n; k0 += NB) {
-      float pm[NB], pl[NB], po[NB][4];
+      at_f2 pm[NB];
+      at_f4 po[NB];
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
-        const float* s = slot(min(k0 + k, n - 1));
-        pm[k] = at_ld(s + (size_t)ld * D + 2 * r);
-        pl[k] = at_ld(s + (size_t)ld * D + 2 * r + 1);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) po[k][x] = at_ld(s + (size_t)r * D + c + x);
+        const uint32_t s = slot(min(k0 + k, n - 1));
+        pm[k] = at_ld2(rs, at_m, s);
+        po[k] = at_ld4(rs, at_o, s);
       }
       float Mn = M;
 #pragma unroll
-      for (int k = 0; k < NB; ++k) Mn = fmaxf(Mn, pm[k]);
+      for (int k = 0; k < NB; ++k) Mn = fmaxf(Mn, pm[k].x);
       const float f0 = at_exp2(M - at_safe(Mn));
       M = Mn;
       L *= f0;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) o[x] *= f0;
+      o *= f0;
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
         if (k0 + k >= n) break;
-        const float f = at_exp2(pm[k] - at_safe(Mn));
-        L = __builtin_fmaf(f, pl[k], L);
+        const float f = at_exp2(pm[k].x - at_safe(Mn));
+        L = __builtin_fmaf(f, pm[k].y, L);
 #pragma unroll
         for (int x = 0; x < 4; ++x) o[x] = __builtin_fmaf(f, po[k][x], o[x]);
       }
     }
-    at_store<BF, 4>(a, e, head, r0 + r, c, o, L);
+    const float res[4] = {o.x, o.y, o.z, o.w};
+    at_store<BF, 4>(a, e, head, r0 + r, c, res, L);
   }
 }
 

@@ -39,7 +39,9 @@ template <int D> struct StepShape {
   static constexpr int VB = D == 64 ? 8 : 16;    // bytes of a lane's value load
   static constexpr int VL = VE * 2 / VB;         // value loads per token
   static constexpr int LD = D + 4;               // padded row of the cross-wave buffer (floats)
-  static constexpr size_t lds = (size_t)ST_NW * 16 * LD * 4 + ST_NW * 16 * 8 + 16;
+  static constexpr int NB = VL * 16;             // bytes of noted values per token (one per value load)
+  static constexpr size_t notes = (size_t)ST_NW * 2 * ST_TK * NB;
+  static constexpr size_t lds = (size_t)ST_NW * 16 * LD * 4 + ST_NW * 16 * 8 + notes + 16;
 };
 
 template <int D, bool BF, int MT> struct StepTile {
@@ -98,12 +100,12 @@ __device__ __forceinline__ void step_load_v(StepTile<D, BF, MT>& t, const KvDev&
 }
 
 // the lane's 8 tokens of its column x: the A operand of product tile x
-template <int VE, class F> __device__ __forceinline__ kv_u4 step_column(const uint32_t (&v)[8][VE / 2], int x, F f) {
+template <int VE> __device__ __forceinline__ kv_u4 step_column(const uint32_t (&v)[8][VE / 2], int x) {
   kv_u4 r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t a = v[2 * i][x >> 1], b = v[2 * i + 1][x >> 1];
-    r[i] = f((x & 1) ? at_halves<1>(a, b) : at_halves<0>(a, b));
+    r[i] = (x & 1) ? at_halves<1>(a, b) : at_halves<0>(a, b);
   }
   return r;
 }
@@ -115,17 +117,20 @@ template <int D> __device__ __forceinline__ int step_col(int q, int i, int x) {
 }
 
 template <int D, bool BF, int MT>
-__global__ __launch_bounds__(64 * ST_NW) __attribute__((amdgpu_waves_per_eu(MT * D <= 256 ? 2 : 1)))
+__global__ __launch_bounds__(64 * ST_NW) __attribute__((amdgpu_waves_per_eu(step_per_cu(MT, D))))
 void k_attn_step(AttnArgs a) {
   using S = StepShape<D>;
   extern __shared__ __align__(16) char smem[];
   float* buf = reinterpret_cast<float*>(smem);                                    // [wave][16][LD]
   float* ml = buf + ST_NW * 16 * S::LD;                                           // [wave][16][2]
-  int* flag = reinterpret_cast<int*>(ml + ST_NW * 16 * 2);
+  uint8_t* notes = reinterpret_cast<uint8_t*>(ml + ST_NW * 16 * 2);               // [wave][2][32][NB]
+  int* flag = reinterpret_cast<int*>(notes + S::notes);
   int* pre = flag + 4;                                                            // [n + 1]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = lane >> 4, col = lane & 15;
   const int n = a.b.n, heads = a.c.kv_heads;
+  notes += (size_t)wave * 2 * ST_TK * S::NB;
+  const auto rs = at_slots(a.partial, a.partial_floats);
 
   // prefix sums of the entries' tiles (at least one for an entry with rows, which
   // has outputs to write even where it sees nothing)
@@ -287,48 +292,59 @@ void k_attn_step(AttnArgs a) {
           const bool seen = key <= p1 && (a.window == 0 || key > max(p0, 0) - a.window || key < a.sinks);
 #pragma unroll
           for (int c = 0; c < S::VE / 2; ++c) {
-            if (!seen) t.v[i][c] = 0;
+            t.v[i][c] = seen ? t.v[i][c] : 0;
             nf |= at_odd<BF>(t.v[i][c]);
           }
         }
         odd = __any(nf);
+        if (odd) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int x = 0; x < S::VL; ++x) {
+              uint32_t bp = 0, bn = 0;
+#pragma unroll
+              for (int c = 0; c < S::VB / 4; ++c)
+                t.v[i][x * S::VB / 4 + c] = at_take<BF>(t.v[i][x * S::VB / 4 + c], 2 * c, bp, bn);
+              notes[(8 * q + i) * S::NB + x * 16 + col] = (uint8_t)bp;
+              notes[(ST_TK + 8 * q + i) * S::NB + x * 16 + col] = (uint8_t)bn;
+              __builtin_amdgcn_sched_barrier(0);
+            }
+        }
       }
-      if (!odd) {
 #pragma unroll
-        for (int c = 0; c < S::VE; ++c) {
-          const kv_u4 A = step_column<S::VE>(t.v, c, [](uint32_t w) { return w; });
+      for (int c = 0; c < S::VE; ++c) {
+        const kv_u4 A = step_column<S::VE>(t.v, c);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) O[mt][c] = at_mfma16<BF>(A, P[mt], O[mt][c]);
-        }
-      } else {
+        for (int mt = 0; mt < MT; ++mt) O[mt][c] = at_mfma16<BF>(A, P[mt], O[mt][c]);
+      }
+      if (odd) {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll 1
+        for (int k = 0; k < ST_TK; ++k)
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          kv_u4 I;  // which of the lane's tokens its row sees
+          for (int mt = 0; mt < MT; ++mt) {
+            if (!at_sees(pos[mt], tok + k, a.window, a.sinks)) continue;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = tok + 8 * q + 2 * i;
-            I[i] = (at_sees(pos[mt], key, a.window, a.sinks) ? at_one<BF>() : 0u) |
-                   (at_sees(pos[mt], key + 1, a.window, a.sinks) ? at_one<BF>() << 16 : 0u);
+            for (int x = 0; x < S::VL; ++x) {
+              // the notes of this lane's 4 groups of columns
+              const uint32_t p = *reinterpret_cast<const uint32_t*>(notes + k * S::NB + x * 16 + 4 * q);
+              const uint32_t n = *reinterpret_cast<const uint32_t*>(notes + (ST_TK + k) * S::NB + x * 16 + 4 * q);
+              if ((p | n) == 0) continue;
+#pragma unroll
+              for (int c = 0; c < S::VB / 2; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) O[mt][x * (S::VB / 2) + c][i] += at_noted(p >> (8 * i + c), n >> (8 * i + c));
+            }
           }
-#pragma unroll
-          for (int c = 0; c < S::VE; ++c) {
-            const at_f4 z = {0, 0, 0, 0};
-            const kv_u4 A = step_column<S::VE>(t.v, c, [](uint32_t w) { return at_fin<BF>(w); });
-            const kv_u4 Ip = step_column<S::VE>(t.v, c, [](uint32_t w) { return at_ind<BF>(w, false); });
-            const kv_u4 In = step_column<S::VE>(t.v, c, [](uint32_t w) { return at_ind<BF>(w, true); });
-            O[mt][c] = at_mfma16<BF>(A, P[mt], O[mt][c]);
-            const at_f4 np = at_mfma16<BF>(Ip, I, z), nn = at_mfma16<BF>(In, I, z);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) O[mt][c][i] += at_add_odd(np[i], nn[i]);
-          }
-        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       }
       if (more) step_load_v(t, a.c, pg, tok2, lane);
     }
 
     // the waves' results, joined in wave order; thread (row, c) has D / 16 columns
     const bool whole = t0 == 0 && t1 == nt;
-    float* slot = a.partial + (size_t)(2 * blockIdx.x + (first ? 0 : 1)) * step_slot(MT, D);
+    const uint32_t slot = (2 * blockIdx.x + (first ? 0 : 1)) * (uint32_t)step_slot(MT, D);
     const int row = tid >> 4, c0 = (tid & 15) * S::VE;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -367,11 +383,8 @@ void k_attn_step(AttnArgs a) {
           at_store<BF, S::VE>(a, e, head, r, c0, o, L);
         } else {
 #pragma unroll
-          for (int x = 0; x < S::VE; ++x) at_st(slot + (size_t)r * D + c0 + x, o[x]);
-          if (c0 == 0) {
-            at_st(slot + (size_t)MT * 16 * D + 2 * r, M);
-            at_st(slot + (size_t)MT * 16 * D + 2 * r + 1, L);
-          }
+          for (int x = 0; x < S::VE; x += 4) at_st4(rs, slot + r * D + c0 + x, at_f4{o[x], o[x + 1], o[x + 2], o[x + 3]});
+          if (c0 == 0) at_st2(rs, slot + MT * 16 * D + 2 * r, M, L);
         }
       }
     }
@@ -383,9 +396,8 @@ void k_attn_step(AttnArgs a) {
     const int64_t w0 = useg / per, w1 = (useg + nt - 1) / per;
     if (!at_last(a.counters + j * heads + head, (int)(w1 - w0) + 1, flag)) continue;
     const int before = w0 * per == useg ? 0 : 1;  // w0's slot: its first part or its last
-    at_join<BF, D>(a, e, head, 0, nrows, MT * 16, (int)(w1 - w0) + 1, [&](int k) {
-      return a.partial + (size_t)(2 * (w0 + k) + (k == 0 ? before : 0)) * step_slot(MT, D);
-    });
+    at_join<BF, D>(a, rs, e, head, 0, nrows, MT * 16, (int)(w1 - w0) + 1,
+                   [&](int k) { return (uint32_t)(2 * (w0 + k) + (k == 0 ? before : 0)) * (uint32_t)step_slot(MT, D); });
   }
 }
 

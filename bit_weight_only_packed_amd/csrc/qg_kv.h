@@ -90,6 +90,7 @@ struct AttnArgs {
   float scale_log2;    // scale * log2(e)
   int window, sinks;   // window 0: none
   float* partial;      // see the kernels
+  size_t partial_floats;
   int* counters;       // zero between launches
   int workers;         // few rows: workgroups that share the tiles
   int splits;          // many rows: workgroups that may share a block's tiles
@@ -98,15 +99,18 @@ struct AttnArgs {
 // rows of one kv head that the few-row kernel takes: (new rows) * (q heads per
 // kv head); wide heads hold fewer for lack of registers
 __host__ __device__ constexpr int step_max_rows(int D) { return D == 256 ? 32 : 64; }
-constexpr int STEP_WORKERS_PER_CU = 2;
+// waves per SIMD that its registers allow, which is workgroups (of four waves) per CU
+__host__ __device__ constexpr int step_per_cu(int MT, int D) { return MT * D <= 256 && D < 256 ? 2 : 1; }
 // fp32 words of one partial of MT row tiles: o, then (max, sum) of each row
 __host__ __device__ constexpr size_t step_slot(int MT, int D) { return (size_t)MT * 16 * (D + 2); }
 hipError_t launch_attn_step(const AttnArgs& a, int D, bool bf16, int MT, hipStream_t st);
 
-constexpr int ROWS_BM = 128;  // rows of a block of the many-row kernel
-__host__ __device__ constexpr size_t rows_slot(int D) { return (size_t)ROWS_BM * (D + 2); }
+// the many-row kernel: waves of a workgroup (wide heads need a SIMD's registers for
+// one wave), rows of a block, fp32 words of a partial
+__host__ __device__ constexpr int rows_waves(int D) { return D == 256 ? 4 : 8; }
+__host__ __device__ constexpr int rows_block(int D) { return 32 * rows_waves(D); }
+__host__ __device__ constexpr size_t rows_slot(int D) { return (size_t)rows_block(D) * (D + 2); }
 hipError_t launch_attn_rows(const AttnArgs& a, int D, bool bf16, unsigned blocks, hipStream_t st);
 hipError_t attn_step_allow_lds();
-hipError_t attn_rows_allow_lds();
 
 }  // namespace qg

@@ -21,6 +21,7 @@ struct qg_kv {
   bool debug_sync = false;
   KvPool pool{};
   float* partial = nullptr;   // attention partials
+  size_t partial_floats = 0;
   int* counters = nullptr;    // arrivals, zero between launches
   int32_t* lists = nullptr;   // head | from | to | place of the page operations
   int ncounters = 0;
@@ -154,18 +155,19 @@ qg_status qgkv_create(qg_kv_handle* out, const qg_kv_desc* d, void* stream) {
     free_kv(h);
     return fail(QG_ERR_DEVICE, "cannot query the compute-unit count");
   }
-  const size_t step = (size_t)2 * STEP_WORKERS_PER_CU * h->cus * step_slot(step_max_rows(d->head_dim) / 16, d->head_dim);
+  const size_t step = (size_t)2 * 2 * h->cus * step_slot(step_max_rows(d->head_dim) / 16, d->head_dim);
   const size_t rows = (size_t)kRowsSlots * rows_slot(d->head_dim);
   const size_t entries = (size_t)std::max(d->pages, d->max_seqs);
   h->ncounters = (std::max(d->max_seqs * d->kv_heads, kRowsSlots) + 3) / 4 * 4;
   hipStream_t st = (hipStream_t)stream;
-  if (hipMalloc(&h->partial, std::max(step, rows) * sizeof(float)) != hipSuccess ||
+  h->partial_floats = std::max(step, rows);
+  if (hipMalloc(&h->partial, h->partial_floats * sizeof(float)) != hipSuccess ||
       hipMalloc(&h->counters, (size_t)h->ncounters * sizeof(int)) != hipSuccess ||
       hipMalloc(&h->lists, (4 + 3 * entries) * sizeof(int32_t)) != hipSuccess) {
     (void)hipGetLastError();
     s = fail(QG_ERR_OOM, "workspace allocation failed");
   }
-  if (s == QG_OK && (attn_step_allow_lds() != hipSuccess || attn_rows_allow_lds() != hipSuccess))
+  if (s == QG_OK && attn_step_allow_lds() != hipSuccess)
     s = fail(QG_ERR_DEVICE, "cannot raise the LDS limit of the kernels");
   if (s == QG_OK && launch_fill_zero(h->counters, (int64_t)h->ncounters * sizeof(int), st) != hipSuccess)
     s = fail(QG_ERR_DEVICE, "counter initialisation failed");
@@ -265,6 +267,7 @@ qg_status qgkv_attend(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const
   a.window = window;
   a.sinks = sinks;
   a.partial = h->partial;
+  a.partial_floats = h->partial_floats;
   a.counters = h->counters;
   const int D = h->d.head_dim;
   const bool bf16 = h->d.dtype == QG_KV_BF16;
@@ -273,11 +276,11 @@ qg_status qgkv_attend(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const
   hipStream_t st = (hipStream_t)stream;
   if (rows <= step_max_rows(D)) {
     const int MT = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
-    a.workers = STEP_WORKERS_PER_CU * h->cus;
+    a.workers = step_per_cu(MT, D) * h->cus;
     return done(h, launch_attn_step(a, D, bf16, MT, st), st);
   }
   // a call of few blocks is split over the tokens until it covers the chip
-  const int64_t blocks = (rows + ROWS_BM - 1) / ROWS_BM * a.b.n * a.c.kv_heads;
+  const int64_t blocks = (rows + rows_block(D) - 1) / rows_block(D) * a.b.n * a.c.kv_heads;
   a.splits = (int)std::max<int64_t>(1, kRowsSlots / blocks);
   if (blocks * a.splits >= (int64_t)1 << 31) return fail(QG_ERR_UNSUPPORTED, "%lld blocks in one call", (long long)blocks);
   return done(h, launch_attn_rows(a, D, bf16, (unsigned)blocks, st), st);
