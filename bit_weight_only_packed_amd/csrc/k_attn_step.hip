@@ -6,8 +6,8 @@ namespace qg {
 namespace {
 
 template <int D, bool BF, int MT> hipError_t go(const AttnArgs& a, hipStream_t st) {
-  const size_t lds = StepShape<D>::lds + (size_t)(a.b.n + 1) * sizeof(int);
-  k_attn_step<D, BF, MT><<<(unsigned)a.workers, 64 * ST_NW, lds, st>>>(a);
+  const size_t lds = StepShape<D, MT>::lds + step_list_bytes(a.b.n);
+  k_attn_step<D, BF, MT><<<(unsigned)a.workers, 64 * step_waves(MT, D), lds, st>>>(a);
   return hipGetLastError();
 }
 
@@ -25,7 +25,7 @@ template <int D> hipError_t by_rows(const AttnArgs& a, bool bf16, int MT, hipStr
 template <int D, bool BF, int MT> hipError_t allow() {
   return hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attn_step<D, BF, MT>),
                              hipFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(StepShape<D>::lds + (KV_MAX_SEQS + 1) * sizeof(int)));
+                             (int)(StepShape<D, MT>::lds + step_list_bytes(KV_MAX_SEQS)));
 }
 
 }  // namespace
@@ -37,10 +37,19 @@ hipError_t launch_attn_step(const AttnArgs& a, int D, bool bf16, int MT, hipStre
 }
 
 hipError_t attn_step_allow_lds() {
-  hipError_t e = allow<256, false, 1>();
-  if (e == hipSuccess) e = allow<256, true, 1>();
-  if (e == hipSuccess) e = allow<256, false, 2>();
-  if (e == hipSuccess) e = allow<256, true, 2>();
+  hipError_t e = hipSuccess;
+  const auto both = [&](auto f, auto g) {
+    if (e == hipSuccess) e = f();
+    if (e == hipSuccess) e = g();
+  };
+  both(allow<64, false, 1>, allow<64, true, 1>);
+  both(allow<64, false, 2>, allow<64, true, 2>);
+  both(allow<64, false, 4>, allow<64, true, 4>);
+  both(allow<128, false, 1>, allow<128, true, 1>);
+  both(allow<128, false, 2>, allow<128, true, 2>);
+  both(allow<128, false, 4>, allow<128, true, 4>);
+  both(allow<256, false, 1>, allow<256, true, 1>);
+  both(allow<256, false, 2>, allow<256, true, 2>);
   return e;
 }
 

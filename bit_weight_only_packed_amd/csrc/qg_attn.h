@@ -41,6 +41,18 @@ template <bool BF> __device__ __forceinline__ uint32_t at_pack(float lo, float h
   else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, at_h2));
 }
 
+// maximum over the lanes that differ in bit 5 (32), or in bits 4 and 5 (16)
+__device__ __forceinline__ float at_max32(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+__device__ __forceinline__ float at_max16(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return at_max32(fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1])));
+}
+
 __device__ __forceinline__ float at_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 // the subtrahend of an exponent: 0 where nothing has been seen (2^(-inf - 0) = 0)
 __device__ __forceinline__ float at_safe(float m) { return m == -__builtin_inff() ? 0.0f : m; }
@@ -91,11 +103,11 @@ __device__ __forceinline__ void at_st4(__amdgpu_buffer_rsrc_t r, uint32_t at, at
 __device__ __forceinline__ void at_st2(__amdgpu_buffer_rsrc_t r, uint32_t at, float x, float y) {
   __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(kv_u2, at_f2{x, y}), r, (int)(at * 4), 0, AT_AGENT);
 }
-__device__ __forceinline__ at_f4 at_ld4(__amdgpu_buffer_rsrc_t r, uint32_t lane_at, uint32_t slot) {
-  return __builtin_bit_cast(at_f4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(lane_at * 4), (int)(slot * 4), AT_AGENT));
+__device__ __forceinline__ at_f4 at_ld4(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+  return __builtin_bit_cast(at_f4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(at * 4), 0, AT_AGENT));
 }
-__device__ __forceinline__ at_f2 at_ld2(__amdgpu_buffer_rsrc_t r, uint32_t lane_at, uint32_t slot) {
-  return __builtin_bit_cast(at_f2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)(lane_at * 4), (int)(slot * 4), AT_AGENT));
+__device__ __forceinline__ at_f2 at_ld2(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+  return __builtin_bit_cast(at_f2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)(at * 4), 0, AT_AGENT));
 }
 
 // The workgroup's arrival at a counter of n, after its partial: true in the one
@@ -124,7 +136,9 @@ __device__ __forceinline__ void at_store(const AttnArgs& a, const KvEntry& e, in
   uint32_t w[N / 2];
 #pragma unroll
   for (int x = 0; x < N / 2; ++x) w[x] = at_pack<BF>(o[2 * x] * inv, o[2 * x + 1] * inv);
-  if constexpr (N == 4) {
+  if constexpr (N == 2) {
+    *reinterpret_cast<uint32_t*>(to) = w[0];
+  } else if constexpr (N == 4) {
     *reinterpret_cast<kv_u2*>(to) = kv_u2{w[0], w[1]};
   } else {
 #pragma unroll
@@ -134,43 +148,72 @@ __device__ __forceinline__ void at_store(const AttnArgs& a, const KvEntry& e, in
 
 // Join n partials of rows r0 .. r0 + nrows - 1 of (entry, head) in the order 0, 1,
 // ...; slot(k) is where the k-th lies (in floats): [ld][D] fp32, then (m, l) of each
-// row.  The loads of eight partials are in flight at once.
-template <bool BF, int D, class F>
+// row.  A round trip to the partials costs about 2 us, so many loads go out at once:
+// NB per thread, and where the rows are few, several threads per four columns, each
+// taking a contiguous part of the partials (put together through `lds`, 6 floats per
+// thread, again in order).
+template <bool BF, int D, int THREADS, class F>
 __device__ __forceinline__ void at_join(const AttnArgs& a, __amdgpu_buffer_rsrc_t rs, const KvEntry& e, int head, int r0,
-                                        int nrows, int ld, int n, F slot) {
+                                        int nrows, int ld, int n, float* lds, F slot) {
   constexpr int NB = 8;
-  for (int it = threadIdx.x; it < nrows * (D / 4); it += blockDim.x) {
+  const int items = nrows * (D / 4);
+  int groups = 1;  // threads per item: a power of two, none with less than NB partials
+  while (2 * groups * items <= THREADS && groups * NB < n) groups *= 2;
+  const int g = groups > 1 ? (int)threadIdx.x / items : 0;
+  const int k0 = n * g / groups, k1 = n * (g + 1) / groups;
+  for (int it = groups > 1 ? (int)threadIdx.x - g * items : (int)threadIdx.x; it < items; it += THREADS) {
     const int r = it / (D / 4), c = (it % (D / 4)) * 4;
     const uint32_t at_o = (uint32_t)r * D + c, at_m = (uint32_t)ld * D + 2 * r;
     float M = -__builtin_inff(), L = 0.0f;
     at_f4 o = {0, 0, 0, 0};
-    for (int k0 = 0; k0 < n; k0 += NB) {
-      at_f2 pm[NB];
-      at_f4 po[NB];
+    if (g < groups)
+      for (int kb = k0; kb < k1; kb += NB) {
+        at_f2 pm[NB];
+        at_f4 po[NB];
 #pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        const uint32_t s = slot(min(k0 + k, n - 1));
-        pm[k] = at_ld2(rs, at_m, s);
-        po[k] = at_ld4(rs, at_o, s);
+        for (int k = 0; k < NB; ++k) {
+          const uint32_t s = slot(min(kb + k, k1 - 1));
+          pm[k] = at_ld2(rs, at_m + s);
+          po[k] = at_ld4(rs, at_o + s);
+        }
+        float Mn = M;
+#pragma unroll
+        for (int k = 0; k < NB; ++k) Mn = fmaxf(Mn, pm[k].x);
+        const float f0 = at_exp2(M - at_safe(Mn));
+        M = Mn;
+        L *= f0;
+        o *= f0;
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+          if (kb + k >= k1) break;
+          const float f = at_exp2(pm[k].x - at_safe(Mn));
+          L = __builtin_fmaf(f, pm[k].y, L);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) o[x] = __builtin_fmaf(f, po[k][x], o[x]);
+        }
       }
-      float Mn = M;
-#pragma unroll
-      for (int k = 0; k < NB; ++k) Mn = fmaxf(Mn, pm[k].x);
-      const float f0 = at_exp2(M - at_safe(Mn));
-      M = Mn;
-      L *= f0;
-      o *= f0;
-#pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        if (k0 + k >= n) break;
-        const float f = at_exp2(pm[k].x - at_safe(Mn));
-        L = __builtin_fmaf(f, pm[k].y, L);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) o[x] = __builtin_fmaf(f, po[k][x], o[x]);
-      }
+    if (groups == 1) {
+      const float res[4] = {o.x, o.y, o.z, o.w};
+      at_store<BF, 4>(a, e, head, r0 + r, c, res, L);
+    } else {
+      float* w = lds + threadIdx.x * 6;
+      w[0] = M, w[1] = L, w[2] = o.x, w[3] = o.y, w[4] = o.z, w[5] = o.w;
     }
-    const float res[4] = {o.x, o.y, o.z, o.w};
-    at_store<BF, 4>(a, e, head, r0 + r, c, res, L);
+  }
+  if (groups == 1) return;
+  __syncthreads();
+  if ((int)threadIdx.x < items) {
+    const int r = threadIdx.x / (D / 4), c = (threadIdx.x % (D / 4)) * 4;
+    float M = -__builtin_inff(), L = 0.0f, o[4] = {0, 0, 0, 0};
+    for (int i = 0; i < groups; ++i) M = fmaxf(M, lds[(i * items + threadIdx.x) * 6]);
+    for (int i = 0; i < groups; ++i) {
+      const float* w = lds + (i * items + threadIdx.x) * 6;
+      const float f = at_exp2(w[0] - at_safe(M));
+      L = __builtin_fmaf(f, w[1], L);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[x] = __builtin_fmaf(f, w[2 + x], o[x]);
+    }
+    at_store<BF, 4>(a, e, head, r0 + r, c, o, L);
   }
 }
 

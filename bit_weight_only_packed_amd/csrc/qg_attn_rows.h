@@ -84,12 +84,6 @@ __device__ __forceinline__ void rw_barrier() {
 }
 constexpr int RW_WAIT_VM = 0x0F70;  // s_waitcnt vmcnt(0), the other counters left alone
 
-// maximum (or sum) of a value over a row's two lanes
-__device__ __forceinline__ float rw_max2(float x) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false, false);
-  return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
-}
-
 // a wave's 32 rows
 template <int D> struct RowsState {
   using S = RowsShape<D>;
@@ -142,7 +136,7 @@ __device__ __forceinline__ void rw_tile(RowsState<D>& r, const AttnArgs& a, cons
   for (int g = 0; g < S::NT; ++g)
 #pragma unroll
     for (int i = g == 0 ? 1 : 0; i < 16; ++i) mx = fmaxf(mx, s[g][i]);
-  mx = rw_max2(mx);
+  mx = at_max32(mx);
   if (__any((mx - r.m) * a.scale_log2 > RW_SLACK || (mx > r.m && r.m == -__builtin_inff()))) {
     const float mn = fmaxf(r.m, mx);
     const float f = at_exp2((r.m - at_safe(mn)) * a.scale_log2);
@@ -252,7 +246,7 @@ void k_attn_rows(AttnArgs a) {
   if (tid == 0) odd_at = 0;
   // page of this wave's tokens of tile t, and the copy of its part
   const auto page_of = [&](int t) {
-    return kv_page(a.c, table[min(tr.at(min(t, t1 - 1)) * S::KT + wave * S::RW, p1) >> a.c.page_shift]);
+    return kv_page(a.c, kv_table(table, min(tr.at(min(t, t1 - 1)) * S::KT + wave * S::RW, p1) >> a.c.page_shift));
   };
   const auto copy = [&](int t, int page, char* keys, char* vals) {
     const int slot = (tr.at(t) * S::KT + wave * S::RW) & ((1 << a.c.page_shift) - 1);
@@ -341,7 +335,7 @@ void k_attn_rows(AttnArgs a) {
     if (h == 0) at_st2(rs, slot + S::BM * D + 2 * row, r.m * a.scale_log2, r.l);
   }
   if (!at_last(a.counters + blockIdx.x / a.splits, parts, &flag)) return;
-  at_join<BF, D>(a, rs, e, head, r0, nrows, S::BM, parts,
+  at_join<BF, D, 64 * S::NW>(a, rs, e, head, r0, nrows, S::BM, parts, reinterpret_cast<float*>(K0),
                  [&](int k) { return (blockIdx.x - z + k) * (uint32_t)rows_slot(D); });
 }
 

@@ -8,96 +8,125 @@
 // all served by one read of the tokens, and the kernel is built to keep reads in
 // flight.
 //
-// A wave takes tiles of 32 tokens.  Keys and values go from memory straight to
-// registers, 16 bytes a lane, with no pass through LDS:
+// A wave takes tiles of 32 tokens, each load instruction whole rows side by side
+// (keys loaded 16 bytes of 16 rows at a time, as the scores want them, cost 20 %
+// of the bandwidth):
 //   scores   S^T = K Q^T on 16x16x32: the A operand is a lane's 8 elements of one
-//            key, which is how keys lie in the page.  Row r of sub-tile t stands
-//            for token 8 (r / 4) + 4 t + r % 4, so that a lane's 2 x 4 scores are
-//            those of tokens 8 q .. 8 q + 7 (q = lane / 16) of one row (lane % 16).
+//            key.  Keys go straight to the wave's own LDS and come back as operands.
+//            A lane's 2 x 4 scores are those of tokens 4 q .. and 16 + 4 q .. (q =
+//            lane / 16) of one row (lane % 16).
 //   products O^T = V^T P^T: the B operand wants a lane's 8 tokens of one row --
 //            the lane's own weights, packed where they are.  The A operand wants
-//            8 tokens of one column: the lane loads 8 tokens x D / 16 columns and
-//            pairs them up with one byte permute per two elements.
-// The next tile's keys are loaded as soon as the scores have used this one's, the
-// next values as soon as the products have: one buffer each, always in use.
+//            8 tokens of one column: the lane loads 8 tokens x D / 16 columns into
+//            registers and pairs them up with one byte permute per two elements.
+// The next tile's keys are copied as soon as the scores have used this one's, the
+// next values loaded as soon as the products have: one buffer each, always in use.
 //
-// Split.  The (entry, kv head, tile) triples of the call form one list; each
-// workgroup takes an equal contiguous run of it, whatever the sequences'
-// lengths, its four waves every fourth tile of a run's part.  A (entry, kv head)
-// that one workgroup covers is finished there; one that several cover is joined
-// by the last of them to arrive, from partials in a fixed order.
+// Split.  The (entry, kv head, tile) triples of the call form one list, each (entry,
+// kv head) lengthened by ST_COST places for what it costs to begin and end it; each
+// workgroup takes an equal contiguous run, whatever the sequences' lengths, its
+// waves every NW-th tile of a run's part.  An (entry, kv head) that one workgroup
+// covers is finished there; one that several cover is joined by the last of them
+// to arrive, from partials in a fixed order.
 #pragma once
 #include "qg_attn.h"
 
 namespace qg {
 
 constexpr int ST_TK = 32;  // tokens of a tile
-constexpr int ST_NW = 4;   // waves of a workgroup
+constexpr int ST_COST = 4; // tiles that beginning and ending an (entry, kv head) is worth
 
-template <int D> struct StepShape {
+template <int D, int MT = 1> struct StepShape {
+  static constexpr int NW = step_waves(MT, D);   // waves of a workgroup
   static constexpr int VE = D / 16;              // columns of a lane
   static constexpr int VB = D == 64 ? 8 : 16;    // bytes of a lane's value load
   static constexpr int VL = VE * 2 / VB;         // value loads per token
   static constexpr int LD = D + 4;               // padded row of the cross-wave buffer (floats)
   static constexpr int NB = VL * 16;             // bytes of noted values per token (one per value load)
-  static constexpr size_t notes = (size_t)ST_NW * 2 * ST_TK * NB;
-  static constexpr size_t lds = (size_t)ST_NW * 16 * LD * 4 + ST_NW * 16 * 8 + notes + 16;
+  static constexpr size_t notes = (size_t)NW * 2 * ST_TK * NB;
+  static constexpr size_t lds = (size_t)NW * 16 * LD * 4 + NW * 16 * 8 + notes + 64;
 };
 
-template <int D, bool BF, int MT> struct StepTile {
+// the call's list in LDS: an entry's slot, length, first row and rows, and its places
+// in the list before it (n + 1 of these)
+constexpr size_t step_list_bytes(int n) { return (size_t)n * 16 + ((size_t)n + 1) * 4; }
+
+template <int D> struct StepTile {
   using S = StepShape<D>;
-  kv_u4 k[2][D / 32];
   uint32_t v[8][S::VE / 2];
 };
 
-// first bytes of the pages of a tile's two halves of 16 tokens
-struct StepPages {
-  const uint16_t* p[2];
+// what a token's chunk index is exclusive-or'ed with in LDS, so that the 16 tokens of a
+// score read fall on distinct banks
+template <int D> __device__ __forceinline__ int step_swz(int t) { return D == 64 ? (t >> 1) & 7 : t & 15; }
+
+// pages of a tile's two halves of 16 tokens, and the first bytes of a head's keys in them
+struct StepIds {
+  int id[2];
 };
-__device__ __forceinline__ StepPages step_pages(const KvDev& c, const int32_t* table, int tok, int last, int head, int D) {
+struct StepPages {
+  __amdgpu_buffer_rsrc_t k[2], v[2];
+};
+__device__ __forceinline__ StepIds step_ids(const KvDev& c, const int32_t* table, int tok, int last) {
+  StepIds r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) r.id[i] = kv_table(table, min((tok + 16 * i) >> c.page_shift, last >> c.page_shift));
+  return r;
+}
+// a tile that is none (live false) loads from an empty range: zeros, no memory access.
+// So every tile issues the same loads and the waits for them are exact.
+__device__ __forceinline__ StepPages step_pages(const KvDev& c, const StepIds& ids, int tok, int head, int D, bool live) {
   StepPages r;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int at = min((tok + 16 * i) >> c.page_shift, last >> c.page_shift);
-    r.p[i] = c.pool + kv_page(c, table[at]) * c.page_stride + (((int64_t)head << c.page_shift)) * D;
+    const int slot = (tok + 16 * i) & ((1 << c.page_shift) - 1);
+    const uint16_t* p = c.pool + kv_page(c, ids.id[i]) * c.page_stride + (((int64_t)head << c.page_shift) + slot) * D;
+    const int bytes = live ? 16 * D * 2 : 0;
+    r.k[i] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, bytes, 0x00020000);
+    r.v[i] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p) + c.v_off, 0, bytes, 0x00020000);
   }
   return r;
 }
 
-template <int D, bool BF, int MT>
-__device__ __forceinline__ void step_load_k(StepTile<D, BF, MT>& t, const KvDev& c, const StepPages& pg, int tok, int lane) {
-  const int mask = (1 << c.page_shift) - 1, r = lane & 15;
-  const int blk = r >> 2;  // the row's 8-token block
-  const uint16_t* base = (blk & 2) ? pg.p[1] : pg.p[0];
+// a tile's keys into the wave's part of LDS, whole rows side by side
+template <int D> __device__ __forceinline__ void step_copy_k(char* to, const StepPages& pg, int lane) {
+  constexpr int KC = D / 8;   // 16-byte chunks of a key
+  constexpr int IN = D / 32;  // copies of 1 KiB per half
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int slot = (tok + 8 * blk + 4 * u + (r & 3)) & mask;
-    const uint16_t* a = base + slot * D + (lane >> 4) * 8;
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) t.k[u][i] = *reinterpret_cast<const kv_u4*>(a + 32 * i);
-  }
+    for (int i = 0; i < IN; ++i) {
+      const int t = (i * 64 + lane) / KC;
+      const int at = t * D * 2 + (((i * 64 + lane) % KC) ^ step_swz<D>(t)) * 16;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(pg.k[h], (__attribute__((address_space(3))) void*)(to + (h * IN + i) * 1024), 16,
+                                               at, 0, 0, 0);
+    }
 }
 
-template <int D, bool BF, int MT>
-__device__ __forceinline__ void step_load_v(StepTile<D, BF, MT>& t, const KvDev& c, const StepPages& pg, int tok, int lane) {
+// a tile's values: register j of a lane is token 16 (j / 4) + 4 q + j % 4 (q = lane / 16)
+template <int D> __device__ __forceinline__ void step_load_v(StepTile<D>& t, const StepPages& pg, int lane) {
   using S = StepShape<D>;
-  const int mask = (1 << c.page_shift) - 1, q = lane >> 4, col = lane & 15;
-  const uint16_t* base = ((q & 2) ? pg.p[1] : pg.p[0]) + c.v_off + col * (S::VB / 2);
+  const int at = (lane >> 4) * 4 * D * 2 + (lane & 15) * S::VB;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint16_t* a = base + ((tok + 8 * q + j) & mask) * D;
+  for (int j = 0; j < 8; ++j)
 #pragma unroll
     for (int e = 0; e < S::VL; ++e) {
+      const int o = (j & 3) * D * 2 + 256 * e;
       if constexpr (S::VB == 16) {
-        const kv_u4 x = *reinterpret_cast<const kv_u4*>(a + 128 * e);
+        const kv_u4 x = __builtin_amdgcn_raw_buffer_load_b128(pg.v[j >> 2], at + o, 0, 0);
         t.v[j][4 * e] = x.x, t.v[j][4 * e + 1] = x.y, t.v[j][4 * e + 2] = x.z, t.v[j][4 * e + 3] = x.w;
       } else {
-        const kv_u2 x = *reinterpret_cast<const kv_u2*>(a);
+        const kv_u2 x = __builtin_amdgcn_raw_buffer_load_b64(pg.v[j >> 2], at + o, 0, 0);
         t.v[j][0] = x.x, t.v[j][1] = x.y;
       }
     }
-  }
 }
+
+// s_waitcnt vmcnt(n), the other counters left alone
+__host__ __device__ constexpr int step_wait_vm(int n) { return (n & 15) | 0x0F70 | (n >> 4) << 14; }
+
+// token of a tile that a lane quarter's register (weight, value) j stands for
+__device__ __forceinline__ int step_tok(int q, int j) { return 16 * (j >> 2) + 4 * q + (j & 3); }
 
 // the lane's 8 tokens of its column x: the A operand of product tile x
 template <int VE> __device__ __forceinline__ kv_u4 step_column(const uint32_t (&v)[8][VE / 2], int x) {
@@ -117,32 +146,38 @@ template <int D> __device__ __forceinline__ int step_col(int q, int i, int x) {
 }
 
 template <int D, bool BF, int MT>
-__global__ __launch_bounds__(64 * ST_NW) __attribute__((amdgpu_waves_per_eu(step_per_cu(MT, D))))
+__global__ __launch_bounds__(64 * step_waves(MT, D)) __attribute__((amdgpu_waves_per_eu(step_waves(MT, D) / 4)))
 void k_attn_step(AttnArgs a) {
-  using S = StepShape<D>;
+  using S = StepShape<D, MT>;
+  constexpr int NW = S::NW;
   extern __shared__ __align__(16) char smem[];
   float* buf = reinterpret_cast<float*>(smem);                                    // [wave][16][LD]
-  float* ml = buf + ST_NW * 16 * S::LD;                                           // [wave][16][2]
-  uint8_t* notes = reinterpret_cast<uint8_t*>(ml + ST_NW * 16 * 2);               // [wave][2][32][NB]
-  int* flag = reinterpret_cast<int*>(notes + S::notes);
-  int* pre = flag + 4;                                                            // [n + 1]
+  float* ml = buf + NW * 16 * S::LD;                                              // [wave][16][2]
+  uint8_t* notes = reinterpret_cast<uint8_t*>(ml + NW * 16 * 2);                  // [wave][2][32][NB]
+  int* flag = reinterpret_cast<int*>(notes + S::notes);                           // [16]
+  KvEntry* list = reinterpret_cast<KvEntry*>(flag + 16);                          // [n]
+  int* pre = reinterpret_cast<int*>(list + a.b.n);                                // [n + 1]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = lane >> 4, col = lane & 15;
   const int n = a.b.n, heads = a.c.kv_heads;
   notes += (size_t)wave * 2 * ST_TK * S::NB;
+  // this wave's tile of keys lies where the results are joined once the tiles are
+  // done; kb: this lane's part of its reads, but for the column step and the sub-tile
+  char* const keys = smem + wave * (ST_TK * D * 2);
+  const int kb = col * D * 2 + ((q ^ step_swz<D>(col)) << 4);
   const auto rs = at_slots(a.partial, a.partial_floats);
 
-  // prefix sums of the entries' tiles (at least one for an entry with rows, which
-  // has outputs to write even where it sees nothing)
+  // the list: prefix sums of the entries' places per kv head (an entry with rows has
+  // outputs to write even where it sees nothing: one tile at least)
   {
     int carry = 0;
-    int* sums = flag;  // the four waves' sums
-    for (int j0 = 0; j0 < n; j0 += 64 * ST_NW) {
+    for (int j0 = 0; j0 < n; j0 += 64 * NW) {
       const int j = j0 + tid;
       int t = 0;
       if (j < n) {
         const KvEntry e = kv_entry(a.c, a.b, j);
-        if (e.rows > 0) t = max(TileRange<ST_TK>(e.len - e.rows, e.len - 1, a.window, a.sinks).n, 1);
+        list[j] = e;
+        if (e.rows > 0) t = ST_COST + max(TileRange<ST_TK>(e.len - e.rows, e.len - 1, a.window, a.sinks).n, 1);
       }
       int x = t;
 #pragma unroll
@@ -150,26 +185,25 @@ void k_attn_step(AttnArgs a) {
         const int y = __shfl_up(x, o);
         if (lane >= o) x += y;
       }
-      if (lane == 63) sums[wave] = x;
+      if (lane == 63) flag[wave] = x;
       __syncthreads();
       int before = carry;
 #pragma unroll
-      for (int w = 0; w < ST_NW; ++w) {
-        before += w < wave ? sums[w] : 0;
-        carry += sums[w];
+      for (int w = 0; w < NW; ++w) {
+        before += w < wave ? flag[w] : 0;
+        carry += flag[w];
       }
       if (j < n) pre[j + 1] = before + x;
+      if (j0 == 0 && tid == 0) pre[0] = 0;
       __syncthreads();
     }
-    if (tid == 0) pre[0] = 0;
-    __syncthreads();
   }
-  const int64_t units = (int64_t)pre[n] * heads;
-  const int64_t per = max((units + a.workers - 1) / a.workers, (int64_t)ST_NW);
+  const int64_t places = (int64_t)pre[n] * heads;
+  const int64_t per = max((places + a.workers - 1) / a.workers, (int64_t)a.min_run);
   int64_t u = blockIdx.x * per;
-  const int64_t u1 = min(u + per, units);
+  const int64_t u1 = min(u + per, places);
 
-  int j = 0;  // the entry that holds unit u
+  int j = 0;  // the entry that holds place u
   if (u < u1)
     for (;; j += 64) {
       const uint64_t past = __ballot(j + lane < n && (int64_t)pre[min(j + lane, n - 1) + 1] * heads > u);
@@ -178,18 +212,21 @@ void k_attn_step(AttnArgs a) {
         break;
       }
     }
-  for (bool first = true; u < u1; first = false) {
+  while (u < u1) {
     // entry, kv head and tiles of the run's next part
     while ((int64_t)pre[j + 1] * heads <= u) ++j;
     j = __builtin_amdgcn_readfirstlane(j);
-    const int nt = __builtin_amdgcn_readfirstlane(pre[j + 1] - pre[j]);
-    const int64_t seg0 = (int64_t)pre[j] * heads;
-    const int head = __builtin_amdgcn_readfirstlane((int)((u - seg0) / nt));
-    const int64_t useg = seg0 + (int64_t)head * nt;  // first unit of (entry, head)
-    const int t0 = __builtin_amdgcn_readfirstlane((int)(u - useg));
-    const int t1 = __builtin_amdgcn_readfirstlane((int)min((int64_t)nt, u1 - useg));
-    u = useg + t1;
-    const KvEntry e = kv_entry(a.c, a.b, j);
+    const int len = __builtin_amdgcn_readfirstlane(pre[j + 1] - pre[j]), nt = len - ST_COST;
+    const int64_t seg = (int64_t)pre[j] * heads;
+    const int head = __builtin_amdgcn_readfirstlane((int)((u - seg) / len));
+    const int64_t tile0 = seg + (int64_t)head * len + ST_COST;  // place of (entry, head)'s first tile
+    const int t0 = __builtin_amdgcn_readfirstlane((int)max(u - tile0, (int64_t)0));
+    const int t1 = __builtin_amdgcn_readfirstlane((int)min((int64_t)nt, u1 - tile0));
+    u = tile0 + nt;
+    if (t0 >= t1) continue;  // the run ends before its first tile
+    KvEntry e = list[j];
+    e.slot = __builtin_amdgcn_readfirstlane(e.slot), e.len = __builtin_amdgcn_readfirstlane(e.len);
+    e.row0 = __builtin_amdgcn_readfirstlane(e.row0), e.rows = __builtin_amdgcn_readfirstlane(e.rows);
     const int p0 = e.len - e.rows, p1 = e.len - 1, nrows = e.rows * a.G;
     const TileRange<ST_TK> tr(p0, p1, a.window, a.sinks);
     const int32_t* table = a.c.tables + (int64_t)e.slot * a.c.max_pages;
@@ -219,32 +256,48 @@ void k_attn_step(AttnArgs a) {
       for (int x = 0; x < S::VE; ++x) O[mt][x] = at_f4{0, 0, 0, 0};
     }
 
-    StepTile<D, BF, MT> t;
+    StepTile<D> t;
+    __syncthreads();  // the last part's use of LDS is over
     int tl = t0 + wave;
     StepPages pg;
+    StepIds ids;  // of the tile after the one whose keys and values are on their way
     const bool any = tr.n > 0;  // else the one tile of an entry that sees nothing
+    const auto token = [&](int i) { return tr.at(min(i, t1 - 1)) * ST_TK; };
     if (any && tl < t1) {
-      const int tok = tr.at(tl) * ST_TK;
-      pg = step_pages(a.c, table, tok, p1, head, D);
-      step_load_k(t, a.c, pg, tok, lane);
-      step_load_v(t, a.c, pg, tok, lane);
+      ids = step_ids(a.c, table, token(tl), p1);
+      pg = step_pages(a.c, ids, token(tl), head, D, true);
+      step_copy_k<D>(keys, pg, lane);
+      __builtin_amdgcn_sched_barrier(0);  // the order that the wait below counts on
+      step_load_v(t, pg, lane);
+      ids = step_ids(a.c, table, token(tl + NW), p1);
     }
-    for (; any && tl < t1; tl += ST_NW) {
-      const int tok = tr.at(tl) * ST_TK;
-      const bool more = tl + ST_NW < t1;
-      const int tok2 = more ? tr.at(tl + ST_NW) * ST_TK : tok;
-      pg = step_pages(a.c, table, tok2, p1, head, D);
-
+    if (any && tl < t1) for (;; tl += NW) {
+      const int tok = token(tl), tok2 = token(tl + NW);
+      const bool more = tl + NW < t1;
+      pg = step_pages(a.c, ids, tok2, head, D, more);
+      // the keys have landed when only the value loads, issued after them, are left
+      __builtin_amdgcn_s_waitcnt(step_wait_vm(8 * S::VL));
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
       at_f4 s[MT][2];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int h = 0; h < 2; ++h) {
+        kv_u4 K[D / 32];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int c = 0; c < D / 32; ++c) K[c] = *reinterpret_cast<const kv_u4*>(keys + (kb ^ (c << 6)) + 16 * h * D * 2);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
           s[mt][h] = at_f4{0, 0, 0, 0};
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) s[mt][h] = at_mfma16<BF>(t.k[h][c], Q[mt][c], s[mt][h]);
+          for (int c = 0; c < D / 32; ++c) s[mt][h] = at_mfma16<BF>(K[c], Q[mt][c], s[mt][h]);
         }
-      if (more) step_load_k(t, a.c, pg, tok2, lane);
+      }
+      // the reads have returned before the next tile's copy may overwrite what they read
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+      __builtin_amdgcn_sched_barrier(0);
+      step_copy_k<D>(keys, pg, lane);
+      __builtin_amdgcn_sched_barrier(0);
+      ids = step_ids(a.c, table, token(tl + 2 * NW), p1);
 
       const bool masked = !at_all_see(p0, p1, tok, tok + ST_TK - 1, a.window, a.sinks);
       kv_u4 P[MT];
@@ -256,13 +309,12 @@ void k_attn_step(AttnArgs a) {
         if (masked) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (!at_sees(pos[mt], tok + 8 * q + i, a.window, a.sinks)) x[i] = -__builtin_inff();
+            if (!at_sees(pos[mt], tok + step_tok(q, i), a.window, a.sinks)) x[i] = -__builtin_inff();
         }
         float mx = x[0];
 #pragma unroll
         for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[i]);
-        mx = fmaxf(mx, __shfl_xor(mx, 16));
-        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        mx = at_max16(mx);
         if (__any(mx > m[mt])) {
           const float mn = fmaxf(m[mt], mx);
           const float f = at_exp2(m[mt] - at_safe(mn));
@@ -288,7 +340,7 @@ void k_attn_step(AttnArgs a) {
         bool nf = false;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int key = tok + 8 * q + i;
+          const int key = tok + step_tok(q, i);
           const bool seen = key <= p1 && (a.window == 0 || key > max(p0, 0) - a.window || key < a.sinks);
 #pragma unroll
           for (int c = 0; c < S::VE / 2; ++c) {
@@ -306,8 +358,8 @@ void k_attn_step(AttnArgs a) {
 #pragma unroll
               for (int c = 0; c < S::VB / 4; ++c)
                 t.v[i][x * S::VB / 4 + c] = at_take<BF>(t.v[i][x * S::VB / 4 + c], 2 * c, bp, bn);
-              notes[(8 * q + i) * S::NB + x * 16 + col] = (uint8_t)bp;
-              notes[(ST_TK + 8 * q + i) * S::NB + x * 16 + col] = (uint8_t)bn;
+              notes[step_tok(q, i) * S::NB + x * 16 + col] = (uint8_t)bp;
+              notes[(ST_TK + step_tok(q, i)) * S::NB + x * 16 + col] = (uint8_t)bn;
               __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -339,13 +391,17 @@ void k_attn_step(AttnArgs a) {
           }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       }
-      if (more) step_load_v(t, a.c, pg, tok2, lane);
+      step_load_v(t, pg, lane);
+      if (!more) break;
     }
 
-    // the waves' results, joined in wave order; thread (row, c) has D / 16 columns
+    // the waves' results, joined in wave order; 16 rows over all threads
     const bool whole = t0 == 0 && t1 == nt;
-    const uint32_t slot = (2 * blockIdx.x + (first ? 0 : 1)) * (uint32_t)step_slot(MT, D);
-    const int row = tid >> 4, c0 = (tid & 15) * S::VE;
+    // a workgroup has at most one part that begins past its first tile (its run's
+    // first) and one that begins there and does not end (its last)
+    const uint32_t slot = (2 * blockIdx.x + (t0 == 0 ? 1 : 0)) * (uint32_t)step_slot(MT, D);
+    constexpr int CW = 16 * D / (64 * NW);  // columns of a thread below
+    const int row = tid / (D / CW), c0 = (tid % (D / CW)) * CW;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       if (mt * 16 >= nrows) break;
@@ -367,37 +423,39 @@ void k_attn_step(AttnArgs a) {
       __syncthreads();
       const int r = mt * 16 + row;
       if (r < nrows) {
-        float M = -__builtin_inff(), L = 0.0f, o[S::VE];
+        float M = -__builtin_inff(), L = 0.0f, o[CW];
 #pragma unroll
-        for (int w = 0; w < ST_NW; ++w) M = fmaxf(M, ml[(w * 16 + row) * 2]);
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[(w * 16 + row) * 2]);
 #pragma unroll
-        for (int x = 0; x < S::VE; ++x) o[x] = 0.0f;
+        for (int x = 0; x < CW; ++x) o[x] = 0.0f;
 #pragma unroll
-        for (int w = 0; w < ST_NW; ++w) {
+        for (int w = 0; w < NW; ++w) {
           const float f = at_exp2(ml[(w * 16 + row) * 2] - at_safe(M));
           L += f * ml[(w * 16 + row) * 2 + 1];
 #pragma unroll
-          for (int x = 0; x < S::VE; ++x) o[x] = __builtin_fmaf(f, buf[(w * 16 + row) * S::LD + c0 + x], o[x]);
+          for (int x = 0; x < CW; ++x) o[x] = __builtin_fmaf(f, buf[(w * 16 + row) * S::LD + c0 + x], o[x]);
         }
         if (whole) {
-          at_store<BF, S::VE>(a, e, head, r, c0, o, L);
+          at_store<BF, CW>(a, e, head, r, c0, o, L);
         } else {
 #pragma unroll
-          for (int x = 0; x < S::VE; x += 4) at_st4(rs, slot + r * D + c0 + x, at_f4{o[x], o[x + 1], o[x + 2], o[x + 3]});
+          for (int x = 0; x < CW; x += 4) {
+            if constexpr (CW >= 4) at_st4(rs, slot + r * D + c0 + x, at_f4{o[x], o[x + 1], o[x + 2], o[x + 3]});
+            else at_st2(rs, slot + r * D + c0, o[0], o[1]);
+          }
           if (c0 == 0) at_st2(rs, slot + MT * 16 * D + 2 * r, M, L);
         }
       }
     }
     if (whole) continue;
 
-    // several workgroups share (entry, head): the last to arrive joins them, in
-    // list order.  The first of them has it as the last part of its run, the
-    // others as the first part of theirs.
-    const int64_t w0 = useg / per, w1 = (useg + nt - 1) / per;
+    // several workgroups share (entry, head): the last to arrive joins them, in list order
+    const int64_t w0 = tile0 / per, w1 = (tile0 + nt - 1) / per;
     if (!at_last(a.counters + j * heads + head, (int)(w1 - w0) + 1, flag)) continue;
-    const int before = w0 * per == useg ? 0 : 1;  // w0's slot: its first part or its last
-    at_join<BF, D>(a, rs, e, head, 0, nrows, MT * 16, (int)(w1 - w0) + 1,
-                   [&](int k) { return (uint32_t)(2 * (w0 + k) + (k == 0 ? before : 0)) * (uint32_t)step_slot(MT, D); });
+    at_join<BF, D, 64 * NW>(a, rs, e, head, 0, nrows, MT * 16, (int)(w1 - w0) + 1, buf, [&](int k) {
+      return (uint32_t)(2 * (w0 + k) + (k == 0 ? 1 : 0)) * (uint32_t)step_slot(MT, D);
+    });
+    __syncthreads();  // the join's use of the buffer is over
   }
 }
 

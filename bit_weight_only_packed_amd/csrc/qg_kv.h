@@ -56,6 +56,14 @@ __device__ __forceinline__ KvEntry kv_entry(const KvDev& c, const KvBatchDev& b,
   return e;
 }
 
+// An entry of a page table, at an address that is the same for the whole wave, by a
+// scalar load: it neither takes a place among the vector loads in flight, which are
+// waited for in order, nor a vector register.  (No kernel that reads tables this way
+// writes them.)
+__device__ __forceinline__ int kv_table(const int32_t* table, int i) {
+  return *(const __attribute__((address_space(4))) int32_t*)(uintptr_t)(table + i);
+}
+
 // page that a table names, or page 0 where it names none of the pool
 __device__ __forceinline__ int kv_page(const KvDev& c, int id) { return (unsigned)id < (unsigned)c.pages ? id : 0; }
 
@@ -92,15 +100,16 @@ struct AttnArgs {
   float* partial;      // see the kernels
   size_t partial_floats;
   int* counters;       // zero between launches
-  int workers;         // few rows: workgroups that share the tiles
+  int workers;         // few rows: workgroups that share the tiles,
+  int min_run;         // and places of their list that each takes at least
   int splits;          // many rows: workgroups that may share a block's tiles
 };
 
 // rows of one kv head that the few-row kernel takes: (new rows) * (q heads per
 // kv head); wide heads hold fewer for lack of registers
 __host__ __device__ constexpr int step_max_rows(int D) { return D == 256 ? 32 : 64; }
-// waves per SIMD that its registers allow, which is workgroups (of four waves) per CU
-__host__ __device__ constexpr int step_per_cu(int MT, int D) { return MT * D <= 256 && D < 256 ? 2 : 1; }
+// waves of a workgroup, one workgroup per CU: two waves per SIMD where the registers allow
+__host__ __device__ constexpr int step_waves(int MT, int D) { return MT * D <= 256 && D < 256 ? 8 : 4; }
 // fp32 words of one partial of MT row tiles: o, then (max, sum) of each row
 __host__ __device__ constexpr size_t step_slot(int MT, int D) { return (size_t)MT * 16 * (D + 2); }
 hipError_t launch_attn_step(const AttnArgs& a, int D, bool bf16, int MT, hipStream_t st);

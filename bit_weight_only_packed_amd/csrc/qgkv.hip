@@ -155,7 +155,7 @@ qg_status qgkv_create(qg_kv_handle* out, const qg_kv_desc* d, void* stream) {
     free_kv(h);
     return fail(QG_ERR_DEVICE, "cannot query the compute-unit count");
   }
-  const size_t step = (size_t)2 * 2 * h->cus * step_slot(step_max_rows(d->head_dim) / 16, d->head_dim);
+  const size_t step = (size_t)2 * h->cus * step_slot(step_max_rows(d->head_dim) / 16, d->head_dim);
   const size_t rows = (size_t)kRowsSlots * rows_slot(d->head_dim);
   const size_t entries = (size_t)std::max(d->pages, d->max_seqs);
   h->ncounters = (std::max(d->max_seqs * d->kv_heads, kRowsSlots) + 3) / 4 * 4;
@@ -276,7 +276,8 @@ qg_status qgkv_attend(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const
   hipStream_t st = (hipStream_t)stream;
   if (rows <= step_max_rows(D)) {
     const int MT = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
-    a.workers = step_per_cu(MT, D) * h->cus;
+    a.workers = h->cus;
+    a.min_run = getenv("QG_MINRUN") ? atoi(getenv("QG_MINRUN")) : 8;
     return done(h, launch_attn_step(a, D, bf16, MT, st), st);
   }
   // a call of few blocks is split over the tokens until it covers the chip
