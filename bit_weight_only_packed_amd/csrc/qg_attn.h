@@ -41,6 +41,9 @@ template <bool BF> __device__ __forceinline__ uint32_t at_pack(float lo, float h
   else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, at_h2));
 }
 
+// s_waitcnt vmcnt(n), the other counters left alone
+__host__ __device__ constexpr int at_wait_vm(int n) { return (n & 15) | 0x0F70 | (n >> 4) << 14; }
+
 // maximum over the lanes that differ in bit 5 (32), or in bits 4 and 5 (16)
 __device__ __forceinline__ float at_max32(float x) {
   const uint32_t u = __builtin_bit_cast(uint32_t, x);
@@ -69,9 +72,8 @@ template <int H> __device__ __forceinline__ uint32_t at_halves(uint32_t a, uint3
 // row that does see the token gets the infinity added, or both.
 template <bool BF> __device__ __forceinline__ uint32_t at_exp_mask() { return BF ? 0x7F80u : 0x7C00u; }
 template <bool BF> __device__ __forceinline__ bool at_odd1(uint32_t h) { return (h & at_exp_mask<BF>()) == at_exp_mask<BF>(); }
-template <bool BF> __device__ __forceinline__ bool at_odd(uint32_t w) {
-  return (int)at_odd1<BF>(w) | (int)at_odd1<BF>(w >> 16);
-}
+// the larger magnitude of two halves and m: not finite from at_exp_mask on
+__device__ __forceinline__ uint32_t at_top(uint32_t m, uint32_t w) { return max(max(m, w & 0x7FFFu), (w >> 16) & 0x7FFFu); }
 // take what is not finite out of two values; bits `at` and `at` + 1 of pos and neg note it
 template <bool BF> __device__ __forceinline__ uint32_t at_take(uint32_t w, int at, uint32_t& pos, uint32_t& neg) {
   asm volatile("" : "+v"(w));  // its classification is not carried over from the check: registers are dearer here
@@ -146,74 +148,91 @@ __device__ __forceinline__ void at_store(const AttnArgs& a, const KvEntry& e, in
   }
 }
 
-// Join n partials of rows r0 .. r0 + nrows - 1 of (entry, head) in the order 0, 1,
-// ...; slot(k) is where the k-th lies (in floats): [ld][D] fp32, then (m, l) of each
-// row.  A round trip to the partials costs about 2 us, so many loads go out at once:
-// NB per thread, and where the rows are few, several threads per four columns, each
-// taking a contiguous part of the partials (put together through `lds`, 6 floats per
-// thread, again in order).
+// Join n partials of rows r0 .. r0 + nrows - 1 of (entry, head); slot(k) is where the
+// k-th lies (in floats): [ld][D] fp32, then (m, l) of each row.  Every sum runs in an
+// order that n fixes.
+//
+// A round trip to the partials costs about 2 us, so there are two: one for all (m, l),
+// whose factors 2^(m_k - M) / sum go to LDS (a wave per row), and one for the outputs,
+// sixteen partials at a time; where the rows are few, several threads share an item
+// of four columns, each with a contiguous part of the partials.
+// fac, tot, part: AT_JOIN_CAP floats of LDS each; n <= AT_JOIN_CAP.
+constexpr int AT_JOIN_CAP = 2720;  // (row, partial) pairs at a time; 4 floats of 512 threads fit as well
 template <bool BF, int D, int THREADS, class F>
 __device__ __forceinline__ void at_join(const AttnArgs& a, __amdgpu_buffer_rsrc_t rs, const KvEntry& e, int head, int r0,
-                                        int nrows, int ld, int n, float* lds, F slot) {
-  constexpr int NB = 8;
-  const int items = nrows * (D / 4);
-  int groups = 1;  // threads per item: a power of two, none with less than NB partials
-  while (2 * groups * items <= THREADS && groups * NB < n) groups *= 2;
-  const int g = groups > 1 ? (int)threadIdx.x / items : 0;
-  const int k0 = n * g / groups, k1 = n * (g + 1) / groups;
-  for (int it = groups > 1 ? (int)threadIdx.x - g * items : (int)threadIdx.x; it < items; it += THREADS) {
-    const int r = it / (D / 4), c = (it % (D / 4)) * 4;
-    const uint32_t at_o = (uint32_t)r * D + c, at_m = (uint32_t)ld * D + 2 * r;
-    float M = -__builtin_inff(), L = 0.0f;
-    at_f4 o = {0, 0, 0, 0};
-    if (g < groups)
-      for (int kb = k0; kb < k1; kb += NB) {
-        at_f2 pm[NB];
-        at_f4 po[NB];
+                                        int nrows, int ld, int n, float* fac, float* tot, float* part, F slot) {
+  constexpr int NB = 16, NW = THREADS / 64;
+  static_assert(4 * THREADS <= AT_JOIN_CAP, "part");
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int chunk = min(nrows, AT_JOIN_CAP / n);
+  // fac [row][partial] m, then its factor; tot [row][partial] l, then [row][0] the sum;
+  // part [thread][4] outputs of threads that share an item
+  for (int rb = 0; rb < nrows; rb += chunk) {
+    const int rows = min(chunk, nrows - rb);
+    __syncthreads();
+    for (int x = tid; x < rows * n; x += THREADS) {
+      const int r = x / n, k = x - r * n;
+      const at_f2 ml = at_ld2(rs, slot(k) + (uint32_t)ld * D + 2 * (rb + r));
+      fac[x] = ml.x;
+      tot[x] = ml.y;
+    }
+    __syncthreads();
+    for (int r = wave; r < rows; r += NW) {
+      float M = -__builtin_inff(), L = 0.0f;
+      for (int k = lane; k < n; k += 64) M = fmaxf(M, fac[r * n + k]);
 #pragma unroll
-        for (int k = 0; k < NB; ++k) {
-          const uint32_t s = slot(min(kb + k, k1 - 1));
-          pm[k] = at_ld2(rs, at_m + s);
-          po[k] = at_ld4(rs, at_o + s);
-        }
-        float Mn = M;
-#pragma unroll
-        for (int k = 0; k < NB; ++k) Mn = fmaxf(Mn, pm[k].x);
-        const float f0 = at_exp2(M - at_safe(Mn));
-        M = Mn;
-        L *= f0;
-        o *= f0;
-#pragma unroll
-        for (int k = 0; k < NB; ++k) {
-          if (kb + k >= k1) break;
-          const float f = at_exp2(pm[k].x - at_safe(Mn));
-          L = __builtin_fmaf(f, pm[k].y, L);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) o[x] = __builtin_fmaf(f, po[k][x], o[x]);
-        }
+      for (int o = 32; o; o >>= 1) M = fmaxf(M, __shfl_xor(M, o));
+      M = at_safe(M);
+      for (int k = lane; k < n; k += 64) {
+        const float f = at_exp2(fac[r * n + k] - M);
+        fac[r * n + k] = f;
+        L = __builtin_fmaf(f, tot[r * n + k], L);
       }
-    if (groups == 1) {
-      const float res[4] = {o.x, o.y, o.z, o.w};
-      at_store<BF, 4>(a, e, head, r0 + r, c, res, L);
-    } else {
-      float* w = lds + threadIdx.x * 6;
-      w[0] = M, w[1] = L, w[2] = o.x, w[3] = o.y, w[4] = o.z, w[5] = o.w;
-    }
-  }
-  if (groups == 1) return;
-  __syncthreads();
-  if ((int)threadIdx.x < items) {
-    const int r = threadIdx.x / (D / 4), c = (threadIdx.x % (D / 4)) * 4;
-    float M = -__builtin_inff(), L = 0.0f, o[4] = {0, 0, 0, 0};
-    for (int i = 0; i < groups; ++i) M = fmaxf(M, lds[(i * items + threadIdx.x) * 6]);
-    for (int i = 0; i < groups; ++i) {
-      const float* w = lds + (i * items + threadIdx.x) * 6;
-      const float f = at_exp2(w[0] - at_safe(M));
-      L = __builtin_fmaf(f, w[1], L);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) o[x] = __builtin_fmaf(f, w[2 + x], o[x]);
+      for (int o = 32; o; o >>= 1) L += __shfl_xor(L, o);
+      if (lane == 0) tot[r * n] = L;
     }
-    at_store<BF, 4>(a, e, head, r0 + r, c, o, L);
+    __syncthreads();
+    const int items = rows * (D / 4);
+    int groups = 1;  // threads per item: a power of two
+    while (2 * groups * items <= THREADS && groups * NB < n) groups *= 2;
+    const int g = groups > 1 ? tid / items : 0;
+    const int k0 = n * g / groups, k1 = n * (g + 1) / groups;
+    for (int it = tid - g * items; it < items; it += THREADS) {
+      const int r = it / (D / 4), c = (it % (D / 4)) * 4;
+      const uint32_t at = (uint32_t)(rb + r) * D + c;
+      at_f4 o = {0, 0, 0, 0};
+      if (g < groups)
+        for (int kb = k0; kb < k1; kb += NB) {
+          at_f4 po[NB];
+#pragma unroll
+          for (int k = 0; k < NB; ++k)
+            if (kb + k < k1) po[k] = at_ld4(rs, at + slot(kb + k));
+#pragma unroll
+          for (int k = 0; k < NB; ++k)
+            if (kb + k < k1) {
+              const float f = fac[r * n + kb + k];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) o[x] = __builtin_fmaf(f, po[k][x], o[x]);
+            }
+        }
+      if (groups == 1) {
+        const float res[4] = {o.x, o.y, o.z, o.w};
+        at_store<BF, 4>(a, e, head, r0 + rb + r, c, res, tot[r * n]);
+      } else if (g < groups) {
+        *reinterpret_cast<at_f4*>(part + tid * 4) = o;
+      }
+    }
+    if (groups == 1) continue;
+    __syncthreads();
+    if (tid < items) {
+      const int r = tid / (D / 4), c = (tid % (D / 4)) * 4;
+      float o[4] = {0, 0, 0, 0};
+      for (int i = 0; i < groups; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[x] += part[(i * items + tid) * 4 + x];
+      at_store<BF, 4>(a, e, head, r0 + rb + r, c, o, tot[r * n]);
+    }
   }
 }
 
@@ -236,6 +255,17 @@ template <int TK> struct TileRange {
 __device__ __forceinline__ bool at_sees(int pos, int t, int window, int sinks) {
   return t <= pos && (window == 0 || t > pos - window || t < sinks);
 }
+// The same for many tokens base + c of one row: t is seen iff pos - t, unsigned, is
+// below `span`, or c below `first`.  (Two compares a token; and the users put up
+// barriers between tokens, for a mask per token and compare would take every
+// scalar register, those of the main loop among them.)
+struct SeenFrom {
+  int d, first;
+  uint32_t span;
+  __device__ __forceinline__ SeenFrom(int pos, int base, int window, int sinks)
+      : d(pos - base), first(min(sinks, pos + 1) - base), span(pos < 0 ? 0u : window ? (uint32_t)window : 0x80000000u) {}
+  __device__ __forceinline__ bool operator()(int c) const { return (int)((uint32_t)(d - c) < span) | (int)(c < first); }
+};
 // do all rows at positions p0 .. p1 see all tokens of [t0, t1]?
 __device__ __forceinline__ bool at_all_see(int p0, int p1, int t0, int t1, int window, int sinks) {
   return t1 <= p0 && (window == 0 || t0 > p1 - window || t1 < sinks);

@@ -8,7 +8,7 @@
 // and a block spans few positions (little is computed past the diagonal).  Tokens
 // come in tiles of KT = 8192 / D, keys and values 16 KiB each, straight from memory
 // into one of two LDS buffers (no registers); the next tile is on its way while
-// this one is computed, and one barrier per tile orders both.
+// this one is computed.
 //
 //   scores   S^T = K Q^T on 32x32x16 (A: keys from LDS, B: q from registers).  A
 //            lane holds 16 tokens of one row per 32, as token 8 (i / 4) + 4 h + i % 4
@@ -30,6 +30,10 @@ namespace qg {
 
 constexpr int RW_MIN_TILES = 4;     // tiles of a split at least
 constexpr float RW_SLACK = 8.0f;    // exponent that a weight may reach
+// operands read from LDS ahead of the product that takes them (an LDS round trip is
+// some 100 cycles, a product 32), and the scheduler's names of the two
+constexpr int RW_DEEP = 6;
+constexpr int RW_MFMA = 0x8, RW_DS_READ = 0x100;
 
 template <int D> struct RowsShape {
   static constexpr int NW = rows_waves(D);  // waves of a workgroup
@@ -41,6 +45,8 @@ template <int D> struct RowsShape {
   static constexpr int LD = 16 / NW;        // 1 KiB copies per wave of a tile's keys (or values)
   static constexpr int RW = KT / NW;        // tokens that a wave copies (they lie in one page)
   static constexpr int bytes = 16384;       // a tile's keys (or values)
+  static constexpr int NB = 4;              // tiles of keys, and of values, in LDS
+  static constexpr int AHEAD = NB - 1;      // a tile's copies go out this many tiles before its use
 };
 
 // what a token's chunk index is exclusive-or'ed with.  Keys: 16 lanes read one chunk
@@ -59,22 +65,10 @@ __device__ __forceinline__ kv_u2 rw_read_tr(const char* p) {
   return __builtin_bit_cast(kv_u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((rw_lds4)(p)));
 }
 
-// this wave's part of a tile's copies: `base` the page's first key of the head
-template <int D>
-__device__ __forceinline__ void rw_copy(const uint16_t* base, int64_t v_off, int slot, char* keys, char* vals, int wave, int lane) {
-  using S = RowsShape<D>;
-#pragma unroll
-  for (int i = 0; i < S::LD; ++i) {
-    const int x = i * 64 + lane, t = x / S::KC, c = x % S::KC;  // token of the wave's, chunk's place
-    const int tt = wave * S::RW + t;                            // token of the tile
-    const uint16_t* k = base + (slot + t) * D + (c ^ rw_key_swz<D>(tt)) * 8;
-    const uint16_t* v = base + v_off + (slot + t) * D + (c ^ rw_val_swz<D>(tt)) * 8;
-    const int to = (wave * S::LD + i) * 1024;
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)k,
-                                     (__attribute__((address_space(3))) void*)(keys + to), 16, 0, 0);
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)v,
-                                     (__attribute__((address_space(3))) void*)(vals + to), 16, 0, 0);
-  }
+// 64 lanes copy 16 bytes each, from `from` (the same for the wave) + ofs, side by side to `to`
+__device__ __forceinline__ void rw_copy(const char* from, int ofs, char* to) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from + (uint32_t)ofs),
+                                   (__attribute__((address_space(3))) void*)to, 16, 0, 0);
 }
 
 __device__ __forceinline__ void rw_barrier() {
@@ -82,7 +76,6 @@ __device__ __forceinline__ void rw_barrier() {
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
-constexpr int RW_WAIT_VM = 0x0F70;  // s_waitcnt vmcnt(0), the other counters left alone
 
 // a wave's 32 rows
 template <int D> struct RowsState {
@@ -93,43 +86,60 @@ template <int D> struct RowsState {
   int pos;      // this lane's row's position
 };
 
-// one tile of tokens tok .. tok + KT - 1 for a wave whose rows stand at pw0 .. pw1.
-// noted: the tile's values that were not finite and have been taken out, or NULL.
-template <int D, bool BF>
-__device__ __forceinline__ void rw_tile(RowsState<D>& r, const AttnArgs& a, const char* keys, const char* vals, int tok, int pw0,
-                                        int pw1, const uint8_t* noted, int lane) {
-  using S = RowsShape<D>;
+// byte of this lane's part of the key reads, and of the value reads, but for what is
+// constant per read: an exclusive-or for the chunk, an immediate for the token
+template <int D> __device__ __forceinline__ int rw_key_byte(int lane) {
   const int h = lane >> 5, col = lane & 31;
-  constexpr int RB = D * 2;  // bytes of a token
-  // Byte of this lane's part of the reads below, but for what is constant per
-  // read: an exclusive-or for the chunk, an immediate for the token.  Computed
-  // anew for each tile (one instruction per read), for the registers are needed.
-  int kb = col * RB + ((h ^ rw_key_swz<D>(col)) << 4);
+  return col * D * 2 + ((h ^ rw_key_swz<D>(col)) << 4);
+}
+template <int D> __device__ __forceinline__ int rw_val_byte(int lane) {
   // the transposing read's lane: token i / 4 of four, columns 4 (i % 4) .. (i = lane % 16)
-  const int i16 = lane & 15, t4 = 4 * h + (i16 >> 2);
-  int vb = t4 * RB + (((((lane >> 4) & 1) * 2 + ((i16 >> 1) & 1)) ^ rw_val_swz<D>(t4)) << 4) + (i16 & 1) * 8;
-  asm volatile("" : "+v"(kb), "+v"(vb));
-  const auto val = [&](int x, int k, int b) {  // 32-column group x, 16-token step k, tokens 8 b + t4
-    return rw_read_tr(vals + (vb ^ (x << 6) ^ (b << 5)) + (16 * k + 8 * b) * RB);
+  const int i = lane & 15, t = 4 * (lane >> 5) + (i >> 2);
+  return t * D * 2 + (((((lane >> 4) & 1) * 2 + ((i >> 1) & 1)) ^ rw_val_swz<D>(t)) << 4) + (i & 1) * 8;
+}
+
+// scores of the wave's rows with a tile of keys
+template <int D, bool BF>
+__device__ __forceinline__ void rw_scores(at_f16 (&s)[RowsShape<D>::NT], const RowsState<D>& r, const char* keys, int lane) {
+  using S = RowsShape<D>;
+  int kb = rw_key_byte<D>(lane);
+  asm volatile("" : "+v"(kb));  // one instruction per read, not a register each: they are needed
+  constexpr int N = S::NT * (D / 16);
+  const auto key = [&](int i) {  // column step i / NT, 32-token group i % NT
+    return *reinterpret_cast<const kv_u4*>(keys + (kb ^ ((i / S::NT) << 5)) + (i % S::NT) * 32 * D * 2);
   };
-  at_f16 s[S::NT];
+  kv_u4 K[N];
 #pragma unroll
-  for (int g = 0; g < S::NT; ++g) {
+  for (int i = 0; i < RW_DEEP; ++i) K[i] = key(i);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s[g][i] = 0.0f;
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) {
-      const kv_u4 K = *reinterpret_cast<const kv_u4*>(keys + (kb ^ (c << 5)) + g * 32 * RB);
-      s[g] = at_mfma32<BF>(K, r.Q[c], s[g]);
-    }
+  for (int i = 0; i < N; ++i) {
+    if (i + RW_DEEP < N) K[i + RW_DEEP] = key(i + RW_DEEP);
+    at_f16& x = s[i % S::NT];
+    x = at_mfma32<BF>(K[i], r.Q[i / S::NT], i < S::NT ? at_f16{} : x);
   }
-  const bool masked = !at_all_see(pw0, pw1, tok, tok + S::KT - 1, a.window, a.sinks);
+  __builtin_amdgcn_sched_group_barrier(RW_DS_READ, RW_DEEP, 0);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(RW_MFMA, 1, 0);
+    if (i + RW_DEEP < N) __builtin_amdgcn_sched_group_barrier(RW_DS_READ, 1, 0);
+  }
+}
+
+// scores of tile tok .. tok + KT - 1 to weights; masked: some row does not see all of it
+template <int D, bool BF>
+__device__ __forceinline__ void rw_softmax(kv_u4 (&P)[2 * RowsShape<D>::NT], at_f16 (&s)[RowsShape<D>::NT], RowsState<D>& r,
+                                           const AttnArgs& a, int tok, bool masked, int lane) {
+  using S = RowsShape<D>;
+  const int h = lane >> 5;
   if (masked) {
+    const SeenFrom seen(r.pos, tok + 4 * h, a.window, a.sinks);
 #pragma unroll
     for (int g = 0; g < S::NT; ++g)
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (!at_sees(r.pos, tok + g * 32 + 8 * (i >> 2) + 4 * h + (i & 3), a.window, a.sinks)) s[g][i] = -__builtin_inff();
+      for (int i = 0; i < 16; ++i) {
+        s[g][i] = seen(g * 32 + 8 * (i >> 2) + (i & 3)) ? s[g][i] : -__builtin_inff();
+        if (i & 1) __builtin_amdgcn_sched_barrier(0);
+      }
   }
   float mx = s[0][0];
 #pragma unroll
@@ -137,7 +147,8 @@ __device__ __forceinline__ void rw_tile(RowsState<D>& r, const AttnArgs& a, cons
 #pragma unroll
     for (int i = g == 0 ? 1 : 0; i < 16; ++i) mx = fmaxf(mx, s[g][i]);
   mx = at_max32(mx);
-  if (__any((mx - r.m) * a.scale_log2 > RW_SLACK || (mx > r.m && r.m == -__builtin_inff()))) {
+  // (r.m = -inf, nothing seen yet: the difference is inf, or NaN where mx is -inf too)
+  if (__builtin_expect(__any((mx - r.m) * a.scale_log2 > RW_SLACK), 0)) {
     const float mn = fmaxf(r.m, mx);
     const float f = at_exp2((r.m - at_safe(mn)) * a.scale_log2);
     r.m = mn;
@@ -148,7 +159,6 @@ __device__ __forceinline__ void rw_tile(RowsState<D>& r, const AttnArgs& a, cons
       for (int i = 0; i < 16; ++i) r.O[x][i] *= f;
   }
   const float ms = at_safe(r.m) * a.scale_log2;
-  kv_u4 P[2 * S::NT];
   float sum[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int g = 0; g < S::NT; ++g)
@@ -161,16 +171,44 @@ __device__ __forceinline__ void rw_tile(RowsState<D>& r, const AttnArgs& a, cons
       P[2 * g + i / 8][(i & 7) / 2] = at_pack<BF>(x, y);
     }
   r.l += sum[0] + sum[1];
+  // here, and not among the products that follow the barrier
+#pragma unroll
+  for (int k = 0; k < 2 * S::NT; ++k) asm volatile("" : "+v"(P[k]));
+}
 
+// products of the weights of tile tok with its values
+// noted: the tile's values that were not finite and have been taken out, or NULL
+template <int D, bool BF>
+__device__ __forceinline__ void rw_products(RowsState<D>& r, const kv_u4 (&P)[2 * RowsShape<D>::NT], const AttnArgs& a,
+                                            const char* vals, int tok, const uint8_t* noted, int lane) {
+  using S = RowsShape<D>;
+  int vb = rw_val_byte<D>(lane);
+  asm volatile("" : "+v"(vb));
+  const auto val = [&](int x, int k, int b) {  // 32-column group x, 16-token step k, tokens 8 b ..
+    return rw_read_tr(vals + (vb ^ (x << 6) ^ (b << 5)) + (16 * k + 8 * b) * D * 2);
+  };
+  constexpr int N = S::ND * 2 * S::NT;
+  const auto op = [&](int i) {  // 16-token step i / ND, column group i % ND
+    const kv_u2 v0 = val(i % S::ND, i / S::ND, 0), v1 = val(i % S::ND, i / S::ND, 1);
+    return kv_u4{v0.x, v0.y, v1.x, v1.y};
+  };
+  kv_u4 V[N];
 #pragma unroll
-  for (int x = 0; x < S::ND; ++x)
+  for (int i = 0; i < RW_DEEP; ++i) V[i] = op(i);
 #pragma unroll
-    for (int k = 0; k < 2 * S::NT; ++k) {
-      const kv_u2 v0 = val(x, k, 0), v1 = val(x, k, 1);
-      r.O[x] = at_mfma32<BF>(kv_u4{v0.x, v0.y, v1.x, v1.y}, P[k], r.O[x]);
-    }
-  if (noted) {
-    // rare: [token][16-byte chunk] bytes of noted +inf or NaN, then of -inf or NaN
+  for (int i = 0; i < N; ++i) {
+    if (i + RW_DEEP < N) V[i + RW_DEEP] = op(i + RW_DEEP);
+    r.O[i % S::ND] = at_mfma32<BF>(V[i], P[i / S::ND], r.O[i % S::ND]);
+  }
+  __builtin_amdgcn_sched_group_barrier(RW_DS_READ, 2 * RW_DEEP, 0);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(RW_MFMA, 1, 0);
+    if (i + RW_DEEP < N) __builtin_amdgcn_sched_group_barrier(RW_DS_READ, 2, 0);
+  }
+  if (__builtin_expect(noted != nullptr, 0)) {
+    // [token][16-byte chunk] bytes of noted +inf or NaN, then of -inf or NaN
+    const int h = lane >> 5;
 #pragma unroll 1
     for (int t = 0; t < S::KT; ++t) {
       const uint32_t* w = reinterpret_cast<const uint32_t*>(noted + t * S::KC);
@@ -193,9 +231,8 @@ template <int D, bool BF>
 __global__ __launch_bounds__(64 * RowsShape<D>::NW) __attribute__((amdgpu_waves_per_eu(RowsShape<D>::NW / 4)))
 void k_attn_rows(AttnArgs a) {
   using S = RowsShape<D>;
-  // arrays of their own, so that a read of one buffer is known not to wait for the
-  // copies that are under way into the other
-  __shared__ __align__(1024) char K0[S::bytes], V0[S::bytes], K1[S::bytes], V1[S::bytes];
+  __shared__ __align__(1024) char keys[S::NB * S::bytes];
+  __shared__ __align__(1024) char vals[S::NB * S::bytes];
   __shared__ __align__(16) uint8_t notes[S::bytes / 8];
   __shared__ int odd_at, flag;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -244,70 +281,130 @@ void k_attn_rows(AttnArgs a) {
   r.m = -__builtin_inff(), r.l = 0.0f;
 
   if (tid == 0) odd_at = 0;
-  // page of this wave's tokens of tile t, and the copy of its part
-  const auto page_of = [&](int t) {
-    return kv_page(a.c, kv_table(table, min(tr.at(min(t, t1 - 1)) * S::KT + wave * S::RW, p1) >> a.c.page_shift));
+  const int nt = t1 - t0;
+  const auto token = [&](int t) { return tr.at(t0 + t) * S::KT; };
+  // Tiles [clear0, clear1) are seen whole by every row of the block, [wclear0, wclear1)
+  // by every row of the wave (of a window's tiles those past the sinks).
+  const auto clear = [&](int a0, int a1, int& from, int& to) {
+    // tok + KT - 1 <= a0, and tok > a1 - window
+    to = min((a0 + 1) / S::KT - (t0 + tr.skip), nt);
+    from = a.window ? max((max(a1 - a.window, -1) + S::KT) / S::KT, tr.ns + tr.skip) - (t0 + tr.skip) : 0;
+    from = max(from, 0);
+    if (a0 < 0) to = 0;
   };
-  const auto copy = [&](int t, int page, char* keys, char* vals) {
-    const int slot = (tr.at(t) * S::KT + wave * S::RW) & ((1 << a.c.page_shift) - 1);
-    rw_copy<D>(a.c.pool + page * a.c.page_stride + ((int64_t)head << a.c.page_shift) * D, a.c.v_off, slot, keys, vals, wave, lane);
-  };
-  int page = 0;
-  if (t0 < t1) {
-    copy(t0, page_of(t0), K0, V0);
-    page = page_of(t0 + 1);
-  }
-  const auto step = [&](int t, char* keys, char* vals, char* keys2, char* vals2) {
-    const int tok = tr.at(t) * S::KT;
-    __builtin_amdgcn_s_waitcnt(RW_WAIT_VM);  // this wave's copies have landed
-    rw_barrier();                            // everyone's have, and the other buffer is free
-    if (t + 1 < t1) {
-      copy(t + 1, page, keys2, vals2);
-      page = page_of(t + 2);
-    }
-    const uint8_t* noted = nullptr;
-    if (!at_all_see(p0, p1, tok, tok + S::KT - 1, a.window, a.sinks)) {
-      // values of tokens that no row of the block sees become 0, whatever their
-      // memory held; is one that some rows see and others may not not finite?
-      bool nf = false;
+  int clear0, clear1, wclear0, wclear1;
+  clear(p0, p1, clear0, clear1);
+  clear(pw0, max(pw0, pw1), wclear0, wclear1);
+  // values of tile t, once they have landed: those of tokens that no row of the block
+  // sees become 0, whatever their memory held; the notes if one that some rows see and
+  // others may not is not finite
+  const auto mend = [&](int t, char* v) -> const uint8_t* {
+    if (t >= clear0 && t < clear1) return nullptr;
+    const int tok = token(t);
+    uint32_t top = 0;
+    const int far = a.window ? max(p0, 0) - a.window + 1 : 0;  // the first row's oldest token
 #pragma unroll
-      for (int i = 0; i < S::LD; ++i) {
-        const int k = tok + wave * S::RW + (i * 64 + lane) / S::KC;
-        kv_u4* p = reinterpret_cast<kv_u4*>(vals + (wave * S::LD + i) * 1024 + lane * 16);
-        const bool seen = k <= p1 && (a.window == 0 || k > max(p0, 0) - a.window || k < a.sinks);
-        if (seen) {
-          const kv_u4 v = *p;
-          nf = nf | at_odd<BF>(v.x) | at_odd<BF>(v.y) | at_odd<BF>(v.z) | at_odd<BF>(v.w);
-        } else {
-          *p = kv_u4{0, 0, 0, 0};
-        }
+    for (int i = 0; i < S::LD; ++i) {
+      const int k = tok + wave * S::RW + (i * 64 + lane) / S::KC;
+      kv_u4* p = reinterpret_cast<kv_u4*>(v + (wave * S::LD + i) * 1024 + lane * 16);
+      if (k <= p1 && ((int)(k >= far) | (int)(k < a.sinks))) {
+        const kv_u4 w = *p;
+        top = at_top(at_top(at_top(at_top(top, w.x), w.y), w.z), w.w);
+      } else {
+        *p = kv_u4{0, 0, 0, 0};
       }
-      if (__any(nf) && lane == 0) odd_at = t + 1;
-      rw_barrier();
-      if (odd_at == t + 1) {
+    }
+    if (__any(top >= at_exp_mask<BF>()) && lane == 0) odd_at = t + 1;
+    rw_barrier();
+    if (odd_at != t + 1) return nullptr;
 #pragma unroll 1
-        for (int i = 0; i < S::LD; ++i) {
-          const int x = i * 64 + lane, tt = wave * S::RW + x / S::KC, c = (x % S::KC) ^ rw_val_swz<D>(tt);
-          kv_u4* p = reinterpret_cast<kv_u4*>(vals + (wave * S::LD + i) * 1024 + lane * 16);
-          kv_u4 v = *p;
-          uint32_t bp = 0, bn = 0;
+    for (int i = 0; i < S::LD; ++i) {
+      const int x = i * 64 + lane, tt = wave * S::RW + x / S::KC, c = (x % S::KC) ^ rw_val_swz<D>(tt);
+      kv_u4* p = reinterpret_cast<kv_u4*>(v + (wave * S::LD + i) * 1024 + lane * 16);
+      kv_u4 w = *p;
+      uint32_t bp = 0, bn = 0;
 #pragma unroll
-          for (int y = 0; y < 4; ++y) v[y] = at_take<BF>(v[y], 2 * y, bp, bn);
-          *p = v;
-          notes[tt * S::KC + c] = (uint8_t)bp;
-          notes[S::bytes / 16 + tt * S::KC + c] = (uint8_t)bn;
-        }
-        rw_barrier();
-        noted = notes;
-      }
+      for (int y = 0; y < 4; ++y) w[y] = at_take<BF>(w[y], 2 * y, bp, bn);
+      *p = w;
+      notes[tt * S::KC + c] = (uint8_t)bp;
+      notes[S::bytes / 16 + tt * S::KC + c] = (uint8_t)bn;
     }
-    // a wave none of whose rows sees the tile passes it by
-    if (pw0 <= pw1 && tok <= pw1 && (a.window == 0 || tok + S::KT - 1 > pw0 - a.window || tok < a.sinks))
-      rw_tile<D, BF>(r, a, keys, vals, tok, pw0, pw1, noted, lane);
+    rw_barrier();
+    return notes;
   };
-  for (int t = t0; t < t1; t += 2) {
-    step(t, K0, V0, K1, V1);
-    if (t + 1 < t1) step(t + 1, K1, V1, K0, V0);
+
+  // The tiles.  Waves w and w + 4 share a SIMD, so the first four and the last four
+  // run half a step apart: while one does matrix products (values of tile t, keys of
+  // tile t + 1), the other does the exponentials of a tile.  Two barriers a step:
+  //   bound(t):  keys t and values t - 1 are there; copies of keys t + AHEAD and values
+  //              t + AHEAD - 1 go out
+  //              early waves: products t - 1, scores t    late waves: softmax t - 1
+  //   barrier
+  //              early waves: softmax t                   late waves: products t - 1, scores t
+  const bool late = S::NW == 8 && wave >= 4;
+  at_f16 s[S::NT];
+  kv_u4 P[2 * S::NT];
+  const uint8_t* noted = nullptr;
+  const auto key_buf = [&](int t) { return keys + (t & (S::NB - 1)) * S::bytes; };
+  const auto val_buf = [&](int t) { return vals + (t & (S::NB - 1)) * S::bytes; };
+  // The copies.  What a send needs is made while the one before is on its way: the
+  // table entry of this wave's tokens of the next tile is loaded then and looked at
+  // only when it is used, and the values' address is the keys' of a send before.
+  const int mask = (1 << a.c.page_shift) - 1;
+  const char* const pool0 = reinterpret_cast<const char*>(a.c.pool) + (((int64_t)head << a.c.page_shift)) * D * 2;
+  const int64_t page_bytes = a.c.page_stride * 2, v_bytes = a.c.v_off * 2;
+  const int lane0 = wave * S::RW;
+  int at_tok = 0, at_id = 0;        // this wave's first token of the tile to be sent next, its page's id
+  const char* before = pool0;    // where the keys sent last came from
+  int kofs[S::LD], vofs[S::LD];  // this lane's byte of each copy
+#pragma unroll
+  for (int i = 0; i < S::LD; ++i) {
+    const int x = i * 64 + lane, k = x / S::KC, c = x % S::KC;  // token of the wave's, chunk's place
+    kofs[i] = k * D * 2 + (c ^ rw_key_swz<D>(lane0 + k)) * 16;
+    vofs[i] = k * D * 2 + (c ^ rw_val_swz<D>(lane0 + k)) * 16;
+  }
+  const auto look = [&](int t) {
+    at_tok = token(min(t, nt - 1)) + lane0;
+    at_id = kv_table(table, min(at_tok, p1) >> a.c.page_shift);
+  };
+  const auto send = [&](int t) {
+    const int to = (t + S::AHEAD) & (S::NB - 1), to1 = (t + S::AHEAD - 1) & (S::NB - 1);
+    const char* const from = pool0 + kv_page(a.c, at_id) * page_bytes + (at_tok & mask) * (D * 2);
+    if (t + S::AHEAD < nt)
+#pragma unroll
+      for (int i = 0; i < S::LD; ++i) rw_copy(from, kofs[i], keys + to * S::bytes + (wave * S::LD + i) * 1024);
+    if (t + S::AHEAD > 0 && t + S::AHEAD - 1 < nt)
+#pragma unroll
+      for (int i = 0; i < S::LD; ++i) rw_copy(before + v_bytes, vofs[i], vals + to1 * S::bytes + (wave * S::LD + i) * 1024);
+    before = from;
+    look(t + S::AHEAD + 1);
+  };
+  const auto bound = [&](int t) {
+    // this wave's copies of keys t and values t - 1 have landed: where the AHEAD - 1
+    // sends since were whole, all but theirs; near the end, all
+    if (t + S::AHEAD <= nt) __builtin_amdgcn_s_waitcnt(at_wait_vm((S::AHEAD - 1) * 2 * S::LD));
+    else __builtin_amdgcn_s_waitcnt(at_wait_vm(0));
+    rw_barrier();  // everyone's have, and the buffers of the tile before are free
+    noted = t > 0 ? mend(t - 1, val_buf(t - 1)) : nullptr;
+    send(t);
+  };
+  if (nt > 0) {
+    look(0);
+#pragma unroll
+    for (int t = -S::AHEAD; t < 0; ++t) send(t);
+    bound(0);
+    if (late) rw_barrier();
+    rw_scores<D, BF>(s, r, key_buf(0), lane);
+    for (int t = 0; t < nt; ++t) {
+      if (late) bound(t + 1);
+      else if constexpr (S::NW == 8) rw_barrier();
+      rw_softmax<D, BF>(P, s, r, a, token(t), t < wclear0 || t >= wclear1, lane);
+      if (!late) bound(t + 1);
+      else rw_barrier();
+      rw_products<D, BF>(r, P, a, val_buf(t), token(t), noted, lane);
+      if (t + 1 < nt) rw_scores<D, BF>(s, r, key_buf(t + 1), lane);
+    }
+    if (S::NW == 8 && !late) rw_barrier();
   }
 
   r.l += __shfl_xor(r.l, 32);
@@ -335,7 +432,8 @@ void k_attn_rows(AttnArgs a) {
     if (h == 0) at_st2(rs, slot + S::BM * D + 2 * row, r.m * a.scale_log2, r.l);
   }
   if (!at_last(a.counters + blockIdx.x / a.splits, parts, &flag)) return;
-  at_join<BF, D, 64 * S::NW>(a, rs, e, head, r0, nrows, S::BM, parts, reinterpret_cast<float*>(K0),
+  at_join<BF, D, 64 * S::NW>(a, rs, e, head, r0, nrows, S::BM, parts, reinterpret_cast<float*>(keys),
+                 reinterpret_cast<float*>(keys) + AT_JOIN_CAP, reinterpret_cast<float*>(vals),
                  [&](int k) { return (blockIdx.x - z + k) * (uint32_t)rows_slot(D); });
 }
 

@@ -34,7 +34,7 @@
 namespace qg {
 
 constexpr int ST_TK = 32;  // tokens of a tile
-constexpr int ST_COST = 4; // tiles that beginning and ending an (entry, kv head) is worth
+constexpr int ST_COST = 16;  // tiles that beginning and ending an (entry, kv head) is worth
 
 template <int D, int MT = 1> struct StepShape {
   static constexpr int NW = step_waves(MT, D);   // waves of a workgroup
@@ -44,7 +44,11 @@ template <int D, int MT = 1> struct StepShape {
   static constexpr int LD = D + 4;               // padded row of the cross-wave buffer (floats)
   static constexpr int NB = VL * 16;             // bytes of noted values per token (one per value load)
   static constexpr size_t notes = (size_t)NW * 2 * ST_TK * NB;
-  static constexpr size_t lds = (size_t)NW * 16 * LD * 4 + NW * 16 * 8 + notes + 64;
+  // q in LDS (else in registers)
+  static constexpr bool QL = false;
+  static constexpr size_t q = QL ? (size_t)MT * 16 * D * 2 : 0;
+  static constexpr size_t lds = (size_t)NW * 16 * LD * 4 + NW * 16 * 8 + notes + q + 64;
+  static_assert(NW * 16 * LD >= 3 * AT_JOIN_CAP && LD * 4 * 16 >= ST_TK * D * 2, "what shares the buffer");
 };
 
 // the call's list in LDS: an entry's slot, length, first row and rows, and its places
@@ -122,9 +126,6 @@ template <int D> __device__ __forceinline__ void step_load_v(StepTile<D>& t, con
     }
 }
 
-// s_waitcnt vmcnt(n), the other counters left alone
-__host__ __device__ constexpr int step_wait_vm(int n) { return (n & 15) | 0x0F70 | (n >> 4) << 14; }
-
 // token of a tile that a lane quarter's register (weight, value) j stands for
 __device__ __forceinline__ int step_tok(int q, int j) { return 16 * (j >> 2) + 4 * q + (j & 3); }
 
@@ -154,7 +155,8 @@ void k_attn_step(AttnArgs a) {
   float* buf = reinterpret_cast<float*>(smem);                                    // [wave][16][LD]
   float* ml = buf + NW * 16 * S::LD;                                              // [wave][16][2]
   uint8_t* notes = reinterpret_cast<uint8_t*>(ml + NW * 16 * 2);                  // [wave][2][32][NB]
-  int* flag = reinterpret_cast<int*>(notes + S::notes);                           // [16]
+  char* const qs = reinterpret_cast<char*>(notes + S::notes);                     // [16 MT][D], QL only
+  int* flag = reinterpret_cast<int*>(qs + S::q);                                  // [16]
   KvEntry* list = reinterpret_cast<KvEntry*>(flag + 16);                          // [n]
   int* pre = reinterpret_cast<int*>(list + a.b.n);                                // [n + 1]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -198,15 +200,16 @@ void k_attn_step(AttnArgs a) {
       __syncthreads();
     }
   }
-  const int64_t places = (int64_t)pre[n] * heads;
-  const int64_t per = max((places + a.workers - 1) / a.workers, (int64_t)a.min_run);
-  int64_t u = blockIdx.x * per;
-  const int64_t u1 = min(u + per, places);
+  // (the host has made sure that the places of all heads stay below 2^30)
+  const int places = __builtin_amdgcn_readfirstlane(pre[n]) * heads;
+  const int per = max((places + a.workers - 1) / a.workers, a.min_run);
+  int u = min((int)blockIdx.x, places / per + 1) * per;
+  const int u1 = min(u + per, places);
 
   int j = 0;  // the entry that holds place u
   if (u < u1)
     for (;; j += 64) {
-      const uint64_t past = __ballot(j + lane < n && (int64_t)pre[min(j + lane, n - 1) + 1] * heads > u);
+      const uint64_t past = __ballot(j + lane < n && pre[min(j + lane, n - 1) + 1] * heads > u);
       if (past) {
         j += __builtin_ctzll(past);
         break;
@@ -214,14 +217,13 @@ void k_attn_step(AttnArgs a) {
     }
   while (u < u1) {
     // entry, kv head and tiles of the run's next part
-    while ((int64_t)pre[j + 1] * heads <= u) ++j;
+    while (pre[j + 1] * heads <= u) ++j;
     j = __builtin_amdgcn_readfirstlane(j);
-    const int len = __builtin_amdgcn_readfirstlane(pre[j + 1] - pre[j]), nt = len - ST_COST;
-    const int64_t seg = (int64_t)pre[j] * heads;
-    const int head = __builtin_amdgcn_readfirstlane((int)((u - seg) / len));
-    const int64_t tile0 = seg + (int64_t)head * len + ST_COST;  // place of (entry, head)'s first tile
-    const int t0 = __builtin_amdgcn_readfirstlane((int)max(u - tile0, (int64_t)0));
-    const int t1 = __builtin_amdgcn_readfirstlane((int)min((int64_t)nt, u1 - tile0));
+    const int before = __builtin_amdgcn_readfirstlane(pre[j]);
+    const int len = __builtin_amdgcn_readfirstlane(pre[j + 1]) - before, nt = len - ST_COST;
+    const int seg = before * heads, head = (u - seg) / len;
+    const int tile0 = seg + head * len + ST_COST;  // place of (entry, head)'s first tile
+    const int t0 = max(u - tile0, 0), t1 = min(nt, u1 - tile0);
     u = tile0 + nt;
     if (t0 >= t1) continue;  // the run ends before its first tile
     KvEntry e = list[j];
@@ -232,19 +234,30 @@ void k_attn_step(AttnArgs a) {
     const int32_t* table = a.c.tables + (int64_t)e.slot * a.c.max_pages;
 
     // the rows of this kv head: row r is new token r / G, q head head * G + r % G
-    kv_u4 Q[MT][D / 32];
+    const auto q_at = [&](int r, int chunk) {
+      const int i = r / a.G;
+      return *reinterpret_cast<const kv_u4*>(a.q.ptr + (int64_t)(e.row0 + i) * a.q.row +
+                                             (int64_t)(head * a.G + r - i * a.G) * a.q.head + chunk * 8);
+    };
+    kv_u4 Q[S::QL ? 1 : MT][D / 32];
     int pos[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       const int r = mt * 16 + col;
       const bool live = r < nrows;
-      const int i = live ? r / a.G : 0;
-      pos[mt] = live ? p0 + i : -1;
-      const uint16_t* qp = a.q.ptr + (int64_t)(e.row0 + i) * a.q.row + (int64_t)(head * a.G + (live ? r - i * a.G : 0)) * a.q.head + q * 8;
+      pos[mt] = live ? p0 + r / a.G : -1;
+      if constexpr (!S::QL) {
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        Q[mt][c] = *reinterpret_cast<const kv_u4*>(qp + 32 * c);
-        if (!live) Q[mt][c] = kv_u4{0, 0, 0, 0};
+        for (int c = 0; c < D / 32; ++c) {
+          Q[mt][c] = q_at(live ? r : 0, 4 * c + q);
+          if (!live) Q[mt][c] = kv_u4{0, 0, 0, 0};
+        }
+      }
+    }
+    if constexpr (S::QL) {
+      for (int x = tid; x < MT * 16 * (D / 8); x += 64 * NW) {
+        const int r = x / (D / 8), c = x % (D / 8);
+        *reinterpret_cast<kv_u4*>(qs + (r * (D / 8) + (c ^ step_swz<D>(r & 15))) * 16) = r < nrows ? q_at(r, c) : kv_u4{0, 0, 0, 0};
       }
     }
     at_f4 O[MT][S::VE];
@@ -276,7 +289,7 @@ void k_attn_step(AttnArgs a) {
       const bool more = tl + NW < t1;
       pg = step_pages(a.c, ids, tok2, head, D, more);
       // the keys have landed when only the value loads, issued after them, are left
-      __builtin_amdgcn_s_waitcnt(step_wait_vm(8 * S::VL));
+      __builtin_amdgcn_s_waitcnt(at_wait_vm(8 * S::VL));
       asm volatile("" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
       at_f4 s[MT][2];
@@ -289,7 +302,11 @@ void k_attn_step(AttnArgs a) {
         for (int mt = 0; mt < MT; ++mt) {
           s[mt][h] = at_f4{0, 0, 0, 0};
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) s[mt][h] = at_mfma16<BF>(K[c], Q[mt][c], s[mt][h]);
+          for (int c = 0; c < D / 32; ++c) {
+            // (row mt * 16 + col of q lies in LDS as token col of a tile's half)
+            const kv_u4 B = S::QL ? *reinterpret_cast<const kv_u4*>(qs + (kb ^ (c << 6)) + mt * 16 * D * 2) : Q[S::QL ? 0 : mt][c];
+            s[mt][h] = at_mfma16<BF>(K[c], B, s[mt][h]);
+          }
         }
       }
       // the reads have returned before the next tile's copy may overwrite what they read
@@ -307,9 +324,12 @@ void k_attn_step(AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = s[mt][i >> 2][i & 3] * a.scale_log2;
         if (masked) {
+          const SeenFrom seen(pos[mt], tok + 4 * q, a.window, a.sinks);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (!at_sees(pos[mt], tok + step_tok(q, i), a.window, a.sinks)) x[i] = -__builtin_inff();
+          for (int i = 0; i < 8; ++i) {
+            x[i] = seen(step_tok(0, i)) ? x[i] : -__builtin_inff();
+            if (i & 1) __builtin_amdgcn_sched_barrier(0);
+          }
         }
         float mx = x[0];
 #pragma unroll
@@ -337,19 +357,21 @@ void k_attn_step(AttnArgs a) {
       if (masked) {
         // tokens that no row sees count for nothing, whatever their memory holds;
         // what only some rows see needs care where it is not finite
-        bool nf = false;
+        uint32_t top = 0;
+        const int far = a.window ? max(p0, 0) - a.window + 1 : 0;  // the first row's oldest token
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int key = tok + step_tok(q, i);
-          const bool seen = key <= p1 && (a.window == 0 || key > max(p0, 0) - a.window || key < a.sinks);
+          const bool seen = (int)(key <= p1) & ((int)(key >= far) | (int)(key < a.sinks));
 #pragma unroll
           for (int c = 0; c < S::VE / 2; ++c) {
             t.v[i][c] = seen ? t.v[i][c] : 0;
-            nf |= at_odd<BF>(t.v[i][c]);
+            top = at_top(top, t.v[i][c]);
           }
+          __builtin_amdgcn_sched_barrier(0);
         }
-        odd = __any(nf);
-        if (odd) {
+        odd = __any(top >= at_exp_mask<BF>());
+        if (__builtin_expect(odd, 0)) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -370,7 +392,7 @@ void k_attn_step(AttnArgs a) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) O[mt][c] = at_mfma16<BF>(A, P[mt], O[mt][c]);
       }
-      if (odd) {
+      if (__builtin_expect(odd, 0)) {
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll 1
         for (int k = 0; k < ST_TK; ++k)
@@ -450,9 +472,9 @@ void k_attn_step(AttnArgs a) {
     if (whole) continue;
 
     // several workgroups share (entry, head): the last to arrive joins them, in list order
-    const int64_t w0 = tile0 / per, w1 = (tile0 + nt - 1) / per;
-    if (!at_last(a.counters + j * heads + head, (int)(w1 - w0) + 1, flag)) continue;
-    at_join<BF, D, 64 * NW>(a, rs, e, head, 0, nrows, MT * 16, (int)(w1 - w0) + 1, buf, [&](int k) {
+    const int w0 = tile0 / per, parts = (tile0 + nt - 1) / per - w0 + 1;
+    if (!at_last(a.counters + j * heads + head, parts, flag)) continue;
+    at_join<BF, D, 64 * NW>(a, rs, e, head, 0, nrows, MT * 16, parts, buf, buf + AT_JOIN_CAP, buf + 2 * AT_JOIN_CAP, [&](int k) {
       return (uint32_t)(2 * (w0 + k) + (k == 0 ? 1 : 0)) * (uint32_t)step_slot(MT, D);
     });
     __syncthreads();  // the join's use of the buffer is over

@@ -276,8 +276,11 @@ qg_status qgkv_attend(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const
   hipStream_t st = (hipStream_t)stream;
   if (rows <= step_max_rows(D)) {
     const int MT = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
+    // places of the few-row kernel's list
+    if ((int64_t)(a.c.cap / 32 + 32) * a.b.n * a.c.kv_heads >= (int64_t)1 << 30)
+      return fail(QG_ERR_UNSUPPORTED, "%d entries of up to %d tokens and %d kv heads in one call", a.b.n, a.c.cap, a.c.kv_heads);
     a.workers = h->cus;
-    a.min_run = getenv("QG_MINRUN") ? atoi(getenv("QG_MINRUN")) : 8;
+    a.min_run = STEP_MIN_RUN;
     return done(h, launch_attn_step(a, D, bf16, MT, st), st);
   }
   // a call of few blocks is split over the tokens until it covers the chip

@@ -8,7 +8,6 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import math
 
 __all__ = ["KVCache"]
 
@@ -118,87 +117,120 @@ class KVCache:
             h = ctypes.c_void_p()
             _check(lib().qgkv_create(ctypes.byref(h), ctypes.byref(d), _stream(stream)))
         self._h = h
+        # what a call needs besides its tensors, made once: the bound functions, the
+        # argument blocks (calls on one cache are ordered by the caller), the device
+        L = lib()
+        self._c = {n: getattr(L, "qgkv_" + n) for n in ("extend", "fork", "trim", "compact", "append", "attend")}
+        self._check = _check
+        self._torch = torch
+        self._dev = pool.get_device()
+        self._dtype = pool.dtype
+        self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self._args = (_KvBatch(), _KvRows(), _KvRows())
+        self._refs = tuple(ctypes.byref(x) for x in self._args)
 
     @property
     def handle(self):
         return self._h
 
-    def _index(self, name, x, n=None):
+    def _on(self, stream) -> int:
+        """The stream of a call: the given one or the current one of the cache's GPU."""
+        if self._h is None:
+            raise ValueError("the cache is closed")
+        if stream is not None:
+            return stream.cuda_stream
+        if self._raw_stream is not None:
+            return self._raw_stream(self._dev)
+        return self._torch.cuda.current_stream(self._dev).cuda_stream
+
+    def _call(self, name, *args) -> None:
+        st = self._c[name](self._h, *args)
+        if st:
+            self._check(st)
+
+    def _index(self, name, x, n=None, stream=None):
         """An int32 tensor on the cache's GPU (lists are copied there)."""
-        import torch
-        if x is None:
-            return None
+        torch = self._torch
         if not isinstance(x, torch.Tensor):
-            x = torch.tensor(list(x), dtype=torch.int32, device=self.pool.device)
-        if x.dtype != torch.int32 or x.dim() != 1 or x.device != self.pool.device or not x.is_contiguous():
+            with _on(stream):  # memory made here belongs to the stream that uses it
+                x = torch.tensor(list(x), dtype=torch.int32, device=self.pool.device)
+        if x.dtype != torch.int32 or x.dim() != 1 or x.get_device() != self._dev or not x.is_contiguous():
             raise ValueError(f"{name} must be a contiguous 1-d int32 tensor on {self.pool.device}")
         if n is not None and x.numel() != n:
             raise ValueError(f"{name} has {x.numel()} entries, not {n}")
         return x
 
-    def _rows(self, name, t, heads=None, rows=None) -> _KvRows:
-        if t.dim() != 3 or t.shape[2] != self.head_dim or (heads is not None and t.shape[1] != heads) \
-                or (rows is not None and t.shape[0] != rows):
+    def _rows(self, into: _KvRows, name, t, heads=None, rows=None) -> tuple:
+        """Fill an argument block; the operand's (rows, heads)."""
+        size = t.shape
+        if len(size) != 3 or size[2] != self.head_dim or (heads is not None and size[1] != heads) \
+                or (rows is not None and size[0] != rows):
             raise ValueError(f"{name} must be [{'rows' if rows is None else rows}]"
-                             f"[{'heads' if heads is None else heads}][{self.head_dim}], not {list(t.shape)}")
-        if t.dtype != self.pool.dtype or t.device != self.pool.device:
-            raise ValueError(f"{name} must be {self.pool.dtype} on {self.pool.device}")
-        if t.stride(2) != 1:
+                             f"[{'heads' if heads is None else heads}][{self.head_dim}], not {list(size)}")
+        if t.dtype != self._dtype or t.get_device() != self._dev:
+            raise ValueError(f"{name} must be {self._dtype} on {self.pool.device}")
+        into.row_stride, into.head_stride, last = t.stride()
+        if last != 1:
             raise ValueError(f"{name}: the last axis must be contiguous")
-        return _KvRows(t.data_ptr(), t.stride(0), t.stride(1))
+        into.ptr = t.data_ptr()
+        return size[0], size[1]
 
-    def _batch(self, rows, seqs, row_start, max_rows):
-        seqs = self._index("seqs", seqs)
+    def _batch(self, rows, seqs, row_start, max_rows, stream):
+        """Fill the call's batch; the index tensors, which the caller holds until the call is made."""
+        b = self._args[0]
+        b.rows = rows
+        n = None
+        if seqs is not None:
+            seqs = self._index("seqs", seqs, None, stream)
+            n = seqs.numel()
         if row_start is not None:
-            row_start = self._index("row_start", row_start, None if seqs is None else seqs.numel() + 1)
-            n = row_start.numel() - 1
+            row_start = self._index("row_start", row_start, None if n is None else n + 1, stream)
             if max_rows is None:
                 raise ValueError("row_start needs max_rows, the largest number of rows of an entry")
+            n = row_start.numel() - 1
+            b.max_rows, b.row_start = int(max_rows), row_start.data_ptr()
         else:
-            n = seqs.numel() if seqs is not None else min(rows, self.max_seqs)
-        b = _KvBatch(n, rows, 0 if row_start is None else int(max_rows),
-                     None if seqs is None else seqs.data_ptr(), None if row_start is None else row_start.data_ptr())
-        return b, (seqs, row_start)
+            n = min(rows, self.max_seqs) if n is None else n
+            b.max_rows, b.row_start = 0, None
+        b.n = n
+        b.seqs = None if seqs is None else seqs.data_ptr()
+        return seqs, row_start
 
     def extend(self, n_new, stream=None) -> None:
         """Room for n_new[s] more tokens in every slot s; lens grow by them."""
-        from . import _check, _stream, lib
-        with self._at(stream):
-            n_new = self._index("n_new", n_new, self.max_seqs)
-            _check(lib().qgkv_extend(self._h, n_new.data_ptr(), _stream(stream)))
+        st = self._on(stream)
+        n_new = self._index("n_new", n_new, self.max_seqs, stream)
+        self._call("extend", n_new.data_ptr(), st)
 
     def fork(self, src, dst, stream=None) -> None:
         """The empty slots dst become second names of the slots src."""
-        from . import _check, _stream, lib
-        with self._at(stream):
-            src = self._index("src", src)
-            dst = self._index("dst", dst, src.numel())
-            _check(lib().qgkv_fork(self._h, src.data_ptr(), dst.data_ptr(), src.numel(), _stream(stream)))
+        st = self._on(stream)
+        src = self._index("src", src, None, stream)
+        dst = self._index("dst", dst, src.numel(), stream)
+        self._call("fork", src.data_ptr(), dst.data_ptr(), src.numel(), st)
 
     def trim(self, seqs, keep=None, stream=None) -> None:
         """Cut slots to their first ``keep`` tokens (default 0: free them)."""
-        from . import _check, _stream, lib
-        with self._at(stream):
-            seqs = self._index("seqs", seqs)
-            keep = self._index("keep", keep, seqs.numel())
-            _check(lib().qgkv_trim(self._h, seqs.data_ptr(), None if keep is None else keep.data_ptr(), seqs.numel(),
-                                   _stream(stream)))
+        st = self._on(stream)
+        seqs = self._index("seqs", seqs, None, stream)
+        if keep is not None:
+            keep = self._index("keep", keep, seqs.numel(), stream)
+        self._call("trim", seqs.data_ptr(), None if keep is None else keep.data_ptr(), seqs.numel(), st)
 
     def compact(self, stream=None) -> None:
         """Move the live pages to the lowest ids."""
-        from . import _check, _stream, lib
-        with self._at(stream):
-            _check(lib().qgkv_compact(self._h, _stream(stream)))
+        self._call("compact", self._on(stream))
 
     def append(self, k, v, *, layer: int = 0, seqs=None, row_start=None, max_rows: int = None, stream=None) -> None:
         """Write the rows' keys and values, [rows][kv_heads][head_dim] each."""
-        from . import _check, _stream, lib
-        with self._at(stream):
-            kr = self._rows("k", k, self.kv_heads)
-            vr = self._rows("v", v, self.kv_heads, k.shape[0])
-            b, _keep = self._batch(k.shape[0], seqs, row_start, max_rows)
-            _check(lib().qgkv_append(self._h, int(layer), ctypes.byref(b), ctypes.byref(kr), ctypes.byref(vr),
-                                     _stream(stream)))
+        st = self._on(stream)
+        _, ka, va = self._args
+        rows, _ = self._rows(ka, "k", k, self.kv_heads)
+        self._rows(va, "v", v, self.kv_heads, rows)
+        held = self._batch(rows, seqs, row_start, max_rows, stream)
+        rb, rk, rv = self._refs
+        self._call("append", layer, rb, rk, rv, st)
+        del held
 
     def attend(self, q, *, layer: int = 0, seqs=None, row_start=None, max_rows: int = None, scale: float = None,
                window: int = 0, sinks: int = 0, out=None, stream=None):
@@ -206,17 +238,17 @@ class KVCache:
         layer; returns out of the same shape.  scale: default head_dim ** -0.5.
         window: a row sees its last ``window`` tokens (0: all) and the first
         ``sinks`` of its slot."""
-        import torch
-        from . import _check, _stream, lib
-        with self._at(stream):
-            qr = self._rows("q", q)
-            if out is None:
-                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            o = self._rows("out", out, q.shape[1], q.shape[0])
-            b, _keep = self._batch(q.shape[0], seqs, row_start, max_rows)
-            sc = 1.0 / math.sqrt(self.head_dim) if scale is None else float(scale)
-            _check(lib().qgkv_attend(self._h, int(layer), ctypes.byref(b), ctypes.byref(qr), ctypes.byref(o),
-                                     q.shape[1], sc, int(window), int(sinks), _stream(stream)))
+        st = self._on(stream)
+        _, qa, oa = self._args
+        rows, heads = self._rows(qa, "q", q)
+        if out is None:
+            with _on(stream):
+                out = self._torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        self._rows(oa, "out", out, heads, rows)
+        held = self._batch(rows, seqs, row_start, max_rows, stream)
+        rb, rq, ro = self._refs
+        self._call("attend", layer, rb, rq, ro, heads, self.head_dim ** -0.5 if scale is None else scale, window, sinks, st)
+        del held
         return out
 
     def check(self) -> None:
@@ -232,12 +264,6 @@ class KVCache:
         if bits & INFO_PAIR:
             raise QGError(QG_ERR_INVALID_ARG, "fork / trim: an entry was refused")
 
-    def _at(self, stream):
-        """Tensors made inside belong to the stream that the work runs on."""
-        if self._h is None:
-            raise ValueError("the cache is closed")
-        return _on(stream)
-
     def close(self):
         if getattr(self, "_h", None) is not None:
             from . import lib
@@ -251,6 +277,12 @@ class KVCache:
             pass
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(stream):
+    """Tensors made inside belong to the stream that the work runs on."""
+    if stream is None:
+        return _HERE
     import torch
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return torch.cuda.stream(stream)
