@@ -71,10 +71,13 @@ __device__ __forceinline__ void rw_copy(const char* from, int ofs, char* to) {
                                    (__attribute__((address_space(3))) void*)to, 16, 0, 0);
 }
 
+// Workgroup barrier that waits for this wave's LDS accesses but not for its copies on
+// their way into LDS (a fence would: to it they are LDS writes like any other).
 __device__ __forceinline__ void rw_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
   __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+  asm volatile("" ::: "memory");
 }
 
 // a wave's 32 rows
@@ -261,7 +264,7 @@ void k_attn_rows(AttnArgs a) {
   // this wave's rows
   RowsState<D> r;
   const int rw = r0 + wave * 32 + col;
-  const bool live = rw < total;
+  const bool live = rw < total, alive = r0 + wave * 32 < total;
   const int ri = live ? rw / a.G : 0;
   r.pos = live ? pe + ri : -1;
   const int pw0 = pe + (r0 + wave * 32) / a.G, pw1 = min(pe + (r0 + wave * 32 + 31) / a.G, p1);
@@ -336,11 +339,12 @@ void k_attn_rows(AttnArgs a) {
   // The tiles.  Waves w and w + 4 share a SIMD, so the first four and the last four
   // run half a step apart: while one does matrix products (values of tile t, keys of
   // tile t + 1), the other does the exponentials of a tile.  Two barriers a step:
-  //   bound(t):  keys t and values t - 1 are there; copies of keys t + AHEAD and values
-  //              t + AHEAD - 1 go out
-  //              early waves: products t - 1, scores t    late waves: softmax t - 1
+  //   bound(t):  keys t and values t - 1 are there
+  //              early waves: products t - 1, scores t    late waves: send t, softmax t - 1
   //   barrier
-  //              early waves: softmax t                   late waves: products t - 1, scores t
+  //              early waves: send t, softmax t           late waves: products t - 1, scores t
+  // send t: the copies of keys t + AHEAD and values t + AHEAD - 1, into the buffers that
+  // tile t - 1 has left.
   const bool late = S::NW == 8 && wave >= 4;
   at_f16 s[S::NT];
   kv_u4 P[2 * S::NT];
@@ -386,23 +390,30 @@ void k_attn_rows(AttnArgs a) {
     else __builtin_amdgcn_s_waitcnt(at_wait_vm(0));
     rw_barrier();  // everyone's have, and the buffers of the tile before are free
     noted = t > 0 ? mend(t - 1, val_buf(t - 1)) : nullptr;
-    send(t);
   };
   if (nt > 0) {
     look(0);
 #pragma unroll
     for (int t = -S::AHEAD; t < 0; ++t) send(t);
     bound(0);
-    if (late) rw_barrier();
-    rw_scores<D, BF>(s, r, key_buf(0), lane);
+    if (late) {
+      send(0);
+      rw_barrier();
+    }
+    // a wave without rows only copies and keeps step
+    if (alive) rw_scores<D, BF>(s, r, key_buf(0), lane);
     for (int t = 0; t < nt; ++t) {
       if (late) bound(t + 1);
       else if constexpr (S::NW == 8) rw_barrier();
-      rw_softmax<D, BF>(P, s, r, a, token(t), t < wclear0 || t >= wclear1, lane);
+      send(late ? t + 1 : t);
+      if (alive) rw_softmax<D, BF>(P, s, r, a, token(t), t < wclear0 || t >= wclear1, lane);
       if (!late) bound(t + 1);
       else rw_barrier();
+      if (!alive) continue;
+      __builtin_amdgcn_s_setprio(1);  // a product is one issue in eight: let it have it
       rw_products<D, BF>(r, P, a, val_buf(t), token(t), noted, lane);
       if (t + 1 < nt) rw_scores<D, BF>(s, r, key_buf(t + 1), lane);
+      __builtin_amdgcn_s_setprio(0);
     }
     if (S::NW == 8 && !late) rw_barrier();
   }
