@@ -44,8 +44,8 @@ template <int D, int MT = 1> struct StepShape {
   static constexpr int LD = D + 4;               // padded row of the cross-wave buffer (floats)
   static constexpr int NB = VL * 16;             // bytes of noted values per token (one per value load)
   static constexpr size_t notes = (size_t)NW * 2 * ST_TK * NB;
-  // q in LDS (else in registers)
-  static constexpr bool QL = false;
+  // q in LDS, where two waves per SIMD have no registers left for it
+  static constexpr bool QL = MT == 3;
   static constexpr size_t q = QL ? (size_t)MT * 16 * D * 2 : 0;
   static constexpr size_t lds = (size_t)NW * 16 * LD * 4 + NW * 16 * 8 + notes + q + 64;
   static_assert(NW * 16 * LD >= 3 * AT_JOIN_CAP && LD * 4 * 16 >= ST_TK * D * 2, "what shares the buffer");

@@ -109,7 +109,7 @@ struct AttnArgs {
 // kv head); wide heads hold fewer for lack of registers
 __host__ __device__ constexpr int step_max_rows(int D) { return D == 256 ? 32 : 64; }
 // waves of a workgroup, one workgroup per CU: two waves per SIMD where the registers allow
-__host__ __device__ constexpr int step_waves(int MT, int D) { return D < 256 && MT * D <= 256 ? 8 : 4; }
+__host__ __device__ constexpr int step_waves(int MT, int D) { return D < 256 && MT * D <= 384 ? 8 : 4; }
 // Places of the list that a workgroup takes at least.  One request of 1,025 tokens, 40
 // q and 8 kv heads of 128: 13.4 us at 8, 13.1 at 12, 13.8 at 16, 16.0 at 24, 21.1 at 48
 // (fewer, longer runs save joins and cost round trips); from a few thousand tokens on

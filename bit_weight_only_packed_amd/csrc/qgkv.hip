@@ -275,7 +275,7 @@ qg_status qgkv_attend(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const
   if (rows >= (int64_t)1 << 30) return fail(QG_ERR_UNSUPPORTED, "%d rows of %d heads in one call", a.b.max_rows, a.G);
   hipStream_t st = (hipStream_t)stream;
   if (rows <= step_max_rows(D)) {
-    const int MT = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
+    const int MT = (int)(rows + 15) / 16;
     // places of the few-row kernel's list
     if ((int64_t)(a.c.cap / 32 + 32) * a.b.n * a.c.kv_heads >= (int64_t)1 << 30)
       return fail(QG_ERR_UNSUPPORTED, "%d entries of up to %d tokens and %d kv heads in one call", a.b.n, a.c.cap, a.c.kv_heads);
