@@ -105,7 +105,7 @@ __global__ __launch_bounds__(256) void k_kv_trim(KvPool p, const int32_t* seqs, 
 // Room for new tokens: thread s decides for slot s.
 __global__ __launch_bounds__(KV_PLAN) void k_kv_extend(KvPool p, const int32_t* n_new) {
   __shared__ int sums[KV_PLAN / 64];
-  __shared__ int tails[KV_PLAN];  // shared tail page that the slot would write to, or -1
+  __shared__ __align__(16) int tails[KV_PLAN];  // shared tail page that the slot would write to, or -1
   __shared__ int begin[KV_PLAN];  // pages taken by the slots before
   __shared__ int first[KV_PLAN];  // table entry of the slot's first new page; bit 30: a copy of its tail comes before
   const int s = threadIdx.x, P = 1 << p.page_shift;
@@ -129,10 +129,12 @@ __global__ __launch_bounds__(KV_PLAN) void k_kv_extend(KvPool p, const int32_t* 
   if (tail >= 0) {
     int growing = 0;
     bool lowest = true;
-    for (int k = 0; k < p.max_seqs; ++k) {
-      const bool same = tails[k] == tail;
-      growing += same;
-      lowest = lowest && !(same && k < s);
+#pragma unroll 4
+    for (int k = 0; k < p.max_seqs; k += 4) {  // (slots past max_seqs have -1)
+      const int4 t = *reinterpret_cast<const int4*>(tails + k);
+      growing += (t.x == tail) + (t.y == tail) + (t.z == tail) + (t.w == tail);
+      lowest = lowest & !((t.x == tail) & (k < s)) & !((t.y == tail) & (k + 1 < s)) & !((t.z == tail) & (k + 2 < s)) &
+               !((t.w == tail) & (k + 3 < s));
     }
     copy = !(growing == holders && lowest);
   }
