@@ -5,17 +5,24 @@ namespace qg {
 
 namespace {
 
-template <int D, bool BF> hipError_t go(const AttnArgs& a, unsigned blocks, hipStream_t st) {
-  k_attn_rows<D, BF><<<blocks * (unsigned)a.splits, 64 * RowsShape<D>::NW, 0, st>>>(a);
+template <int D> hipError_t go(const AttnArgs& a, bool bf16, unsigned blocks, hipStream_t st) {
+  const unsigned grid = blocks * (unsigned)a.splits;
+  if (bf16) k_attn_rows<D, true><<<grid, 64 * ROWS_WAVES, 0, st>>>(a);
+  else k_attn_rows<D, false><<<grid, 64 * ROWS_WAVES, 0, st>>>(a);
+  if (a.splits > 1) {
+    const unsigned join = blocks * (unsigned)(ROWS_BLOCK / RJ_ROWS);
+    if (bf16) k_attn_rows_join<D, true><<<join, RJ_THREADS, 0, st>>>(a);
+    else k_attn_rows_join<D, false><<<join, RJ_THREADS, 0, st>>>(a);
+  }
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_attn_rows(const AttnArgs& a, int D, bool bf16, unsigned blocks, hipStream_t st) {
-  if (D == 64) return bf16 ? go<64, true>(a, blocks, st) : go<64, false>(a, blocks, st);
-  if (D == 128) return bf16 ? go<128, true>(a, blocks, st) : go<128, false>(a, blocks, st);
-  return bf16 ? go<256, true>(a, blocks, st) : go<256, false>(a, blocks, st);
+  if (D == 64) return go<64>(a, bf16, blocks, st);
+  if (D == 128) return go<128>(a, bf16, blocks, st);
+  return go<256>(a, bf16, blocks, st);
 }
 
 }  // namespace qg

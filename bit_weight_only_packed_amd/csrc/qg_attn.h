@@ -148,8 +148,8 @@ __device__ __forceinline__ void at_store(const AttnArgs& a, const KvEntry& e, in
   }
 }
 
-// Join n partials of rows r0 .. r0 + nrows - 1 of (entry, head); slot(k) is where the
-// k-th lies (in floats): [ld][D] fp32, then (m, l) of each row.  Every sum runs in an
+// Join n partials of rows f0 .. f0 + nrows - 1 of a block of (entry, head) that begins
+// with row r0; slot(k) is where the k-th lies (in floats): [ld][D] fp32, then (m, l) of each row.  Every sum runs in an
 // order that n fixes.
 //
 // A round trip to the partials costs about 2 us, so there are two: one for all (m, l),
@@ -159,7 +159,7 @@ __device__ __forceinline__ void at_store(const AttnArgs& a, const KvEntry& e, in
 // fac, tot, part: AT_JOIN_CAP floats of LDS each; n <= AT_JOIN_CAP.
 constexpr int AT_JOIN_CAP = 2720;  // (row, partial) pairs at a time; 4 floats of 512 threads fit as well
 template <bool BF, int D, int THREADS, class F>
-__device__ __forceinline__ void at_join(const AttnArgs& a, __amdgpu_buffer_rsrc_t rs, const KvEntry& e, int head, int r0,
+__device__ __forceinline__ void at_join(const AttnArgs& a, __amdgpu_buffer_rsrc_t rs, const KvEntry& e, int head, int r0, int f0,
                                         int nrows, int ld, int n, float* fac, float* tot, float* part, F slot) {
   constexpr int NB = 16, NW = THREADS / 64;
   static_assert(4 * THREADS <= AT_JOIN_CAP, "part");
@@ -167,8 +167,8 @@ __device__ __forceinline__ void at_join(const AttnArgs& a, __amdgpu_buffer_rsrc_
   const int chunk = min(nrows, AT_JOIN_CAP / n);
   // fac [row][partial] m, then its factor; tot [row][partial] l, then [row][0] the sum;
   // part [thread][4] outputs of threads that share an item
-  for (int rb = 0; rb < nrows; rb += chunk) {
-    const int rows = min(chunk, nrows - rb);
+  for (int rb = f0; rb < f0 + nrows; rb += chunk) {
+    const int rows = min(chunk, f0 + nrows - rb);
     __syncthreads();
     for (int x = tid; x < rows * n; x += THREADS) {
       const int r = x / n, k = x - r * n;

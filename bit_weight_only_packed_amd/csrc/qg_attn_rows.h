@@ -6,9 +6,8 @@
 // A block is 32 rows per wave of one (entry, kv head): row r is new token r / G, q
 // head r % G of the group, so the q heads that share a kv head share its tokens,
 // and a block spans few positions (little is computed past the diagonal).  Tokens
-// come in tiles of KT = 8192 / D, keys and values 16 KiB each, straight from memory
-// into one of two LDS buffers (no registers); the next tile is on its way while
-// this one is computed.
+// come in tiles of KT, keys and values straight from memory into LDS (no registers),
+// the next tiles on their way while one is computed.
 //
 //   scores   S^T = K Q^T on 32x32x16 (A: keys from LDS, B: q from registers).  A
 //            lane holds 16 tokens of one row per 32, as token 8 (i / 4) + 4 h + i % 4
@@ -28,7 +27,7 @@
 
 namespace qg {
 
-constexpr int RW_MIN_TILES = 4;     // tiles of a split at least
+constexpr int RW_MIN_TILES = 8;     // tiles of a split at least
 constexpr float RW_SLACK = 8.0f;    // exponent that a weight may reach
 // operands read from LDS ahead of the product that takes them (an LDS round trip is
 // some 100 cycles, a product 32), and the scheduler's names of the two
@@ -36,17 +35,20 @@ constexpr int RW_DEEP = 6;
 constexpr int RW_MFMA = 0x8, RW_DS_READ = 0x100;
 
 template <int D> struct RowsShape {
-  static constexpr int NW = rows_waves(D);  // waves of a workgroup
-  static constexpr int BM = rows_block(D);  // rows of a block
-  static constexpr int KT = 8192 / D;       // tokens of a tile
+  static constexpr int NW = ROWS_WAVES;     // waves of a workgroup
+  static constexpr int BM = ROWS_BLOCK;     // rows of a block
+  static constexpr int KT = D == 256 ? 32 : 64;  // tokens of a tile
   static constexpr int KC = D / 8;          // 16-byte chunks of a token's key or value
   static constexpr int NT = KT / 32;        // 32-token groups
   static constexpr int ND = D / 32;         // 32-column groups
-  static constexpr int LD = 16 / NW;        // 1 KiB copies per wave of a tile's keys (or values)
+  static constexpr int bytes = KT * D * 2;  // a tile's keys (or values)
+  static constexpr int LD = bytes / 1024 / NW;  // 1 KiB copies per wave of them
   static constexpr int RW = KT / NW;        // tokens that a wave copies (they lie in one page)
-  static constexpr int bytes = 16384;       // a tile's keys (or values)
-  static constexpr int NB = 4;              // tiles of keys, and of values, in LDS
+  // tiles of keys, and of values, in LDS: two where two workgroups share a CU, four
+  // where the registers leave room for one
+  static constexpr int NB = D < 256 ? 2 : 4;
   static constexpr int AHEAD = NB - 1;      // a tile's copies go out this many tiles before its use
+  static_assert(RW <= 16, "a wave's tokens of a tile lie in one page");
 };
 
 // what a token's chunk index is exclusive-or'ed with.  Keys: 16 lanes read one chunk
@@ -89,6 +91,10 @@ template <int D> struct RowsState {
   int pos;      // this lane's row's position
 };
 
+// its scores with a tile, and their weights
+template <int D> using RowsScores = at_f16[RowsShape<D>::NT];
+template <int D> using RowsWeights = kv_u4[2 * RowsShape<D>::NT];
+
 // byte of this lane's part of the key reads, and of the value reads, but for what is
 // constant per read: an exclusive-or for the chunk, an immediate for the token
 template <int D> __device__ __forceinline__ int rw_key_byte(int lane) {
@@ -103,7 +109,7 @@ template <int D> __device__ __forceinline__ int rw_val_byte(int lane) {
 
 // scores of the wave's rows with a tile of keys
 template <int D, bool BF>
-__device__ __forceinline__ void rw_scores(at_f16 (&s)[RowsShape<D>::NT], const RowsState<D>& r, const char* keys, int lane) {
+__device__ __forceinline__ void rw_scores(RowsScores<D>& s, const RowsState<D>& r, const char* keys, int lane) {
   using S = RowsShape<D>;
   int kb = rw_key_byte<D>(lane);
   asm volatile("" : "+v"(kb));  // one instruction per read, not a register each: they are needed
@@ -130,7 +136,7 @@ __device__ __forceinline__ void rw_scores(at_f16 (&s)[RowsShape<D>::NT], const R
 
 // scores of tile tok .. tok + KT - 1 to weights; masked: some row does not see all of it
 template <int D, bool BF>
-__device__ __forceinline__ void rw_softmax(kv_u4 (&P)[2 * RowsShape<D>::NT], at_f16 (&s)[RowsShape<D>::NT], RowsState<D>& r,
+__device__ __forceinline__ void rw_softmax(RowsWeights<D>& P, RowsScores<D>& s, RowsState<D>& r,
                                            const AttnArgs& a, int tok, bool masked, int lane) {
   using S = RowsShape<D>;
   const int h = lane >> 5;
@@ -182,7 +188,7 @@ __device__ __forceinline__ void rw_softmax(kv_u4 (&P)[2 * RowsShape<D>::NT], at_
 // products of the weights of tile tok with its values
 // noted: the tile's values that were not finite and have been taken out, or NULL
 template <int D, bool BF>
-__device__ __forceinline__ void rw_products(RowsState<D>& r, const kv_u4 (&P)[2 * RowsShape<D>::NT], const AttnArgs& a,
+__device__ __forceinline__ void rw_products(RowsState<D>& r, const RowsWeights<D>& P, const AttnArgs& a,
                                             const char* vals, int tok, const uint8_t* noted, int lane) {
   using S = RowsShape<D>;
   int vb = rw_val_byte<D>(lane);
@@ -230,34 +236,46 @@ __device__ __forceinline__ void rw_products(RowsState<D>& r, const kv_u4 (&P)[2 
   }
 }
 
+// A block of the call.  Longest first: the last block of every (entry, kv head), then
+// the one before, ...; kv heads fastest, so that with 8 of them (or a multiple) a
+// head's blocks meet its tokens in one XCD's L2.
+template <int D> struct RowsBlock {
+  using S = RowsShape<D>;
+  int head, rb, total, r0, nrows, pe, p0, p1, parts;  // rb < 0: none; parts that share its tiles
+  KvEntry e;
+  TileRange<S::KT> tr;
+  __device__ __forceinline__ RowsBlock(const AttnArgs& a, int id) : tr(-1, -1, 0, 0) {
+    head = id % a.c.kv_heads;
+    const int back = id / (a.c.kv_heads * a.b.n);
+    e = kv_entry(a.c, a.b, (id / a.c.kv_heads) % a.b.n);
+    total = e.rows * a.G;
+    rb = (total + S::BM - 1) / S::BM - 1 - back;
+    if (rb < 0) return;
+    r0 = rb * S::BM, nrows = min(total - r0, S::BM);
+    pe = e.len - e.rows;
+    p0 = pe + r0 / a.G, p1 = pe + (r0 + nrows - 1) / a.G;
+    tr = TileRange<S::KT>(p0, p1, a.window, a.sinks);
+    parts = max(min(a.splits, tr.n / RW_MIN_TILES), 1);
+  }
+};
+
 template <int D, bool BF>
-__global__ __launch_bounds__(64 * RowsShape<D>::NW) __attribute__((amdgpu_waves_per_eu(RowsShape<D>::NW / 4)))
+__global__ __launch_bounds__(64 * ROWS_WAVES) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2)))
 void k_attn_rows(AttnArgs a) {
   using S = RowsShape<D>;
   __shared__ __align__(1024) char keys[S::NB * S::bytes];
   __shared__ __align__(1024) char vals[S::NB * S::bytes];
   __shared__ __align__(16) uint8_t notes[S::bytes / 8];
-  __shared__ int odd_at, flag;
+  __shared__ int odd_at;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5, col = lane & 31;
 
-  // the blocks of the call, longest first: the last block of every (entry, kv
-  // head), then the one before, ...; kv heads fastest, so that with 8 of them (or
-  // a multiple) a head's blocks meet its tokens in one XCD's L2
-  int id = blockIdx.x;
-  const int z = id % a.splits;
-  id /= a.splits;
-  const int head = id % a.c.kv_heads, j = (id / a.c.kv_heads) % a.b.n, back = id / (a.c.kv_heads * a.b.n);
-  const KvEntry e = kv_entry(a.c, a.b, j);
-  const int total = e.rows * a.G;
-  const int rb = (total + S::BM - 1) / S::BM - 1 - back;
-  if (rb < 0) return;
-  const int r0 = rb * S::BM, nrows = min(total - r0, S::BM);
-  const int pe = e.len - e.rows;
-  const int p0 = pe + r0 / a.G, p1 = pe + (r0 + nrows - 1) / a.G;
-  const TileRange<S::KT> tr(p0, p1, a.window, a.sinks);
-  const int parts = max(min(a.splits, tr.n / RW_MIN_TILES), 1);
-  if (z >= parts) return;
+  const RowsBlock<D> blk(a, blockIdx.x / a.splits);
+  const int z = blockIdx.x % a.splits;
+  if (blk.rb < 0 || z >= blk.parts) return;
+  const KvEntry& e = blk.e;
+  const TileRange<S::KT>& tr = blk.tr;
+  const int head = blk.head, total = blk.total, r0 = blk.r0, pe = blk.pe, p0 = blk.p0, p1 = blk.p1, parts = blk.parts;
   const int t0 = (int)((int64_t)tr.n * z / parts), t1 = (int)((int64_t)tr.n * (z + 1) / parts);
   const int32_t* table = a.c.tables + (int64_t)e.slot * a.c.max_pages;
 
@@ -336,16 +354,12 @@ void k_attn_rows(AttnArgs a) {
     return notes;
   };
 
-  // The tiles.  Waves w and w + 4 share a SIMD, so the first four and the last four
-  // run half a step apart: while one does matrix products (values of tile t, keys of
-  // tile t + 1), the other does the exponentials of a tile.  Two barriers a step:
-  //   bound(t):  keys t and values t - 1 are there
-  //              early waves: products t - 1, scores t    late waves: send t, softmax t - 1
-  //   barrier
-  //              early waves: send t, softmax t           late waves: products t - 1, scores t
-  // send t: the copies of keys t + AHEAD and values t + AHEAD - 1, into the buffers that
-  // tile t - 1 has left.
-  const bool late = S::NW == 8 && wave >= 4;
+  // The tiles, one barrier each.
+  //   bound(t):  keys t and values t - 1 are there, and every wave is done with step t - 1
+  //              products t - 1, scores t
+  //              send t: the copies of keys t + AHEAD and values t + AHEAD - 1, into the
+  //              buffers that tile t - 1 has left
+  //              softmax t
   at_f16 s[S::NT];
   kv_u4 P[2 * S::NT];
   const uint8_t* noted = nullptr;
@@ -396,26 +410,18 @@ void k_attn_rows(AttnArgs a) {
 #pragma unroll
     for (int t = -S::AHEAD; t < 0; ++t) send(t);
     bound(0);
-    if (late) {
-      send(0);
-      rw_barrier();
-    }
-    // a wave without rows only copies and keeps step
+    // (a wave without rows only copies and keeps step)
     if (alive) rw_scores<D, BF>(s, r, key_buf(0), lane);
     for (int t = 0; t < nt; ++t) {
-      if (late) bound(t + 1);
-      else if constexpr (S::NW == 8) rw_barrier();
-      send(late ? t + 1 : t);
+      send(t);
       if (alive) rw_softmax<D, BF>(P, s, r, a, token(t), t < wclear0 || t >= wclear1, lane);
-      if (!late) bound(t + 1);
-      else rw_barrier();
+      bound(t + 1);
       if (!alive) continue;
       __builtin_amdgcn_s_setprio(1);  // a product is one issue in eight: let it have it
       rw_products<D, BF>(r, P, a, val_buf(t), token(t), noted, lane);
       if (t + 1 < nt) rw_scores<D, BF>(s, r, key_buf(t + 1), lane);
       __builtin_amdgcn_s_setprio(0);
     }
-    if (S::NW == 8 && !late) rw_barrier();
   }
 
   r.l += __shfl_xor(r.l, 32);
@@ -431,7 +437,7 @@ void k_attn_rows(AttnArgs a) {
     }
     return;
   }
-  // several workgroups share the block: the last to arrive joins their partials in order
+  // several workgroups share the block: k_attn_rows_join puts their partials together
   const auto rs = at_slots(a.partial, a.partial_floats);
   const uint32_t slot = blockIdx.x * (uint32_t)rows_slot(D), row = wave * 32 + col;
   if (live) {
@@ -442,10 +448,22 @@ void k_attn_rows(AttnArgs a) {
         at_st4(rs, slot + row * D + x * 32 + 2 * i + 4 * h, at_f4{r.O[x][i], r.O[x][i + 1], r.O[x][i + 2], r.O[x][i + 3]});
     if (h == 0) at_st2(rs, slot + S::BM * D + 2 * row, r.m * a.scale_log2, r.l);
   }
-  if (!at_last(a.counters + blockIdx.x / a.splits, parts, &flag)) return;
-  at_join<BF, D, 64 * S::NW>(a, rs, e, head, r0, nrows, S::BM, parts, reinterpret_cast<float*>(keys),
-                 reinterpret_cast<float*>(keys) + AT_JOIN_CAP, reinterpret_cast<float*>(vals),
-                 [&](int k) { return (blockIdx.x - z + k) * (uint32_t)rows_slot(D); });
+}
+
+// The blocks that several workgroups have shared, eight rows to a workgroup: a launch
+// of its own, for one workgroup per block (the last to arrive) would have to read all
+// of a block's partials alone (64 parts of 80 rows: 97 us where the tokens take 20).
+constexpr int RJ_ROWS = 8, RJ_THREADS = 256;
+template <int D, bool BF> __global__ __launch_bounds__(RJ_THREADS) void k_attn_rows_join(AttnArgs a) {
+  using S = RowsShape<D>;
+  __shared__ __align__(16) float lds[3 * AT_JOIN_CAP];
+  constexpr int PER = S::BM / RJ_ROWS;
+  const RowsBlock<D> b(a, blockIdx.x / PER);
+  const int f0 = (blockIdx.x % PER) * RJ_ROWS;
+  if (b.rb < 0 || b.parts == 1 || f0 >= b.nrows) return;
+  at_join<BF, D, RJ_THREADS>(a, at_slots(a.partial, a.partial_floats), b.e, b.head, b.r0, f0, min(b.nrows - f0, RJ_ROWS), S::BM,
+                             b.parts, lds, lds + AT_JOIN_CAP, lds + 2 * AT_JOIN_CAP,
+                             [&](int k) { return (blockIdx.x / PER * a.splits + k) * (uint32_t)rows_slot(D); });
 }
 
 }  // namespace qg

@@ -474,7 +474,7 @@ void k_attn_step(AttnArgs a) {
     // several workgroups share (entry, head): the last to arrive joins them, in list order
     const int w0 = tile0 / per, parts = (tile0 + nt - 1) / per - w0 + 1;
     if (!at_last(a.counters + j * heads + head, parts, flag)) continue;
-    at_join<BF, D, 64 * NW>(a, rs, e, head, 0, nrows, MT * 16, parts, buf, buf + AT_JOIN_CAP, buf + 2 * AT_JOIN_CAP, [&](int k) {
+    at_join<BF, D, 64 * NW>(a, rs, e, head, 0, 0, nrows, MT * 16, parts, buf, buf + AT_JOIN_CAP, buf + 2 * AT_JOIN_CAP, [&](int k) {
       return (uint32_t)(2 * (w0 + k) + (k == 0 ? 1 : 0)) * (uint32_t)step_slot(MT, D);
     });
     __syncthreads();  // the join's use of the buffer is over

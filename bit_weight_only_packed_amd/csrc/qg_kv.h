@@ -119,11 +119,10 @@ constexpr int STEP_MIN_RUN = 12;
 __host__ __device__ constexpr size_t step_slot(int MT, int D) { return (size_t)MT * 16 * (D + 2); }
 hipError_t launch_attn_step(const AttnArgs& a, int D, bool bf16, int MT, hipStream_t st);
 
-// the many-row kernel: waves of a workgroup (wide heads need a SIMD's registers for
-// one wave), rows of a block, fp32 words of a partial
-__host__ __device__ constexpr int rows_waves(int D) { return D == 256 ? 4 : 8; }
-__host__ __device__ constexpr int rows_block(int D) { return 32 * rows_waves(D); }
-__host__ __device__ constexpr size_t rows_slot(int D) { return (size_t)rows_block(D) * (D + 2); }
+// the many-row kernel: waves of a workgroup, rows of a block (32 a wave), fp32 words of
+// its partial
+constexpr int ROWS_WAVES = 4, ROWS_BLOCK = 32 * ROWS_WAVES;
+__host__ __device__ constexpr size_t rows_slot(int D) { return (size_t)ROWS_BLOCK * (D + 2); }
 hipError_t launch_attn_rows(const AttnArgs& a, int D, bool bf16, unsigned blocks, hipStream_t st);
 hipError_t attn_step_allow_lds();
 

@@ -158,7 +158,7 @@ qg_status qgkv_create(qg_kv_handle* out, const qg_kv_desc* d, void* stream) {
   const size_t step = (size_t)2 * h->cus * step_slot(step_max_rows(d->head_dim) / 16, d->head_dim);
   const size_t rows = (size_t)kRowsSlots * rows_slot(d->head_dim);
   const size_t entries = (size_t)std::max(d->pages, d->max_seqs);
-  h->ncounters = (std::max(d->max_seqs * d->kv_heads, kRowsSlots) + 3) / 4 * 4;
+  h->ncounters = (d->max_seqs * d->kv_heads + 3) / 4 * 4;
   hipStream_t st = (hipStream_t)stream;
   h->partial_floats = std::max(step, rows);
   if (hipMalloc(&h->partial, h->partial_floats * sizeof(float)) != hipSuccess ||
@@ -284,7 +284,7 @@ qg_status qgkv_attend(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const
     return done(h, launch_attn_step(a, D, bf16, MT, st), st);
   }
   // a call of few blocks is split over the tokens until it covers the chip
-  const int64_t blocks = (rows + rows_block(D) - 1) / rows_block(D) * a.b.n * a.c.kv_heads;
+  const int64_t blocks = (rows + ROWS_BLOCK - 1) / ROWS_BLOCK * a.b.n * a.c.kv_heads;
   a.splits = (int)std::max<int64_t>(1, kRowsSlots / blocks);
   if (blocks * a.splits >= (int64_t)1 << 31) return fail(QG_ERR_UNSUPPORTED, "%lld blocks in one call", (long long)blocks);
   return done(h, launch_attn_rows(a, D, bf16, (unsigned)blocks, st), st);
