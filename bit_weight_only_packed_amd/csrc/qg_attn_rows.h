@@ -1,13 +1,25 @@
 // qg_attn_rows.h -- attention of many rows over a paged cache: prompts, chunks of
 // prompts behind a history, and verify batches too wide for the few-row kernel.
 //
-// Bound.  4 D flops per visible (row, q head, token) on the matrix cores.
+// Bound.  4 D flops per visible (row, q head, token) on the matrix cores, and one
+// exponential per 4 D flops beside them.  8,191 prompt tokens, 40 q and 8 kv heads of
+// 128 (687 GFLOP): 691 us, 994 TFLOP/s, where the card's best fp16 matrix product
+// reaches 1,154; the last 4,096 rows of 16,411 tokens through a window of 2,048 with 8
+// sinks (bf16, 172 GFLOP): 217 us, 793 TFLOP/s.
 //
 // A block is 32 rows per wave of one (entry, kv head): row r is new token r / G, q
 // head r % G of the group, so the q heads that share a kv head share its tokens,
 // and a block spans few positions (little is computed past the diagonal).  Tokens
 // come in tiles of KT, keys and values straight from memory into LDS (no registers),
 // the next tiles on their way while one is computed.
+//
+// Four waves make a block, two blocks share a CU, and each runs at its own pace: one's
+// exponentials fall beside the other's products.  Against one block of eight waves per
+// CU, four of them half a step behind the other four (8,191 tokens: 702 against 691 us):
+// half the rows per block waste less on short prompts, 47 against 33 us at 1,024 tokens,
+// 96 against 59 at 16 prompts of 1 to 1,901
+// tokens with 16 heads of 64.  Heads of 256 need all of a SIMD's
+// registers for one wave: one block a CU.
 //
 //   scores   S^T = K Q^T on 32x32x16 (A: keys from LDS, B: q from registers).  A
 //            lane holds 16 tokens of one row per 32, as token 8 (i / 4) + 4 h + i % 4
@@ -27,10 +39,12 @@
 
 namespace qg {
 
-constexpr int RW_MIN_TILES = 8;     // tiles of a split at least
+// tiles of a split at least: a part costs its rows' partials, 4 D bytes each to write and
+// to read, and its turn of the pipeline's start
+constexpr int RW_MIN_TILES = 8;
 constexpr float RW_SLACK = 8.0f;    // exponent that a weight may reach
 // operands read from LDS ahead of the product that takes them (an LDS round trip is
-// some 100 cycles, a product 32), and the scheduler's names of the two
+// some 100 cycles, a product 32; 8,191 tokens at 4, 6 and 8: level within 1 %), and the scheduler's names of the two
 constexpr int RW_DEEP = 6;
 constexpr int RW_MFMA = 0x8, RW_DS_READ = 0x100;
 
@@ -452,7 +466,8 @@ void k_attn_rows(AttnArgs a) {
 
 // The blocks that several workgroups have shared, eight rows to a workgroup: a launch
 // of its own, for one workgroup per block (the last to arrive) would have to read all
-// of a block's partials alone (64 parts of 80 rows: 97 us where the tokens take 20).
+// of a block's partials alone.  16 new rows of 40 heads behind 8,192 tokens: 40 us
+// against 97; a prompt of 1,024 tokens: 33 against 94.
 constexpr int RJ_ROWS = 8, RJ_THREADS = 256;
 template <int D, bool BF> __global__ __launch_bounds__(RJ_THREADS) void k_attn_rows_join(AttnArgs a) {
   using S = RowsShape<D>;

@@ -28,13 +28,24 @@
 // waves every NW-th tile of a run's part.  An (entry, kv head) that one workgroup
 // covers is finished there; one that several cover is joined by the last of them
 // to arrive, from partials in a fixed order.
+//
+// Measured, 40 q and 8 kv heads of 128, fp16, where the card's large read reaches 5.7
+// TB/s: one row of 131,071 tokens 104 us (537 MB, 5.2 TB/s); of 48 sequences of 3 to
+// 24,577 tokens each (bf16) 110 us (578 MB, 5.3 TB/s); 8 rows each of sequences of 4,100
+// and 12,290 38 us (67 MB, 1.8 TB/s: three row tiles' exponentials and products per
+// read); one row of 1,025 tokens 12.8 us, a chain of some eight memory round trips
+// (entry, table, keys, join).  16 q and 2 kv heads of 256, 32 sequences, window 4,096:
+// 50 us (204 MB, 4.1 TB/s).
 #pragma once
 #include "qg_attn.h"
 
 namespace qg {
 
 constexpr int ST_TK = 32;  // tokens of a tile
-constexpr int ST_COST = 16;  // tiles that beginning and ending an (entry, kv head) is worth
+// Tiles that beginning and ending an (entry, kv head) is worth: without it a workgroup
+// whose run holds many short sequences ends last (48 sequences of 3 to 24,577 tokens, 8
+// kv heads of 128, an (entry, kv head) counted as its tiles alone: 384 us; at 16: 109).
+constexpr int ST_COST = 16;
 
 template <int D, int MT = 1> struct StepShape {
   static constexpr int NW = step_waves(MT, D);   // waves of a workgroup

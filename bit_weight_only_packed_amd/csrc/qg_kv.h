@@ -97,9 +97,9 @@ struct AttnArgs {
   int G;               // q heads per kv head
   float scale_log2;    // scale * log2(e)
   int window, sinks;   // window 0: none
-  float* partial;      // see the kernels
+  float* partial;      // partials of work that several workgroups share (o, max, sum of a row)
   size_t partial_floats;
-  int* counters;       // zero between launches
+  int* counters;       // few rows: arrivals at a shared (entry, kv head), zero between launches
   int workers;         // few rows: workgroups that share the tiles,
   int min_run;         // and places of their list that each takes at least
   int splits;          // many rows: workgroups that may share a block's tiles

@@ -30,7 +30,8 @@ struct qg_kv {
 namespace {
 
 constexpr int kMaxPages = 1 << 20;
-constexpr int kRowsSlots = 512;  // (block, split) pairs of a split many-row call
+// (block, split) pairs of a split many-row call: two workgroups for each of 256 CUs
+constexpr int kRowsSlots = 512;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -264,6 +265,9 @@ qg_status qgkv_attend(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const
   if (window < 0 || sinks < 0) return fail(QG_ERR_INVALID_ARG, "window = %d, sinks = %d: negative", window, sinks);
   a.G = q_heads / a.c.kv_heads;
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  if (!std::isfinite(a.scale_log2)) return fail(QG_ERR_INVALID_ARG, "scale = %g is too large", scale);
+  if ((a.b.rows > 1 && a.out.row < h->d.head_dim) || (q_heads > 1 && a.out.head < h->d.head_dim))
+    return fail(QG_ERR_INVALID_ARG, "out: strides %lld, %lld: rows or heads overlap", (long long)a.out.row, (long long)a.out.head);
   a.window = window;
   a.sinks = sinks;
   a.partial = h->partial;
