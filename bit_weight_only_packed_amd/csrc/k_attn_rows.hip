@@ -19,6 +19,11 @@ template <int D> hipError_t go(const AttnArgs& a, bool bf16, unsigned blocks, hi
 
 }  // namespace
 
+int rows_parts(int D, int cap, int splits1) {
+  const int kt = D == 256 ? RowsShape<256>::KT : RowsShape<128>::KT;
+  return rw_parts((cap + kt - 1) / kt, splits1);
+}
+
 hipError_t launch_attn_rows(const AttnArgs& a, int D, bool bf16, unsigned blocks, hipStream_t st) {
   if (D == 64) return go<64>(a, bf16, blocks, st);
   if (D == 128) return go<128>(a, bf16, blocks, st);

@@ -13,13 +13,14 @@
 // come in tiles of KT, keys and values straight from memory into LDS (no registers),
 // the next tiles on their way while one is computed.
 //
-// Four waves make a block, two blocks share a CU, and each runs at its own pace: one's
-// exponentials fall beside the other's products.  Against one block of eight waves per
-// CU, four of them half a step behind the other four (8,191 tokens: 702 against 691 us):
-// half the rows per block waste less on short prompts, 47 against 33 us at 1,024 tokens,
-// 96 against 59 at 16 prompts of 1 to 1,901
-// tokens with 16 heads of 64.  Heads of 256 need all of a SIMD's
-// registers for one wave: one block a CU.
+// Four waves make a block; two blocks share a CU (three with heads of 64) and each runs
+// at its own pace: one's exponentials fall beside the other's products.  Against one
+// block of eight waves per CU, four of them half a step behind the other four (8,191
+// tokens: 702 against 691 us): half the rows per block waste less on short prompts, 47
+// against 33 us at 1,024 tokens.  Three blocks against two with heads of 64: 16 prompts of
+// 1 to 1,901 tokens 52 against 60 us, 8,192 tokens 176 against 183.  Two against one, which
+// would have had registers to spare, with heads of 256: 8,192 tokens 661 against 898 us
+// (with two, q and the sums leave some 60 of 256 registers, and what spills is q).
 //
 //   scores   S^T = K Q^T on 32x32x16 (A: keys from LDS, B: q from registers).  A
 //            lane holds 16 tokens of one row per 32, as token 8 (i / 4) + 4 h + i % 4
@@ -39,13 +40,22 @@
 
 namespace qg {
 
-// tiles of a split at least: a part costs its rows' partials, 4 D bytes each to write and
-// to read, and its turn of the pipeline's start
-constexpr int RW_MIN_TILES = 8;
+// Tiles of a part at least, of a block that several workgroups share: a part costs its
+// rows' partials, 4 D bytes each to write and to read, and its turn of the pipeline's
+// start.  The first where CUs would else have no workgroup (splits1 parts give each one),
+// the second for what a second workgroup of a CU brings over one (2 prompts of 1,500 rows
+// of 3,000 tokens, 8 q heads of 128 and one kv head: 67 us unshared, 76 at 23 tiles a part).
+constexpr int RW_MIN_TILES = 8, RW_LONG_TILES = 32;
+__host__ __device__ constexpr int rw_parts(int tiles, int splits1) {
+  const int few = tiles / RW_MIN_TILES < splits1 ? tiles / RW_MIN_TILES : splits1;
+  return few > tiles / RW_LONG_TILES ? few : tiles / RW_LONG_TILES;
+}
 constexpr float RW_SLACK = 8.0f;    // exponent that a weight may reach
-// operands read from LDS ahead of the product that takes them (an LDS round trip is
-// some 100 cycles, a product 32; 8,191 tokens at 4, 6 and 8: level within 1 %), and the scheduler's names of the two
-constexpr int RW_DEEP = 6;
+// operands read from LDS ahead of the product that takes them: 4 where there are
+// registers for them (8,191 tokens, heads of 128: 691 us at 4, 689 at 2, 728 at 1), 1 where
+// there are none (8,192 tokens, 16 q and 4 kv heads of 256: 661 us at 1, 685 at 2, 742 at
+// 3); and the scheduler's names of the two instructions
+template <int D> constexpr int RW_DEEP = D == 256 ? 1 : 4;
 constexpr int RW_MFMA = 0x8, RW_DS_READ = 0x100;
 
 template <int D> struct RowsShape {
@@ -58,10 +68,7 @@ template <int D> struct RowsShape {
   static constexpr int bytes = KT * D * 2;  // a tile's keys (or values)
   static constexpr int LD = bytes / 1024 / NW;  // 1 KiB copies per wave of them
   static constexpr int RW = KT / NW;        // tokens that a wave copies (they lie in one page)
-  // tiles of keys, and of values, in LDS: two where two workgroups share a CU, four
-  // where the registers leave room for one
-  static constexpr int NB = D < 256 ? 2 : 4;
-  static constexpr int AHEAD = NB - 1;      // a tile's copies go out this many tiles before its use
+  static constexpr int NB = 2;              // tiles of keys, and of values, in LDS
   static_assert(RW <= 16, "a wave's tokens of a tile lie in one page");
 };
 
@@ -127,24 +134,24 @@ __device__ __forceinline__ void rw_scores(RowsScores<D>& s, const RowsState<D>& 
   using S = RowsShape<D>;
   int kb = rw_key_byte<D>(lane);
   asm volatile("" : "+v"(kb));  // one instruction per read, not a register each: they are needed
-  constexpr int N = S::NT * (D / 16);
+  constexpr int N = S::NT * (D / 16), DEEP = RW_DEEP<D>;
   const auto key = [&](int i) {  // column step i / NT, 32-token group i % NT
     return *reinterpret_cast<const kv_u4*>(keys + (kb ^ ((i / S::NT) << 5)) + (i % S::NT) * 32 * D * 2);
   };
   kv_u4 K[N];
 #pragma unroll
-  for (int i = 0; i < RW_DEEP; ++i) K[i] = key(i);
+  for (int i = 0; i < DEEP; ++i) K[i] = key(i);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    if (i + RW_DEEP < N) K[i + RW_DEEP] = key(i + RW_DEEP);
+    if (i + DEEP < N) K[i + DEEP] = key(i + DEEP);
     at_f16& x = s[i % S::NT];
     x = at_mfma32<BF>(K[i], r.Q[i / S::NT], i < S::NT ? at_f16{} : x);
   }
-  __builtin_amdgcn_sched_group_barrier(RW_DS_READ, RW_DEEP, 0);
+  __builtin_amdgcn_sched_group_barrier(RW_DS_READ, DEEP, 0);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     __builtin_amdgcn_sched_group_barrier(RW_MFMA, 1, 0);
-    if (i + RW_DEEP < N) __builtin_amdgcn_sched_group_barrier(RW_DS_READ, 1, 0);
+    if (i + DEEP < N) __builtin_amdgcn_sched_group_barrier(RW_DS_READ, 1, 0);
   }
 }
 
@@ -210,24 +217,24 @@ __device__ __forceinline__ void rw_products(RowsState<D>& r, const RowsWeights<D
   const auto val = [&](int x, int k, int b) {  // 32-column group x, 16-token step k, tokens 8 b ..
     return rw_read_tr(vals + (vb ^ (x << 6) ^ (b << 5)) + (16 * k + 8 * b) * D * 2);
   };
-  constexpr int N = S::ND * 2 * S::NT;
+  constexpr int N = S::ND * 2 * S::NT, DEEP = RW_DEEP<D>;
   const auto op = [&](int i) {  // 16-token step i / ND, column group i % ND
     const kv_u2 v0 = val(i % S::ND, i / S::ND, 0), v1 = val(i % S::ND, i / S::ND, 1);
     return kv_u4{v0.x, v0.y, v1.x, v1.y};
   };
   kv_u4 V[N];
 #pragma unroll
-  for (int i = 0; i < RW_DEEP; ++i) V[i] = op(i);
+  for (int i = 0; i < DEEP; ++i) V[i] = op(i);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    if (i + RW_DEEP < N) V[i + RW_DEEP] = op(i + RW_DEEP);
+    if (i + DEEP < N) V[i + DEEP] = op(i + DEEP);
     r.O[i % S::ND] = at_mfma32<BF>(V[i], P[i / S::ND], r.O[i % S::ND]);
   }
-  __builtin_amdgcn_sched_group_barrier(RW_DS_READ, 2 * RW_DEEP, 0);
+  __builtin_amdgcn_sched_group_barrier(RW_DS_READ, 2 * DEEP, 0);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     __builtin_amdgcn_sched_group_barrier(RW_MFMA, 1, 0);
-    if (i + RW_DEEP < N) __builtin_amdgcn_sched_group_barrier(RW_DS_READ, 2, 0);
+    if (i + DEEP < N) __builtin_amdgcn_sched_group_barrier(RW_DS_READ, 2, 0);
   }
   if (__builtin_expect(noted != nullptr, 0)) {
     // [token][16-byte chunk] bytes of noted +inf or NaN, then of -inf or NaN
@@ -269,12 +276,12 @@ template <int D> struct RowsBlock {
     pe = e.len - e.rows;
     p0 = pe + r0 / a.G, p1 = pe + (r0 + nrows - 1) / a.G;
     tr = TileRange<S::KT>(p0, p1, a.window, a.sinks);
-    parts = max(min(a.splits, tr.n / RW_MIN_TILES), 1);
+    parts = max(min(a.splits, rw_parts(tr.n, a.splits1)), 1);
   }
 };
 
 template <int D, bool BF>
-__global__ __launch_bounds__(64 * ROWS_WAVES) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2)))
+__global__ __launch_bounds__(64 * ROWS_WAVES) __attribute__((amdgpu_waves_per_eu(D == 64 ? 3 : 2)))
 void k_attn_rows(AttnArgs a) {
   using S = RowsShape<D>;
   __shared__ __align__(1024) char keys[S::NB * S::bytes];
@@ -284,8 +291,12 @@ void k_attn_rows(AttnArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5, col = lane & 31;
 
-  const RowsBlock<D> blk(a, blockIdx.x / a.splits);
-  const int z = blockIdx.x % a.splits;
+  // parts slowest: the workgroups past a block's parts come last, and the CUs between
+  // those that work do not wait for them (the last 16 rows of 16,384 tokens: 29 us against
+  // 36 with parts fastest)
+  const unsigned blocks = gridDim.x / (unsigned)a.splits;
+  const int z = blockIdx.x / blocks;
+  const RowsBlock<D> blk(a, blockIdx.x - z * blocks);
   if (blk.rb < 0 || z >= blk.parts) return;
   const KvEntry& e = blk.e;
   const TileRange<S::KT>& tr = blk.tr;
@@ -371,8 +382,8 @@ void k_attn_rows(AttnArgs a) {
   // The tiles, one barrier each.
   //   bound(t):  keys t and values t - 1 are there, and every wave is done with step t - 1
   //              products t - 1, scores t
-  //              send t: the copies of keys t + AHEAD and values t + AHEAD - 1, into the
-  //              buffers that tile t - 1 has left
+  //              send t: the copies of keys t + 1 and values t, into the buffers that
+  //              tile t - 1 has left
   //              softmax t
   at_f16 s[S::NT];
   kv_u4 P[2 * S::NT];
@@ -400,29 +411,25 @@ void k_attn_rows(AttnArgs a) {
     at_id = kv_table(table, min(at_tok, p1) >> a.c.page_shift);
   };
   const auto send = [&](int t) {
-    const int to = (t + S::AHEAD) & (S::NB - 1), to1 = (t + S::AHEAD - 1) & (S::NB - 1);
+    const int to = (t + 1) & (S::NB - 1), to1 = t & (S::NB - 1);
     const char* const from = pool0 + kv_page(a.c, at_id) * page_bytes + (at_tok & mask) * (D * 2);
-    if (t + S::AHEAD < nt)
+    if (t + 1 < nt)
 #pragma unroll
       for (int i = 0; i < S::LD; ++i) rw_copy(from, kofs[i], keys + to * S::bytes + (wave * S::LD + i) * 1024);
-    if (t + S::AHEAD > 0 && t + S::AHEAD - 1 < nt)
+    if (t >= 0)
 #pragma unroll
       for (int i = 0; i < S::LD; ++i) rw_copy(before + v_bytes, vofs[i], vals + to1 * S::bytes + (wave * S::LD + i) * 1024);
     before = from;
-    look(t + S::AHEAD + 1);
+    look(t + 2);
   };
   const auto bound = [&](int t) {
-    // this wave's copies of keys t and values t - 1 have landed: where the AHEAD - 1
-    // sends since were whole, all but theirs; near the end, all
-    if (t + S::AHEAD <= nt) __builtin_amdgcn_s_waitcnt(at_wait_vm((S::AHEAD - 1) * 2 * S::LD));
-    else __builtin_amdgcn_s_waitcnt(at_wait_vm(0));
+    __builtin_amdgcn_s_waitcnt(at_wait_vm(0));  // this wave's copies of keys t and values t - 1 have landed
     rw_barrier();  // everyone's have, and the buffers of the tile before are free
     noted = t > 0 ? mend(t - 1, val_buf(t - 1)) : nullptr;
   };
   if (nt > 0) {
     look(0);
-#pragma unroll
-    for (int t = -S::AHEAD; t < 0; ++t) send(t);
+    send(-1);
     bound(0);
     // (a wave without rows only copies and keeps step)
     if (alive) rw_scores<D, BF>(s, r, key_buf(0), lane);
@@ -466,19 +473,20 @@ void k_attn_rows(AttnArgs a) {
 
 // The blocks that several workgroups have shared, eight rows to a workgroup: a launch
 // of its own, for one workgroup per block (the last to arrive) would have to read all
-// of a block's partials alone.  16 new rows of 40 heads behind 8,192 tokens: 40 us
-// against 97; a prompt of 1,024 tokens: 33 against 94.
+// of a block's partials alone.  The last 16 rows of 16,384 tokens, 40 q and 8 kv heads of
+// 128: 40 us against 97 in the same parts; a prompt of 1,024 tokens: 33 against 94.
 constexpr int RJ_ROWS = 8, RJ_THREADS = 256;
 template <int D, bool BF> __global__ __launch_bounds__(RJ_THREADS) void k_attn_rows_join(AttnArgs a) {
   using S = RowsShape<D>;
   __shared__ __align__(16) float lds[3 * AT_JOIN_CAP];
   constexpr int PER = S::BM / RJ_ROWS;
-  const RowsBlock<D> b(a, blockIdx.x / PER);
+  const unsigned id = blockIdx.x / PER, blocks = gridDim.x / PER;
+  const RowsBlock<D> b(a, id);
   const int f0 = (blockIdx.x % PER) * RJ_ROWS;
   if (b.rb < 0 || b.parts == 1 || f0 >= b.nrows) return;
   at_join<BF, D, RJ_THREADS>(a, at_slots(a.partial, a.partial_floats), b.e, b.head, b.r0, f0, min(b.nrows - f0, RJ_ROWS), S::BM,
                              b.parts, lds, lds + AT_JOIN_CAP, lds + 2 * AT_JOIN_CAP,
-                             [&](int k) { return (blockIdx.x / PER * a.splits + k) * (uint32_t)rows_slot(D); });
+                             [&](int k) { return (k * blocks + id) * (uint32_t)rows_slot(D); });
 }
 
 }  // namespace qg

@@ -102,7 +102,7 @@ struct AttnArgs {
   int* counters;       // few rows: arrivals at a shared (entry, kv head), zero between launches
   int workers;         // few rows: workgroups that share the tiles,
   int min_run;         // and places of their list that each takes at least
-  int splits;          // many rows: workgroups that may share a block's tiles
+  int splits, splits1; // many rows: workgroups that may share a block's tiles, however many it has; and if few
 };
 
 // rows of one kv head that the few-row kernel takes: (new rows) * (q heads per
@@ -123,6 +123,8 @@ hipError_t launch_attn_step(const AttnArgs& a, int D, bool bf16, int MT, hipStre
 // its partial
 constexpr int ROWS_WAVES = 4, ROWS_BLOCK = 32 * ROWS_WAVES;
 __host__ __device__ constexpr size_t rows_slot(int D) { return (size_t)ROWS_BLOCK * (D + 2); }
+// parts of a block that sees every token of a slot that holds cap
+int rows_parts(int D, int cap, int splits1);
 hipError_t launch_attn_rows(const AttnArgs& a, int D, bool bf16, unsigned blocks, hipStream_t st);
 hipError_t attn_step_allow_lds();
 

@@ -30,7 +30,8 @@ struct qg_kv {
 namespace {
 
 constexpr int kMaxPages = 1 << 20;
-// (block, split) pairs of a split many-row call: two workgroups for each of 256 CUs
+// (block, part) pairs of a many-row call whose blocks are shared: two workgroups for each
+// of 256 CUs where the parts are long, one where they are short
 constexpr int kRowsSlots = 512;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -287,9 +288,13 @@ qg_status qgkv_attend(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const
     a.min_run = STEP_MIN_RUN;
     return done(h, launch_attn_step(a, D, bf16, MT, st), st);
   }
-  // a call of few blocks is split over the tokens until it covers the chip
+  // A call of few blocks is split over the tokens until it covers the chip: once for parts
+  // of few tiles, twice for parts of many (the last 512 rows of 65,536 tokens, 40 q and 8
+  // kv heads of 128: 741 us with two, 1,507 with one; the last 16 of each of 4 slots of
+  // 8,192: 53 and 47).  A cache whose slots hold too little for parts saves the join.
   const int64_t blocks = (rows + ROWS_BLOCK - 1) / ROWS_BLOCK * a.b.n * a.c.kv_heads;
-  a.splits = (int)std::max<int64_t>(1, kRowsSlots / blocks);
+  a.splits1 = (int)std::max<int64_t>(1, kRowsSlots / 2 / blocks);
+  a.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kRowsSlots / blocks, rows_parts(D, a.c.cap, a.splits1)));
   if (blocks * a.splits >= (int64_t)1 << 31) return fail(QG_ERR_UNSUPPORTED, "%lld blocks in one call", (long long)blocks);
   return done(h, launch_attn_rows(a, D, bf16, (unsigned)blocks, st), st);
 }
