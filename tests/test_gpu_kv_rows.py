@@ -42,6 +42,11 @@ def test_joins_through_windows(D, window, sinks):
     run(Pair([2100, 150], "bf16", 16, 1, D), [90, 150], 1, window=window, sinks=sinks)
 
 
+def test_many_parts():
+    """One block of a long slot: over a hundred parts, more of them than a wave has lanes."""
+    run(Pair([70001], "f16", 256, 1, 64), [35], 2)
+
+
 @pytest.mark.parametrize("heads", [1, 3, 8])
 def test_block_order_covers_every_head_and_entry(heads):
     run(Pair([65, 1, 130, 258], "f16", 16, heads, 64), [65, 1, 130, 129], 1)
