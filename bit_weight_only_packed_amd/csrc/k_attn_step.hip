@@ -7,7 +7,7 @@ namespace {
 
 template <int D, bool BF, int MT> hipError_t go(const AttnArgs& a, hipStream_t st) {
   const size_t lds = StepShape<D, MT>::lds + step_list_bytes(a.b.n);
-  k_attn_step<D, BF, MT><<<(unsigned)a.workers, 64 * step_waves(MT, D), lds, st>>>(a);
+  k_attn_step<D, BF, MT><<<(unsigned)a.workers, 64 * step_waves(D), lds, st>>>(a);
   return hipGetLastError();
 }
 
@@ -16,10 +16,10 @@ template <int D, int MT> hipError_t by_type(const AttnArgs& a, bool bf16, hipStr
 }
 
 template <int D> hipError_t by_rows(const AttnArgs& a, bool bf16, int MT, hipStream_t st) {
-  if (MT == 1) return by_type<D, 1>(a, bf16, st);
-  if (MT == 2) return by_type<D, 2>(a, bf16, st);
-  if constexpr (step_max_rows(D) > 32) return MT == 3 ? by_type<D, 3>(a, bf16, st) : by_type<D, 4>(a, bf16, st);
-  return hipErrorInvalidValue;
+  if constexpr (step_max_rows(D) > 16) {
+    if (MT == 2) return by_type<D, 2>(a, bf16, st);
+  }
+  return by_type<D, 1>(a, bf16, st);
 }
 
 template <int D, bool BF, int MT> hipError_t allow() {
@@ -44,14 +44,9 @@ hipError_t attn_step_allow_lds() {
   };
   both(allow<64, false, 1>, allow<64, true, 1>);
   both(allow<64, false, 2>, allow<64, true, 2>);
-  both(allow<64, false, 3>, allow<64, true, 3>);
-  both(allow<64, false, 4>, allow<64, true, 4>);
   both(allow<128, false, 1>, allow<128, true, 1>);
   both(allow<128, false, 2>, allow<128, true, 2>);
-  both(allow<128, false, 3>, allow<128, true, 3>);
-  both(allow<128, false, 4>, allow<128, true, 4>);
   both(allow<256, false, 1>, allow<256, true, 1>);
-  both(allow<256, false, 2>, allow<256, true, 2>);
   return e;
 }
 

@@ -4,7 +4,7 @@
 // Bound.  Every cached token's key and value are read once per kv head,
 // 4 D bytes, for 4 D G R flops (G q heads per kv head, R new rows: 5 to 160 at
 // the shapes met) -- HBM, with matrix-core work to spare.  So the G * R rows that
-// share a kv head are packed into tiles of 16 (MT of them, up to 64 rows) and
+// share a kv head are packed into tiles of 16 (MT of them, one or two) and
 // all served by one read of the tokens, and the kernel is built to keep reads in
 // flight.
 //
@@ -30,12 +30,10 @@
 // to arrive, from partials in a fixed order.
 //
 // Measured, 40 q and 8 kv heads of 128, fp16, where the card's large read reaches 5.7
-// TB/s: one row of 131,071 tokens 104 us (537 MB, 5.2 TB/s); of 48 sequences of 3 to
-// 24,577 tokens each (bf16) 110 us (578 MB, 5.3 TB/s); 8 rows each of sequences of 4,100
-// and 12,290 38 us (67 MB, 1.8 TB/s: three row tiles' exponentials and products per
-// read); one row of 1,025 tokens 12.8 us, a chain of some eight memory round trips
-// (entry, table, keys, join).  16 q and 2 kv heads of 256, 32 sequences, window 4,096:
-// 50 us (204 MB, 4.1 TB/s).
+// TB/s: one row of 131,071 tokens 103 us (537 MB, 5.2 TB/s); of 48 sequences of 3 to
+// 24,577 tokens each (bf16) 108 us (578 MB, 5.3 TB/s); one row of 1,025 tokens 11 to 13
+// us, a chain of some eight memory round trips (entry, table, keys, join).  16 q and 2 kv
+// heads of 256, 32 sequences, window 4,096: 50 us (204 MB, 4.1 TB/s).
 #pragma once
 #include "qg_attn.h"
 
@@ -48,17 +46,14 @@ constexpr int ST_TK = 32;  // tokens of a tile
 constexpr int ST_COST = 16;
 
 template <int D, int MT = 1> struct StepShape {
-  static constexpr int NW = step_waves(MT, D);   // waves of a workgroup
+  static constexpr int NW = step_waves(D);       // waves of a workgroup
   static constexpr int VE = D / 16;              // columns of a lane
   static constexpr int VB = D == 64 ? 8 : 16;    // bytes of a lane's value load
   static constexpr int VL = VE * 2 / VB;         // value loads per token
   static constexpr int LD = D + 4;               // padded row of the cross-wave buffer (floats)
   static constexpr int NB = VL * 16;             // bytes of noted values per token (one per value load)
   static constexpr size_t notes = (size_t)NW * 2 * ST_TK * NB;
-  // q in LDS, where two waves per SIMD have no registers left for it
-  static constexpr bool QL = MT == 3;
-  static constexpr size_t q = QL ? (size_t)MT * 16 * D * 2 : 0;
-  static constexpr size_t lds = (size_t)NW * 16 * LD * 4 + NW * 16 * 8 + notes + q + 64;
+  static constexpr size_t lds = (size_t)NW * 16 * LD * 4 + NW * 16 * 8 + notes + 64;
   static_assert(NW * 16 * LD >= 3 * AT_JOIN_CAP && LD * 4 * 16 >= ST_TK * D * 2, "what shares the buffer");
 };
 
@@ -158,7 +153,7 @@ template <int D> __device__ __forceinline__ int step_col(int q, int i, int x) {
 }
 
 template <int D, bool BF, int MT>
-__global__ __launch_bounds__(64 * step_waves(MT, D)) __attribute__((amdgpu_waves_per_eu(step_waves(MT, D) / 4)))
+__global__ __launch_bounds__(64 * step_waves(D)) __attribute__((amdgpu_waves_per_eu(step_waves(D) / 4)))
 void k_attn_step(AttnArgs a) {
   using S = StepShape<D, MT>;
   constexpr int NW = S::NW;
@@ -166,8 +161,7 @@ void k_attn_step(AttnArgs a) {
   float* buf = reinterpret_cast<float*>(smem);                                    // [wave][16][LD]
   float* ml = buf + NW * 16 * S::LD;                                              // [wave][16][2]
   uint8_t* notes = reinterpret_cast<uint8_t*>(ml + NW * 16 * 2);                  // [wave][2][32][NB]
-  char* const qs = reinterpret_cast<char*>(notes + S::notes);                     // [16 MT][D], QL only
-  int* flag = reinterpret_cast<int*>(qs + S::q);                                  // [16]
+  int* flag = reinterpret_cast<int*>(notes + S::notes);                           // [16]
   KvEntry* list = reinterpret_cast<KvEntry*>(flag + 16);                          // [n]
   int* pre = reinterpret_cast<int*>(list + a.b.n);                                // [n + 1]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -245,30 +239,20 @@ void k_attn_step(AttnArgs a) {
     const int32_t* table = a.c.tables + (int64_t)e.slot * a.c.max_pages;
 
     // the rows of this kv head: row r is new token r / G, q head head * G + r % G
-    const auto q_at = [&](int r, int chunk) {
-      const int i = r / a.G;
-      return *reinterpret_cast<const kv_u4*>(a.q.ptr + (int64_t)(e.row0 + i) * a.q.row +
-                                             (int64_t)(head * a.G + r - i * a.G) * a.q.head + chunk * 8);
-    };
-    kv_u4 Q[S::QL ? 1 : MT][D / 32];
+    kv_u4 Q[MT][D / 32];
     int pos[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       const int r = mt * 16 + col;
       const bool live = r < nrows;
-      pos[mt] = live ? p0 + r / a.G : -1;
-      if constexpr (!S::QL) {
+      const int ri = live ? r / a.G : 0;
+      pos[mt] = live ? p0 + ri : -1;
+      const uint16_t* qp = a.q.ptr + (int64_t)(e.row0 + ri) * a.q.row +
+                           (int64_t)(head * a.G + (live ? r - ri * a.G : 0)) * a.q.head + q * 8;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          Q[mt][c] = q_at(live ? r : 0, 4 * c + q);
-          if (!live) Q[mt][c] = kv_u4{0, 0, 0, 0};
-        }
-      }
-    }
-    if constexpr (S::QL) {
-      for (int x = tid; x < MT * 16 * (D / 8); x += 64 * NW) {
-        const int r = x / (D / 8), c = x % (D / 8);
-        *reinterpret_cast<kv_u4*>(qs + (r * (D / 8) + (c ^ step_swz<D>(r & 15))) * 16) = r < nrows ? q_at(r, c) : kv_u4{0, 0, 0, 0};
+      for (int c = 0; c < D / 32; ++c) {
+        Q[mt][c] = *reinterpret_cast<const kv_u4*>(qp + 32 * c);
+        if (!live) Q[mt][c] = kv_u4{0, 0, 0, 0};
       }
     }
     at_f4 O[MT][S::VE];
@@ -313,11 +297,7 @@ void k_attn_step(AttnArgs a) {
         for (int mt = 0; mt < MT; ++mt) {
           s[mt][h] = at_f4{0, 0, 0, 0};
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            // (row mt * 16 + col of q lies in LDS as token col of a tile's half)
-            const kv_u4 B = S::QL ? *reinterpret_cast<const kv_u4*>(qs + (kb ^ (c << 6)) + mt * 16 * D * 2) : Q[S::QL ? 0 : mt][c];
-            s[mt][h] = at_mfma16<BF>(K[c], B, s[mt][h]);
-          }
+          for (int c = 0; c < D / 32; ++c) s[mt][h] = at_mfma16<BF>(K[c], Q[mt][c], s[mt][h]);
         }
       }
       // the reads have returned before the next tile's copy may overwrite what they read

@@ -105,11 +105,18 @@ struct AttnArgs {
   int splits, splits1; // many rows: workgroups that may share a block's tiles, however many it has; and if few
 };
 
-// rows of one kv head that the few-row kernel takes: (new rows) * (q heads per
-// kv head); wide heads hold fewer for lack of registers
-__host__ __device__ constexpr int step_max_rows(int D) { return D == 256 ? 32 : 64; }
+// Rows of one kv head that the few-row kernel takes, (new rows) * (q heads per kv head).
+// us of the few-row and of the many-row kernel, fp16, 8 kv heads of 128 (2 of 256):
+//   rows          one slot of 8,192   8 of 2,048     16 of 8,192
+//   25            25.9 / 24.7         27.7 / 31.6    107.7 / 116.5
+//   32            26.7 / 25.3         28.1 / 32.3    108.5 / 120.5
+//   45            33.7 / 27.1         34.5 / 33.5    117.4 / 121.2
+//   64            54.4 / 27.7         47.1 / 35.5    128.2 / 126.2
+//   16, heads 256 28.0 / 32.1         27.7 / 35.0    66.4 / 95.0
+//   32, heads 256 50.3 / 33.4         44.4 / 36.9    87.2 / 97.7
+__host__ __device__ constexpr int step_max_rows(int D) { return D == 256 ? 16 : 32; }
 // waves of a workgroup, one workgroup per CU: two waves per SIMD where the registers allow
-__host__ __device__ constexpr int step_waves(int MT, int D) { return D < 256 && MT * D <= 384 ? 8 : 4; }
+__host__ __device__ constexpr int step_waves(int D) { return D == 256 ? 4 : 8; }
 // Places of the list that a workgroup takes at least.  One request of 1,025 tokens, 40
 // q and 8 kv heads of 128: 13.4 us at 8, 13.1 at 12, 13.8 at 16, 16.0 at 24, 21.1 at 48
 // (fewer, longer runs save joins and cost round trips); from a few thousand tokens on
