@@ -69,7 +69,7 @@ def test_heads_and_pages(heads, page):
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("R,G", [(2, 5), (4, 4), (8, 4), (8, 5), (8, 8), (13, 5), (16, 8), (32, 5), (3, 64)])
 def test_verify_rows(D, R, G):
-    """Verify batches over both kernels (up to 64 or 32 rows of a kv head, and more)."""
+    """Verify batches over both kernels (up to 32 or 16 rows of a kv head, and more)."""
     run(Pair([R, R + 1, 50 + R, 301], "f16", 16, 2, D), [R] * 4, G, uniform=True)
 
 
