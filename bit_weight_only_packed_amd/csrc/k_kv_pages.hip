@@ -28,14 +28,14 @@ hipError_t launch_kv_compact(const KvPool& p, int cus, hipStream_t st) {
   return hipGetLastError();
 }
 
-hipError_t launch_kv_append(const KvDev& c, const KvBatchDev& b, const KvRows& k, const KvRows& v, int D,
-                            hipStream_t st) {
+hipError_t launch_kv_append(const KvDev& c, const KvBatchDev& b, const KvRows& k, const KvRows& v, const int32_t* refused,
+                            const int32_t* info, int D, hipStream_t st) {
   const int64_t items = (int64_t)b.max_rows * 2 * c.kv_heads;
   const int per = 256 / (D / 8);  // items of a workgroup
   const dim3 grid((unsigned)std::min<int64_t>((items + per - 1) / per, 4096), (unsigned)b.n);
-  if (D == 64) k_kv_append<64><<<grid, 256, 0, st>>>(c, b, k, v);
-  else if (D == 128) k_kv_append<128><<<grid, 256, 0, st>>>(c, b, k, v);
-  else k_kv_append<256><<<grid, 256, 0, st>>>(c, b, k, v);
+  if (D == 64) k_kv_append<64><<<grid, 256, 0, st>>>(c, b, k, v, refused, info);
+  else if (D == 128) k_kv_append<128><<<grid, 256, 0, st>>>(c, b, k, v, refused, info);
+  else k_kv_append<256><<<grid, 256, 0, st>>>(c, b, k, v, refused, info);
   return hipGetLastError();
 }
 

@@ -77,8 +77,9 @@ struct KvPool {
   int32_t *tables, *lens, *refs, *info;
   int64_t page_bytes;
   int pages, max_seqs, max_pages, page_shift;
-  // workspace: [0] copies to make, [1] first id that moves (compact), then the
-  // lists of source and destination pages and the moved pages' new ids
+  // workspace: [0] copies to make, [1] first id that moves (compact), [2] the bit of info
+  // that the last extend was refused with (0: it was granted), then the lists of source
+  // and destination pages and the moved pages' new ids
   int32_t* head;
   int32_t *from, *to, *place;
 };
@@ -87,7 +88,9 @@ hipError_t launch_kv_fork(const KvPool& p, const int32_t* src, const int32_t* ds
 hipError_t launch_kv_trim(const KvPool& p, const int32_t* seqs, const int32_t* keep, int n, hipStream_t st);
 hipError_t launch_kv_extend(const KvPool& p, const int32_t* n_new, int cus, hipStream_t st);
 hipError_t launch_kv_compact(const KvPool& p, int cus, hipStream_t st);
-hipError_t launch_kv_append(const KvDev& c, const KvBatchDev& b, const KvRows& k, const KvRows& v, int D, hipStream_t st);
+// refused, info: KvPool's head + 2 and info
+hipError_t launch_kv_append(const KvDev& c, const KvBatchDev& b, const KvRows& k, const KvRows& v, const int32_t* refused,
+                            const int32_t* info, int D, hipStream_t st);
 
 // ---- attention ---------------------------------------------------------------
 struct AttnArgs {

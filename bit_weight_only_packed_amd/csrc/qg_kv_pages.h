@@ -146,6 +146,7 @@ __global__ __launch_bounds__(KV_PLAN) void k_kv_extend(KvPool p, const int32_t* 
   if (__syncthreads_or(too_long)) {
     if (s == 0) {
       p.head[0] = 0;
+      p.head[2] = 2;
       atomicOr(p.info, 2);
     }
     return;
@@ -168,6 +169,7 @@ __global__ __launch_bounds__(KV_PLAN) void k_kv_extend(KvPool p, const int32_t* 
   if (found < total) {
     if (s == 0) {
       p.head[0] = 0;
+      p.head[2] = 1;
       p.info[1] = total - found;
       atomicOr(p.info, 1);
     }
@@ -181,7 +183,10 @@ __global__ __launch_bounds__(KV_PLAN) void k_kv_extend(KvPool p, const int32_t* 
     }
     p.lens[s] = (int)grown;
   }
-  if (s == 0) p.head[0] = copies;
+  if (s == 0) {
+    p.head[0] = copies;
+    p.head[2] = 0;
+  }
   // page k of the list belongs to the last slot whose run starts at or before it
   // (a slot that takes none starts where the next one does, so the last is the taker)
   for (int k = s; k < total; k += KV_PLAN) {
@@ -292,8 +297,13 @@ __global__ __launch_bounds__(256) void k_kv_copy(KvPool p) {
 // or of v, 16 bytes a lane.  blockIdx.y is the entry.  16,383 tokens of 8 heads of 128:
 // 32 us (134 MB read and written, 4.2 TB/s); one token of each of 64 slots: 3.5 us, the
 // launch and three dependent loads (length, table, key).
+// Nothing is written while a refused extend stands: the lengths have not grown, so the
+// rows would take the places of tokens that the slots, or others through shared pages,
+// hold.
 template <int D>
-__global__ __launch_bounds__(256) void k_kv_append(KvDev c, KvBatchDev b, KvRows k, KvRows v) {
+__global__ __launch_bounds__(256) void k_kv_append(KvDev c, KvBatchDev b, KvRows k, KvRows v, const int32_t* refused,
+                                                   const int32_t* info) {
+  if (*refused & *info) return;
   const KvEntry e = kv_entry(c, b, blockIdx.y);
   const int per = 2 * c.kv_heads;  // (k or v, head) pairs of a row
   const uint32_t items = (uint32_t)e.rows * per;  // below 2^31 (checked on the host)

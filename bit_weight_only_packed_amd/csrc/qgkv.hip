@@ -171,8 +171,9 @@ qg_status qgkv_create(qg_kv_handle* out, const qg_kv_desc* d, void* stream) {
   }
   if (s == QG_OK && attn_step_allow_lds() != hipSuccess)
     s = fail(QG_ERR_DEVICE, "cannot raise the LDS limit of the kernels");
-  if (s == QG_OK && launch_fill_zero(h->counters, (int64_t)h->ncounters * sizeof(int), st) != hipSuccess)
-    s = fail(QG_ERR_DEVICE, "counter initialisation failed");
+  if (s == QG_OK && (launch_fill_zero(h->counters, (int64_t)h->ncounters * sizeof(int), st) != hipSuccess ||
+                     launch_fill_zero(h->lists, 4 * sizeof(int32_t), st) != hipSuccess))
+    s = fail(QG_ERR_DEVICE, "workspace initialisation failed");
   if (hipStreamSynchronize(st) != hipSuccess && s == QG_OK) s = fail(QG_ERR_DEVICE, "stream synchronisation failed");
   if (s != QG_OK) {
     free_kv(h);
@@ -249,7 +250,7 @@ qg_status qgkv_append(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const
   if ((int64_t)bd.max_rows * 2 * c.kv_heads >= (int64_t)1 << 31)
     return fail(QG_ERR_UNSUPPORTED, "%d rows of %d heads in one call", bd.max_rows, c.kv_heads);
   hipStream_t st = (hipStream_t)stream;
-  return done(h, launch_kv_append(c, bd, kr, vr, h->d.head_dim, st), st);
+  return done(h, launch_kv_append(c, bd, kr, vr, h->pool.head + 2, h->pool.info, h->d.head_dim, st), st);
 }
 
 qg_status qgkv_attend(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const qg_kv_rows* q, const qg_kv_rows* out,

@@ -197,7 +197,10 @@ class KVCache:
         return seqs, row_start
 
     def extend(self, n_new, stream=None) -> None:
-        """Room for n_new[s] more tokens in every slot s; lens grow by them."""
+        """Room for n_new[s] more tokens in every slot s; lens grow by them.  Refused
+        on the device if pages are short or a slot would be too long: then nothing
+        changes, and appends write nothing until an extend is granted or ``check``
+        has been called."""
         st = self._on(stream)
         n_new = self._index("n_new", n_new, self.max_seqs, stream)
         self._call("extend", n_new.data_ptr(), st)

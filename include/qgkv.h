@@ -124,8 +124,10 @@ qg_status qgkv_destroy(qg_kv_handle h);
  * first, slots in order.  A partly filled last page that another slot also
  * names is first copied to a fresh page (all layers) -- unless every slot that
  * names it grows in this call, where the lowest of them keeps it.  All or
- * nothing: if pages are short or a table is too small, nothing changes and
- * info says so. */
+ * nothing: if pages are short or a table is too small, nothing changes, info
+ * says so, and qgkv_append on this handle writes nothing until an extend is
+ * granted or the caller has cleared that bit of info[0].  (qgkv_attend computes
+ * as ever, from the lengths that stand.) */
 qg_status qgkv_extend(qg_kv_handle h, const int32_t* n_new, void* stream);
 
 /* dst[i] becomes a second name of src[i]'s tokens: same pages, refs + 1, no
@@ -145,7 +147,8 @@ qg_status qgkv_trim(qg_kv_handle h, const int32_t* seqs, const int32_t* keep, in
 qg_status qgkv_compact(qg_kv_handle h, void* stream);
 
 /* Write the rows' keys and values of one layer into their pages: k and v are
- * [rows][kv_heads][head_dim]. */
+ * [rows][kv_heads][head_dim].  Writes nothing while a refused qgkv_extend
+ * stands (see there): the rows' places are then other tokens'. */
 qg_status qgkv_append(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const qg_kv_rows* k, const qg_kv_rows* v,
                       void* stream);
 

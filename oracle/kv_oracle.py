@@ -35,6 +35,7 @@ class Cache:
         self.pool, self.tables = np.array(pool), np.array(tables)
         self.lens, self.refs = np.array(lens), np.array(refs)
         self.info = [0, 0, 0, 0]
+        self.refused = 0  # the bit that the last extend was refused with
         self.P = self.pool.shape[4]
 
     def used(self, s: int, length=None) -> int:
@@ -50,6 +51,8 @@ class Cache:
         return np.concatenate([p.transpose(1, 0, 2) for p in pages])[:n]
 
     def append(self, layer: int, slots, rows, k, v):
+        if self.refused & self.info[0]:
+            return
         at = 0
         for s, r in zip(slots, rows):
             for i in range(r):
@@ -77,6 +80,7 @@ class Cache:
         slots = range(len(self.lens))
         if any(int(self.lens[s]) + n_new[s] > self.tables.shape[1] * self.P for s in slots):
             self.info[0] |= LONG
+            self.refused = LONG
             return
         # slots that would write into a page that others name too
         tail = {s: int(self.tables[s, self.used(s) - 1]) for s in slots if n_new[s] > 0 and self.lens[s] % self.P != 0}
@@ -92,7 +96,9 @@ class Cache:
         if total > len(free):
             self.info[0] |= SHORT
             self.info[1] = total - len(free)
+            self.refused = SHORT
             return
+        self.refused = 0
         for s in slots:
             if s in copies:
                 p = free.pop(0)

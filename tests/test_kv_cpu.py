@@ -171,3 +171,19 @@ def test_extend_counts_what_is_short():
     assert c.info[:2] == [KO.SHORT, 3 + 1 - 1] and list(c.lens) == [5, 8]
     c.extend([100, 0])
     assert c.info[0] == KO.SHORT | KO.LONG
+
+
+def test_append_after_a_refused_extend():
+    c = _cache([5, 8], pages=5)
+    before = c.pool.copy()
+    k = np.ones((2, 1, 2))
+    c.extend([12, 4])
+    c.append(0, [0, 1], [1, 1], k, k)
+    assert np.array_equal(before, c.pool)
+    c.extend([1, 0])
+    c.append(0, [0], [1], k[:1], k[:1])
+    assert list(c.lens) == [6, 8] and (c.tokens(0, 0, 0)[5] == 1).all()
+    c.extend([12, 4])
+    c.info[0] = 0
+    c.append(0, [1], [1], k[:1], k[:1])
+    assert (c.tokens(1, 0, 0)[7] == 1).all()
