@@ -132,7 +132,7 @@ __device__ __forceinline__ bool at_last(int* counter, int n, int* flag) {
 template <bool BF, int N>
 __device__ __forceinline__ void at_store(const AttnArgs& a, const KvEntry& e, int head, int r, int c, const float* o, float L) {
   const int i = r / a.G;
-  const float inv = L != 0.0f ? 1.0f / L : (e.len - e.rows + i < 0 ? 0.0f : __builtin_nanf(""));
+  const float inv = L != 0.0f ? 1.0f / L : (e.pos + i < 0 ? 0.0f : __builtin_nanf(""));
   uint16_t* to = const_cast<uint16_t*>(a.out.ptr) + (int64_t)(e.row0 + i) * a.out.row +
                  (int64_t)(head * a.G + r - i * a.G) * a.out.head + c;
   uint32_t w[N / 2];
@@ -242,7 +242,7 @@ __device__ __forceinline__ void at_join(const AttnArgs& a, __amdgpu_buffer_rsrc_
 template <int TK> struct TileRange {
   int ns, skip, n;
   __device__ __forceinline__ TileRange(int p0, int p1, int window, int sinks) {
-    const int end = (p1 + TK) / TK;  // p1 >= -1
+    const int end = (p1 + TK) / TK;  // p1 < 0: none (0 or less)
     const int lo = window ? max(max(p0, 0) - window + 1, 0) / TK : 0;
     ns = window ? min((min(sinks, p1 + 1) + TK - 1) / TK, end) : 0;
     skip = max(lo - ns, 0);

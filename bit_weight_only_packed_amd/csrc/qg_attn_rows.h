@@ -273,7 +273,7 @@ template <int D> struct RowsBlock {
     rb = (total + S::BM - 1) / S::BM - 1 - back;
     if (rb < 0) return;
     r0 = rb * S::BM, nrows = min(total - r0, S::BM);
-    pe = e.len - e.rows;
+    pe = e.pos;
     p0 = pe + r0 / a.G, p1 = pe + (r0 + nrows - 1) / a.G;
     tr = TileRange<S::KT>(p0, p1, a.window, a.sinks);
     parts = max(min(a.splits, rw_parts(tr.n, a.splits1)), 1);

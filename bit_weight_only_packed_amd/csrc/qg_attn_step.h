@@ -57,7 +57,7 @@ template <int D, int MT = 1> struct StepShape {
   static_assert(NW * 16 * LD >= 3 * AT_JOIN_CAP && LD * 4 * 16 >= ST_TK * D * 2, "what shares the buffer");
 };
 
-// the call's list in LDS: an entry's slot, length, first row and rows, and its places
+// the call's list in LDS: an entry's slot, position, first row and rows, and its places
 // in the list before it (n + 1 of these)
 constexpr size_t step_list_bytes(int n) { return (size_t)n * 16 + ((size_t)n + 1) * 4; }
 
@@ -184,7 +184,7 @@ void k_attn_step(AttnArgs a) {
       if (j < n) {
         const KvEntry e = kv_entry(a.c, a.b, j);
         list[j] = e;
-        if (e.rows > 0) t = ST_COST + max(TileRange<ST_TK>(e.len - e.rows, e.len - 1, a.window, a.sinks).n, 1);
+        if (e.rows > 0) t = ST_COST + max(TileRange<ST_TK>(e.pos, e.pos + e.rows - 1, a.window, a.sinks).n, 1);
       }
       int x = t;
 #pragma unroll
@@ -232,9 +232,9 @@ void k_attn_step(AttnArgs a) {
     u = tile0 + nt;
     if (t0 >= t1) continue;  // the run ends before its first tile
     KvEntry e = list[j];
-    e.slot = __builtin_amdgcn_readfirstlane(e.slot), e.len = __builtin_amdgcn_readfirstlane(e.len);
+    e.slot = __builtin_amdgcn_readfirstlane(e.slot), e.pos = __builtin_amdgcn_readfirstlane(e.pos);
     e.row0 = __builtin_amdgcn_readfirstlane(e.row0), e.rows = __builtin_amdgcn_readfirstlane(e.rows);
-    const int p0 = e.len - e.rows, p1 = e.len - 1, nrows = e.rows * a.G;
+    const int p0 = e.pos, p1 = p0 + e.rows - 1, nrows = e.rows * a.G;
     const TileRange<ST_TK> tr(p0, p1, a.window, a.sinks);
     const int32_t* table = a.c.tables + (int64_t)e.slot * a.c.max_pages;
 

@@ -33,26 +33,28 @@ struct KvBatchDev {
   int n, rows, max_rows;     // entries, rows in all, rows of an entry at most
 };
 
-// entry j of a call: slot, length, first row, rows.  Everything that comes from
-// device memory is cut to what the cache and the call's operands hold.
+// entry j of a call: slot, position of its first row, first row, rows.  Everything that
+// comes from device memory is cut to what the cache and the call's operands hold.  Rows
+// past max_rows are left out, but count for the position: the others stand where they
+// would without the cut.
 struct KvEntry {
-  int slot, len, row0, rows;
+  int slot, pos, row0, rows;
 };
 __device__ __forceinline__ KvEntry kv_entry(const KvDev& c, const KvBatchDev& b, int j) {
   KvEntry e;
   int s = b.seqs ? b.seqs[j] : j;
   const bool ok = (unsigned)s < (unsigned)c.max_seqs;
   e.slot = ok ? s : 0;
-  const int len = c.lens[e.slot];
-  e.len = ok ? min(max(len, 0), c.cap) : 0;
+  const int l = c.lens[e.slot], len = ok ? min(max(l, 0), c.cap) : 0;
+  int rows = b.max_rows;
   if (b.row_start) {
     e.row0 = min(max(b.row_start[j], 0), b.rows);
-    const int end = min(max(b.row_start[j + 1], e.row0), b.rows);
-    e.rows = min(end - e.row0, b.max_rows);
+    rows = min(max(b.row_start[j + 1], e.row0), b.rows) - e.row0;
   } else {
     e.row0 = j * b.max_rows;
-    e.rows = b.max_rows;
   }
+  e.pos = len - rows;
+  e.rows = min(rows, b.max_rows);
   return e;
 }
 

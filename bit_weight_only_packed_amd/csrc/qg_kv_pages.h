@@ -312,7 +312,7 @@ __global__ __launch_bounds__(256) void k_kv_append(KvDev c, KvBatchDev b, KvRows
   for (uint32_t i = blockIdx.x * (256 / (D / 8)) + threadIdx.x / (D / 8); i < items;
        i += gridDim.x * (256 / (D / 8))) {
     const int row = (int)(i / per), w = (int)(i - (uint32_t)row * per);
-    const int pos = e.len - e.rows + row;
+    const int pos = e.pos + row;
     if (pos < 0) continue;
     const int id = table[pos >> c.page_shift];
     if ((unsigned)id >= (unsigned)c.pages) continue;

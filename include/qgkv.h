@@ -28,7 +28,8 @@
  * slot j) with R_j new rows, rows row_start[j] .. row_start[j + 1] - 1 of the
  * call's `rows` rows (NULL: rows / n each).  They are the LAST R_j tokens of the
  * slot, whose length already counts them: row i stands at position
- * p = lens - R_j + i.  seqs and row_start are device memory and may change
+ * p = lens - R_j + i (of more than max_rows rows the later ones are left out:
+ * not written, no output; the others keep their positions).  seqs and row_start are device memory and may change
  * between replays of a captured call.  A slot index out of range acts as an
  * empty slot.  A row at a position before 0 (an idle slot, length 0) is
  * not written by append and sees nothing in attend: its output is 0.
@@ -97,8 +98,8 @@ typedef struct {
 typedef struct {
   int32_t n;                /* entries, 1 .. max_seqs                                          */
   int32_t rows;             /* rows of the call over all entries, >= 1                         */
-  int32_t max_rows;         /* with row_start: at least the largest R_j (rows past it are left
-                               out); ignored without                                           */
+  int32_t max_rows;         /* with row_start: at least the largest R_j (an entry's rows past
+                               it are left out); ignored without                               */
   const int32_t* seqs;      /* device [n] or NULL                                              */
   const int32_t* row_start; /* device [n + 1], ascending from 0 to rows, or NULL               */
 } qg_kv_batch;

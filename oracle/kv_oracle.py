@@ -50,12 +50,12 @@ class Cache:
             return np.zeros((0,) + self.pool.shape[3:4] + self.pool.shape[5:], dtype=self.pool.dtype)
         return np.concatenate([p.transpose(1, 0, 2) for p in pages])[:n]
 
-    def append(self, layer: int, slots, rows, k, v):
+    def append(self, layer: int, slots, rows, k, v, max_rows=None):
         if self.refused & self.info[0]:
             return
         at = 0
         for s, r in zip(slots, rows):
-            for i in range(r):
+            for i in range(r if max_rows is None else min(r, max_rows)):
                 pos = int(self.lens[s]) - r + i
                 if pos >= 0:
                     page = self.tables[s, pos // self.P]

@@ -1,12 +1,13 @@
 """What calls on the cache refuse, leave out or leave alone."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from _kv import Pair, np64, rand  # noqa: E402
+from _kv import Pair, check_out, np64, rand  # noqa: E402
 import bit_weight_only_packed_amd as Q  # noqa: E402
 
 
@@ -74,3 +75,36 @@ def test_captured_steps_that_run_out_of_pages():
         p.ref.append(0, [0, 1], [1, 1], np64(k), np64(v))
         p.same_state()
     assert p.ref.info[0] and p.gpu.lens.tolist() == [32, 16]
+
+
+@pytest.mark.parametrize("most", [1, 3, 16, 40])
+def test_rows_past_max_rows_are_left_out(most):
+    """The others stand where they would: at len - R + i with all R rows counted, through both kernels."""
+    lens, rows, slots = [70, 9, 130], [50, 9, 41], [0, 1, 2]
+    p = Pair(lens, "f16", 16, 2, 64)
+    n, start = sum(rows), [0] + list(np.cumsum(rows))
+    k, v, q = rand((n, 2, 64), "f16", 5), rand((n, 2, 64), "f16", 6), rand((n, 4, 64), "f16", 7, 1.5)
+    kw = dict(seqs=ints(*slots), row_start=ints(*start), max_rows=most)
+    off = [r for a, b in zip(start, start[1:]) for r in range(a + most, b)]
+    for window, sinks in ((0, 0), (8, 2)):
+        ref = p.ref.attend(0, slots, rows, np64(q), 0.125, window, sinks)
+        out = torch.full_like(q, 7.0)
+        p.gpu.attend(q, window=window, sinks=sinks, out=out, **kw)
+        assert (out[off] == 7).all()
+        out[off] = torch.from_numpy(ref[off]).half().cuda()
+        check_out(out, ref, "f16", q, p, 0, slots, rows, 0.125)
+    p.gpu.append(k, v, **kw)
+    p.ref.append(0, slots, rows, np64(k), np64(v), max_rows=most)
+    p.same_state()
+
+
+def test_rows_past_max_rows_before_the_start():
+    """Rows that are left out count for the position also where that is before the first token."""
+    p = Pair([5, 40], "f16", 16, 1, 64)
+    q = rand((90, 2, 64), "f16", 7)
+    for most in (8, 40):
+        out = p.gpu.attend(q, seqs=ints(0, 1), row_start=ints(0, 45, 90), max_rows=most, out=torch.full_like(q, 7.0))
+        o = np64(out)
+        assert (o[:most] == 0).all()  # positions -40 ..
+        assert (o[45:50] == 0).all() and (o[50:45 + most] != 0).any(axis=(1, 2)).all()  # positions -5 ..
+        assert (o[most:45] == 7).all() and (o[45 + most:] == 7).all()
