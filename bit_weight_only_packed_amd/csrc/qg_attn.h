@@ -8,10 +8,18 @@
 // by 2^(m_old - m).  Partial results (o, m, l) of disjoint token ranges join as
 //   M = max m_i,  o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
 // A range in which a row sees nothing has m = -inf and contributes 0.
+//
+// Weights meet the values on the matrix cores as fp16 or bf16, one rounding each.  fp16
+// would lose those below 2^-14 of the largest bit by bit and those below 2^-25 whole:
+// behind one token that takes nearly all the weight (a sink with a value of 0) that can be
+// all of the output.  So in fp16 every weight, in o and in l alike, is larger by a fixed power
+// of two, which the division by l takes away again: the largest reach 2^AT_FP16_TOP.
 #pragma once
 #include "qg_kv.h"
 
 namespace qg {
+
+constexpr float AT_FP16_TOP = 15.0f;
 
 typedef _Float16 at_h8 __attribute__((ext_vector_type(8)));
 typedef __bf16 at_b8 __attribute__((ext_vector_type(8)));

@@ -33,8 +33,10 @@
 // read fall on distinct banks.
 //
 // The running maximum is raised, and what has been summed rescaled, only where a
-// row's new maximum is more than 2^8 above it in the exponent: weights stay below
-// 2^8, far inside fp16, and the rescaling of the accumulators almost never runs.
+// row's new maximum is more than RW_SLACK above it in the exponent, so the rescaling of
+// the accumulators almost never runs.  In fp16 that is 2^4 (level with 2^8 in time) and
+// weights are carried 2^11 times larger: up to 2^15, and only those below 2^-36 of the row's
+// largest are lost.
 #pragma once
 #include "qg_attn.h"
 
@@ -50,7 +52,10 @@ __host__ __device__ constexpr int rw_parts(int tiles, int splits1) {
   const int few = tiles / RW_MIN_TILES < splits1 ? tiles / RW_MIN_TILES : splits1;
   return few > tiles / RW_LONG_TILES ? few : tiles / RW_LONG_TILES;
 }
-constexpr float RW_SLACK = 8.0f;    // exponent that a weight may reach
+// the exponent that a weight may reach above the running maximum, and what is added to it
+// for the matrix cores' sake (AT_FP16_TOP)
+template <bool BF> constexpr float RW_SLACK = BF ? 8.0f : 4.0f;
+template <bool BF> constexpr float RW_BIAS = BF ? 0.0f : AT_FP16_TOP - RW_SLACK<BF>;
 // operands read from LDS ahead of the product that takes them: 4 where there are
 // registers for them (8,191 tokens, heads of 128: 691 us at 4, 689 at 2, 728 at 1), 1 where
 // there are none (8,192 tokens, 16 q and 4 kv heads of 256: 661 us at 1, 685 at 2, 742 at
@@ -178,7 +183,7 @@ __device__ __forceinline__ void rw_softmax(RowsWeights<D>& P, RowsScores<D>& s, 
     for (int i = g == 0 ? 1 : 0; i < 16; ++i) mx = fmaxf(mx, s[g][i]);
   mx = at_max32(mx);
   // (r.m = -inf, nothing seen yet: the difference is inf, or NaN where mx is -inf too)
-  if (__builtin_expect(__any((mx - r.m) * a.scale_log2 > RW_SLACK), 0)) {
+  if (__builtin_expect(__any((mx - r.m) * a.scale_log2 > RW_SLACK<BF>), 0)) {
     const float mn = fmaxf(r.m, mx);
     const float f = at_exp2((r.m - at_safe(mn)) * a.scale_log2);
     r.m = mn;
@@ -188,7 +193,7 @@ __device__ __forceinline__ void rw_softmax(RowsWeights<D>& P, RowsScores<D>& s, 
 #pragma unroll
       for (int i = 0; i < 16; ++i) r.O[x][i] *= f;
   }
-  float ms = at_safe(r.m) * a.scale_log2;
+  float ms = at_safe(r.m) * a.scale_log2 - RW_BIAS<BF>;
   // c s - ms, rounded once, is off by the rounding of ms: by 2^-5 at most below 2^20.  Scores so
   // large that it could overflow the weights are subtracted first (taken everywhere that
   // costs 8,191 tokens 709 against 694 us; the look costs nothing there).
@@ -197,7 +202,7 @@ __device__ __forceinline__ void rw_softmax(RowsWeights<D>& P, RowsScores<D>& s, 
     for (int g = 0; g < S::NT; ++g)
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[g][i] -= at_safe(r.m);
-    ms = 0.0f;
+    ms = -RW_BIAS<BF>;
   }
   float sum[2] = {0.0f, 0.0f};
 #pragma unroll

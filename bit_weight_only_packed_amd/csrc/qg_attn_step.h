@@ -44,6 +44,8 @@ constexpr int ST_TK = 32;  // tokens of a tile
 // whose run holds many short sequences ends last (48 sequences of 3 to 24,577 tokens, 8
 // kv heads of 128, an (entry, kv head) counted as its tiles alone: 384 us; at 16: 109).
 constexpr int ST_COST = 16;
+// added to a weight's exponent, at most 0, for the matrix cores' sake
+template <bool BF> constexpr float ST_BIAS = BF ? 0.0f : AT_FP16_TOP;
 
 template <int D, int MT = 1> struct StepShape {
   static constexpr int NW = step_waves(D);       // waves of a workgroup
@@ -337,7 +339,7 @@ void k_attn_step(AttnArgs a) {
         const float ms = at_safe(m[mt]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          x[i] = at_exp2(x[i] - ms);
+          x[i] = at_exp2((x[i] - ms) + ST_BIAS<BF>);
           l[mt] += x[i];
         }
 #pragma unroll

@@ -39,8 +39,10 @@
  * over the tokens t <= p that lie in the window, t > p - window (window 0: all),
  * or among the first `sinks`, t < sinks.  Scores, maxima, sums and outputs are
  * held in fp32; the weights exp(s_t - max) are rounded once to the cache's type
- * (relative error at most 2^-11, bf16 2^-8) to enter the matrix cores beside the values,
- * and the output is rounded once.  The sum is of the unrounded weights.
+ * to enter the matrix cores beside the values, and the output is rounded once.  The
+ * sum is of the unrounded weights.  A weight's rounding is off by 2^-11 of it (bf16 2^-8)
+ * or, if that is more, in fp16 by 2^-36 of the row's largest weight; fp16 weights are
+ * carried larger by a power of two for that, which the division takes away.
  * Tokens that a row does not see never reach it, whatever they hold (NaN,
  * infinities, memory never written).  A NaN or infinity that it sees makes its
  * output NaN (or infinite where IEEE arithmetic gives that).
