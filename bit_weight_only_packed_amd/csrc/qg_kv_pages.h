@@ -115,7 +115,8 @@ __global__ __launch_bounds__(KV_PLAN) void k_kv_extend(KvPool p, const int32_t* 
   const bool too_long = grown > ((int64_t)p.max_pages << p.page_shift);
   const int used = kv_used(len, p.page_shift);
   // more than the pool holds is short anyway (and 1024 of these stay below 2^31)
-  const int need = too_long ? 0 : min(kv_used((int)grown, p.page_shift) - used, p.pages + 1);
+  const int wanted = too_long ? 0 : kv_used((int)grown, p.page_shift) - used;  // at most 2^26
+  const int need = min(wanted, p.pages + 1);
   int32_t* table = p.tables + (int64_t)(slot ? s : 0) * p.max_pages;
   int tail = -1, holders = 0;
   if (add > 0 && (len & (P - 1)) != 0 && !too_long) {
@@ -151,7 +152,7 @@ __global__ __launch_bounds__(KV_PLAN) void k_kv_extend(KvPool p, const int32_t* 
     }
     return;
   }
-  // the lowest `total` free ids, ascending, into the list `to`
+  // the lowest `total` free ids, ascending, into the list `place`
   int found = 0;
   for (int i0 = 0; 4 * (int64_t)i0 < p.pages && found < total; i0 += KV_PLAN) {
     const int4 r = plan_refs(p, i0 + s);
@@ -167,10 +168,13 @@ __global__ __launch_bounds__(KV_PLAN) void k_kv_extend(KvPool p, const int32_t* 
   }
   __syncthreads();
   if (found < total) {
+    int lo, hi;  // of the pages wanted, all slots together
+    plan_scan((wanted & 0xFFFF) + copy, sums, &lo);
+    plan_scan(wanted >> 16, sums, &hi);
     if (s == 0) {
       p.head[0] = 0;
       p.head[2] = 1;
-      p.info[1] = total - found;
+      p.info[1] = (int)min<int64_t>(((int64_t)hi << 16) + lo - found, INT32_MAX);
       atomicOr(p.info, 1);
     }
     return;

@@ -108,3 +108,16 @@ def test_rows_past_max_rows_before_the_start():
         assert (o[:most] == 0).all()  # positions -40 ..
         assert (o[45:50] == 0).all() and (o[50:45 + most] != 0).any(axis=(1, 2)).all()  # positions -5 ..
         assert (o[most:45] == 7).all() and (o[45 + most:] == 7).all()
+
+
+@pytest.mark.parametrize("n_new", [[50, 0, 0], [1000, 7, 900], [0, 33, 0], [1 << 22, 1 << 22, 1 << 22]])
+def test_extend_says_how_many_pages_are_short(n_new):
+    """Also where one slot wants more than the whole pool."""
+    p = Pair([20, 3, 0], "f16", 16, 1, 64, extra=1, max_pages=1 << 20)
+    p.gpu.fork([0], [2])
+    p.ref.fork([0], [2])
+    p.gpu.extend(n_new)
+    p.ref.extend(n_new)
+    p.same_state()
+    assert p.gpu.info.tolist()[:2] == p.ref.info[:2] and p.ref.info[1] > 0
+    assert p.ref.info[1] > (3 * (1 << 18) - 2 if n_new[2] > 1000 else 0)
