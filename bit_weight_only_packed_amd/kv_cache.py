@@ -254,12 +254,18 @@ class KVCache:
         del held
         return out
 
-    def check(self) -> None:
+    def check(self, stream=None) -> None:
         """Raise if a call found something to refuse on the device since the last
-        check (waits for the GPU)."""
+        check.  Waits for the given stream, or for all work on the cache's GPU, and
+        returns after ``info`` has been cleared."""
         from . import QGError, QG_ERR_INVALID_ARG, QG_ERR_OOM
-        bits, short = self.info[:2].tolist()
-        self.info[:2] = 0
+        cuda = self._torch.cuda
+        with cuda.device(self._dev), _on(stream):
+            (cuda.synchronize if stream is None else stream.synchronize)()
+            bits, short = self.info[:2].tolist()
+            if bits or short:
+                self.info[:2] = 0
+                cuda.current_stream().synchronize()
         if bits & INFO_SHORT:
             raise QGError(QG_ERR_OOM, f"extend: {short} free pages short")
         if bits & INFO_LONG:

@@ -121,3 +121,21 @@ def test_extend_says_how_many_pages_are_short(n_new):
     p.same_state()
     assert p.gpu.info.tolist()[:2] == p.ref.info[:2] and p.ref.info[1] > 0
     assert p.ref.info[1] > (3 * (1 << 18) - 2 if n_new[2] > 1000 else 0)
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_check_waits_for_work_on_other_streams(given):
+    """An extend that is refused late, on a stream of its own, is found, and its bits are gone when check returns."""
+    kv = Q.KVCache(2, 16, 1, 64, max_seqs=1, max_pages=4)
+    n = ints(50)
+    for _ in range(2):
+        s, other = torch.cuda.Stream(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(100_000_000)
+        kv.extend(n, stream=s)
+        with pytest.raises(Q.QGError, match="2 free pages short"):
+            kv.check(stream=s if given else None)
+        with torch.cuda.stream(other):
+            assert kv.info.tolist()[:2] == [0, 0]
+        kv.check()
