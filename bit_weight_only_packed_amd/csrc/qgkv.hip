@@ -115,6 +115,40 @@ qg_status rows_of(const qg_kv_rows* r, const char* name, KvRows* out) {
   return QG_OK;
 }
 
+// Whether two of the D-element runs that begin at r * row + h * head (r < rows, h < heads)
+// and at those places + ofs share elements; with ofs 0 two runs of the same kind.
+bool runs_meet(int64_t row, int64_t head, int64_t rows, int64_t heads, int64_t D, int64_t ofs) {
+  if (ofs == 0 && rows > 1 && row < D) return true;
+  for (int64_t dh = 1 - heads; dh < heads; ++dh) {
+    if (ofs == 0 && dh == 0) continue;
+    const int64_t to = ofs + dh * head;  // less the dr rows that come nearest to it
+    const int64_t dr = row > 0 ? std::clamp(to / row, 1 - rows, rows - 1) : 0;
+    for (int64_t x = std::max(dr - 1, 1 - rows); x <= std::min(dr + 1, rows - 1); ++x)
+      if (std::abs(to - x * row) < D) return true;
+  }
+  return false;
+}
+
+// out [rows][heads][D] against itself and against q of the same shape.  What is plainly apart
+// is not looked into: rows that hold their heads, operands in different memory or in columns of
+// one tensor's rows.  (Operands of different strides that share memory are left to the caller.)
+qg_status check_overlap(const KvRows& q, const KvRows& out, int64_t rows, int64_t heads, int64_t D) {
+  const int64_t ow = (heads - 1) * out.head + D, qw = (heads - 1) * q.head + D;  // a row's extent
+  const bool nested = (heads == 1 || out.head >= D) && (rows == 1 || out.row >= ow);
+  if (!nested && runs_meet(out.row, out.head, rows, heads, D, 0))
+    return fail(QG_ERR_INVALID_ARG, "out: strides %lld, %lld: rows or heads overlap", (long long)out.row, (long long)out.head);
+  const int64_t ofs = (int64_t)((intptr_t)out.ptr - (intptr_t)q.ptr) / 2;
+  if (ofs >= (rows - 1) * q.row + qw || -ofs >= (rows - 1) * out.row + ow) return QG_OK;
+  if (rows > 1 && q.row == out.row && q.row > 0) {
+    const int64_t at = (ofs % q.row + q.row) % q.row;
+    if (at >= qw && at + ow <= q.row) return QG_OK;
+  }
+  if (ofs == 0 || ((rows == 1 || q.row == out.row) && (heads == 1 || q.head == out.head) &&
+                   runs_meet(q.row, q.head, rows, heads, D, ofs)))
+    return fail(QG_ERR_INVALID_ARG, "out overlaps q");
+  return QG_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -268,8 +302,8 @@ qg_status qgkv_attend(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const
   a.G = q_heads / a.c.kv_heads;
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
   if (!std::isfinite(a.scale_log2)) return fail(QG_ERR_INVALID_ARG, "scale = %g is too large", scale);
-  if ((a.b.rows > 1 && a.out.row < h->d.head_dim) || (q_heads > 1 && a.out.head < h->d.head_dim))
-    return fail(QG_ERR_INVALID_ARG, "out: strides %lld, %lld: rows or heads overlap", (long long)a.out.row, (long long)a.out.head);
+  s = check_overlap(a.q, a.out, a.b.rows, q_heads, h->d.head_dim);
+  if (s != QG_OK) return s;
   a.window = window;
   a.sinks = sinks;
   a.partial = h->partial;

@@ -157,7 +157,8 @@ qg_status qgkv_append(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const
 
 /* out = attention of q over the cached tokens of one layer: q and out are
  * [rows][q_heads][head_dim], q_heads a multiple of kv_heads; scale > 0;
- * window >= 0 and sinks >= 0 as above.  out overlaps neither q nor itself. */
+ * window >= 0 and sinks >= 0 as above.  out overlaps neither q nor itself
+ * (refused where it can be told from pointers and equal strides). */
 qg_status qgkv_attend(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const qg_kv_rows* q, const qg_kv_rows* out,
                       int32_t q_heads, float scale, int32_t window, int32_t sinks, void* stream);
 

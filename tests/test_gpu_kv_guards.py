@@ -139,3 +139,37 @@ def test_check_waits_for_work_on_other_streams(given):
         with torch.cuda.stream(other):
             assert kv.info.tolist()[:2] == [0, 0]
         kv.check()
+
+
+@pytest.mark.parametrize("rows", [2, 70])
+def test_outputs_that_overlap_are_refused(rows):
+    """out over itself or over q, whole or in part; not where they only lie between each other."""
+    p = Pair([rows + 30], "f16", 16, 2, 64)
+    q = rand((rows, 4, 64), "f16", 7, 1.5)
+    kw = dict(seqs=ints(0))
+    want = p.gpu.attend(q, **kw)
+    store = torch.zeros(rows * 1024, dtype=torch.float16, device="cuda")
+
+    def view(row, head, ofs=0):
+        return store[ofs:].as_strided((rows, 4, 64), (row, head, 1))
+
+    for row, head in ((64, 64), (128, 64), (192, 64), (64, 128), (320, 128), (0, 64), (256, 32), (256, 0), (256, 64),
+                      (264, 64), (64, 64 * rows), (640, 192), (1024, 256)):
+        places = [r * row + h * head + e for r in range(rows) for h in range(4) for e in range(0, 64, 8)]
+        if len(set(places)) < len(places):
+            with pytest.raises(Q.QGError, match="overlap"):
+                p.gpu.attend(q, out=view(row, head), **kw)
+        else:
+            assert torch.equal(want, p.gpu.attend(q, out=view(row, head), **kw))
+    for row, head, ofs in ((256, 64, 0), (256, 64, 8), (256, 64, 256), (512, 64, 224), (1024, 128, 32), (512, 128, 128)):
+        store.zero_()
+        x = view(row, head)
+        x.copy_(q)
+        with pytest.raises(Q.QGError, match="out overlaps q"):
+            p.gpu.attend(x, out=view(row, head, ofs), **kw)
+        assert torch.equal(x, q)
+    for row, head, ofs in ((512, 64, 256), (512, 128, 64), (1024, 128, 64), (1024, 192, 64), (256, 64, 256 * rows)):
+        store.zero_()
+        x = view(row, head)
+        x.copy_(q)
+        assert torch.equal(want, p.gpu.attend(x, out=view(row, head, ofs), **kw)) and torch.equal(x, q)
