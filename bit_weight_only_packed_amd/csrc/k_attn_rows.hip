@@ -1,14 +1,25 @@
 // k_attn_rows.hip -- launcher of the many-row attention kernel (qg_attn_rows.h).
+#include <algorithm>
+
 #include "qg_attn_rows.h"
 
 namespace qg {
 
 namespace {
 
-template <int D> hipError_t go(const AttnArgs& a, bool bf16, unsigned blocks, hipStream_t st) {
+// Blocks of a launch at most: a launch holds fewer than 2^32 threads.  More than one is for
+// ragged calls alone, in which nearly all blocks are those of rows that their entry has not.
+constexpr unsigned kRowsLaunch = 1u << 23;
+static_assert((uint64_t)kRowsLaunch * 64 * ROWS_WAVES < (uint64_t)1 << 32, "threads of a launch");
+
+template <int D> hipError_t go(AttnArgs a, bool bf16, unsigned blocks, hipStream_t st) {
   const unsigned grid = blocks * (unsigned)a.splits;
-  if (bf16) k_attn_rows<D, true><<<grid, 64 * ROWS_WAVES, 0, st>>>(a);
-  else k_attn_rows<D, false><<<grid, 64 * ROWS_WAVES, 0, st>>>(a);
+  for (unsigned at = 0; at < grid; at += kRowsLaunch) {
+    const unsigned part = std::min(grid - at, kRowsLaunch);
+    a.first = (int)at;  // (0 where blocks are shared: their grids are small)
+    if (bf16) k_attn_rows<D, true><<<part, 64 * ROWS_WAVES, 0, st>>>(a);
+    else k_attn_rows<D, false><<<part, 64 * ROWS_WAVES, 0, st>>>(a);
+  }
   if (a.splits > 1) {
     const unsigned join = blocks * (unsigned)(ROWS_BLOCK / RJ_ROWS);
     if (bf16) k_attn_rows_join<D, true><<<join, RJ_THREADS, 0, st>>>(a);

@@ -311,7 +311,7 @@ void k_attn_rows(AttnArgs a) {
   // 36 with parts fastest)
   const unsigned blocks = gridDim.x / (unsigned)a.splits;
   const int z = blockIdx.x / blocks;
-  const RowsBlock<D> blk(a, blockIdx.x - z * blocks);
+  const RowsBlock<D> blk(a, a.first + (int)(blockIdx.x - z * blocks));
   if (blk.rb < 0 || z >= blk.parts) return;
   const KvEntry& e = blk.e;
   const TileRange<S::KT>& tr = blk.tr;

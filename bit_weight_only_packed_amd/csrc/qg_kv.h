@@ -108,6 +108,7 @@ struct AttnArgs {
   int workers;         // few rows: workgroups that share the tiles,
   int min_run;         // and places of their list that each takes at least
   int splits, splits1; // many rows: workgroups that may share a block's tiles, however many it has; and if few
+  int first;           // many rows: the launch's first block (0 where blocks are shared)
 };
 
 // Rows of one kv head that the few-row kernel takes, (new rows) * (q heads per kv head).
