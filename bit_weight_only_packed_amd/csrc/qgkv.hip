@@ -73,11 +73,13 @@ qg_status check_list(const qg_kv* h, const void* p, int n, const char* name) {
 qg_status batch_of(const qg_kv* h, int layer, const qg_kv_batch* b, KvDev* c, KvBatchDev* out) {
   if (layer < 0 || layer >= h->d.layers) return fail(QG_ERR_INVALID_ARG, "layer = %d is not in [0, %d)", layer, h->d.layers);
   if (!b) return fail(QG_ERR_INVALID_ARG, "batch is NULL");
-  if (b->n < 1 || b->n > h->d.max_seqs)
+  if (b->n < (b->rows ? 1 : 0) || b->n > h->d.max_seqs)
     return fail(QG_ERR_INVALID_ARG, "n = %d is not in [1, max_seqs = %d]", b->n, h->d.max_seqs);
-  if (b->rows < 1) return fail(QG_ERR_INVALID_ARG, "rows = %d is not positive", b->rows);
+  if (b->rows < 0) return fail(QG_ERR_INVALID_ARG, "rows = %d is negative", b->rows);
   if (!aligned4(b->seqs) || !aligned4(b->row_start))
     return fail(QG_ERR_INVALID_ARG, "seqs and row_start must be 4-byte aligned");
+  out->rows = b->rows;
+  if (b->rows == 0) return QG_OK;  // nothing to do, and no more to check
   if (b->row_start) {
     if (b->max_rows < 1 || b->max_rows > b->rows)
       return fail(QG_ERR_INVALID_ARG, "max_rows = %d is not in [1, rows = %d]", b->max_rows, b->rows);
@@ -100,7 +102,6 @@ qg_status batch_of(const qg_kv* h, int layer, const qg_kv_batch* b, KvDev* c, Kv
   out->seqs = b->seqs;
   out->row_start = b->row_start;
   out->n = b->n;
-  out->rows = b->rows;
   out->max_rows = b->row_start ? b->max_rows : b->rows / b->n;
   return QG_OK;
 }
@@ -278,6 +279,7 @@ qg_status qgkv_append(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const
   KvBatchDev bd;
   KvRows kr, vr;
   if (s == QG_OK) s = batch_of(h, layer, b, &c, &bd);
+  if (s == QG_OK && bd.rows == 0) return QG_OK;
   if (s == QG_OK) s = rows_of(k, "k", &kr);
   if (s == QG_OK) s = rows_of(v, "v", &vr);
   if (s != QG_OK) return s;
@@ -292,6 +294,7 @@ qg_status qgkv_attend(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const
   qg_status s = check_handle(h);
   AttnArgs a{};
   if (s == QG_OK) s = batch_of(h, layer, b, &a.c, &a.b);
+  if (s == QG_OK && a.b.rows == 0) return QG_OK;
   if (s == QG_OK) s = rows_of(q, "q", &a.q);
   if (s == QG_OK) s = rows_of(out, "out", &a.out);
   if (s != QG_OK) return s;

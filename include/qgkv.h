@@ -98,8 +98,8 @@ typedef struct {
 } qg_kv_desc;
 
 typedef struct {
-  int32_t n;                /* entries, 1 .. max_seqs                                          */
-  int32_t rows;             /* rows of the call over all entries, >= 1                         */
+  int32_t n;                /* entries, 1 .. max_seqs (0 without rows)                         */
+  int32_t rows;             /* rows of the call over all entries; 0: the call does nothing     */
   int32_t max_rows;         /* with row_start: at least the largest R_j (an entry's rows past
                                it are left out); ignored without                               */
   const int32_t* seqs;      /* device [n] or NULL                                              */

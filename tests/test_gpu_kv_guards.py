@@ -173,3 +173,23 @@ def test_outputs_that_overlap_are_refused(rows):
         x = view(row, head)
         x.copy_(q)
         assert torch.equal(want, p.gpu.attend(x, out=view(row, head, ofs), **kw)) and torch.equal(x, q)
+
+
+def test_steps_without_rows():
+    """A call of no rows does nothing, whatever its entries."""
+    p = Pair([20, 33], "f16", 16, 2, 64)
+    kv = torch.empty((0, 2, 64), dtype=torch.float16, device="cuda")
+    q = torch.empty((0, 4, 64), dtype=torch.float16, device="cuda")
+    for kw in (dict(), dict(seqs=[]), dict(seqs=[1]), dict(seqs=ints(0, 1)), dict(row_start=[0], max_rows=0),
+               dict(seqs=[1, 0], row_start=ints(0, 0, 0), max_rows=0), dict(seqs=[0], row_start=[0, 0], max_rows=5)):
+        p.gpu.append(kv, kv, **kw)
+        assert p.gpu.attend(q, **kw).shape == (0, 4, 64)
+    p.same_state()
+    for bad in (dict(layer=1), dict(seqs=[0, 1, 1])):
+        with pytest.raises(Q.QGError):
+            p.gpu.append(kv, kv, **bad)
+        with pytest.raises(Q.QGError):
+            p.gpu.attend(q, **bad)
+    one = rand((1, 2, 64), "f16", 5)
+    with pytest.raises(Q.QGError):
+        p.gpu.append(one, one, seqs=[])
