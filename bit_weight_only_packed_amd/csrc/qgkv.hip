@@ -106,13 +106,15 @@ qg_status batch_of(const qg_kv* h, int layer, const qg_kv_batch* b, KvDev* c, Kv
   return QG_OK;
 }
 
-qg_status rows_of(const qg_kv_rows* r, const char* name, KvRows* out) {
+// an operand of so many rows and heads (the stride of one alone is never used, and may be anything)
+qg_status rows_of(const qg_kv_rows* r, const char* name, int64_t rows, int64_t heads, KvRows* out) {
   if (!r || !r->ptr) return fail(QG_ERR_INVALID_ARG, "%s is NULL", name);
   if (!aligned16(r->ptr)) return fail(QG_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
-  if (r->row_stride % 8 || r->head_stride % 8 || r->row_stride < 0 || r->head_stride < 0)
+  const int64_t row = rows > 1 ? r->row_stride : 0, head = heads > 1 ? r->head_stride : 0;
+  if (row % 8 || head % 8 || row < 0 || head < 0)
     return fail(QG_ERR_INVALID_ARG, "%s: strides %lld, %lld are not multiples of 8 elements", name,
                 (long long)r->row_stride, (long long)r->head_stride);
-  *out = KvRows{static_cast<const uint16_t*>(r->ptr), r->row_stride, r->head_stride};
+  *out = KvRows{static_cast<const uint16_t*>(r->ptr), row, head};
   return QG_OK;
 }
 
@@ -280,8 +282,8 @@ qg_status qgkv_append(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const
   KvRows kr, vr;
   if (s == QG_OK) s = batch_of(h, layer, b, &c, &bd);
   if (s == QG_OK && bd.rows == 0) return QG_OK;
-  if (s == QG_OK) s = rows_of(k, "k", &kr);
-  if (s == QG_OK) s = rows_of(v, "v", &vr);
+  if (s == QG_OK) s = rows_of(k, "k", bd.rows, c.kv_heads, &kr);
+  if (s == QG_OK) s = rows_of(v, "v", bd.rows, c.kv_heads, &vr);
   if (s != QG_OK) return s;
   if ((int64_t)bd.max_rows * 2 * c.kv_heads >= (int64_t)1 << 31)
     return fail(QG_ERR_UNSUPPORTED, "%d rows of %d heads in one call", bd.max_rows, c.kv_heads);
@@ -295,8 +297,8 @@ qg_status qgkv_attend(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const
   AttnArgs a{};
   if (s == QG_OK) s = batch_of(h, layer, b, &a.c, &a.b);
   if (s == QG_OK && a.b.rows == 0) return QG_OK;
-  if (s == QG_OK) s = rows_of(q, "q", &a.q);
-  if (s == QG_OK) s = rows_of(out, "out", &a.out);
+  if (s == QG_OK) s = rows_of(q, "q", a.b.rows, q_heads, &a.q);
+  if (s == QG_OK) s = rows_of(out, "out", a.b.rows, q_heads, &a.out);
   if (s != QG_OK) return s;
   if (q_heads < 1 || q_heads % a.c.kv_heads)
     return fail(QG_ERR_INVALID_ARG, "q_heads = %d is not a positive multiple of kv_heads = %d", q_heads, a.c.kv_heads);

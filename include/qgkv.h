@@ -107,8 +107,9 @@ typedef struct {
 } qg_kv_batch;
 
 /* A 3-d operand [rows][heads][head_dim] of the cache's type: strides in
- * elements, multiples of 8; head_dim is contiguous; 16-byte aligned.  So k and
- * v may be columns of stacked q|k|v rows. */
+ * elements, multiples of 8 (that of a single row or head is not used);
+ * head_dim is contiguous; 16-byte aligned.  So k and v may be columns of stacked
+ * q|k|v rows. */
 typedef struct {
   void* ptr;
   int64_t row_stride;

@@ -193,3 +193,30 @@ def test_steps_without_rows():
     one = rand((1, 2, 64), "f16", 5)
     with pytest.raises(Q.QGError):
         p.gpu.append(one, one, seqs=[])
+
+
+@pytest.mark.parametrize("heads,rows", [(1, 5), (2, 1), (1, 1), (1, 40), (2, 40)])
+def test_strides_of_a_single_row_or_head_are_not_used(heads, rows):
+    """They may be anything, as a slice's are; those that are used are held to their rule."""
+    p, same = (Pair([60], "f16", 16, heads, 64) for _ in range(2))
+    q, k, v = rand((rows, 2 * heads, 64), "f16", 3), rand((rows, heads, 64), "f16", 4), rand((rows, heads, 64), "f16", 5)
+    kw = dict(seqs=ints(0))
+
+    def odd(x):
+        row, head = (3 if rows == 1 else x.stride(0)), (5 if x.shape[1] == 1 else x.stride(1))
+        return x.as_strided(x.shape, (row, head, 1))
+
+    same.gpu.append(k, v, **kw)
+    p.gpu.append(odd(k), odd(v), **kw)
+    assert torch.equal(p.gpu.pool.view(torch.int16), same.gpu.pool.view(torch.int16))
+    out = odd(torch.empty_like(q))
+    assert torch.equal(p.gpu.attend(odd(q), out=out, **kw), same.gpu.attend(q, **kw))
+    if heads == 1:  # a single q head too
+        one = odd(q[:, :1].contiguous())
+        assert torch.equal(p.gpu.attend(one, **kw), same.gpu.attend(q[:, :1].contiguous(), **kw))
+    wide = torch.zeros(rows * 1024 + 1024, dtype=torch.float16, device="cuda")
+    with pytest.raises(Q.QGError, match="strides"):
+        p.gpu.attend(wide.as_strided((rows, 2 * heads, 64), (1000, 68, 1)), **kw)
+    if rows > 1:
+        with pytest.raises(Q.QGError, match="strides"):
+            p.gpu.append(wide.as_strided((rows, heads, 64), (1004, 64, 1)), v, **kw)
