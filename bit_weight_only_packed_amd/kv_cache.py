@@ -67,7 +67,8 @@ class KVCache:
     slots; with ``row_start`` (int32 [n + 1], with ``max_rows`` at least the
     largest count) entry j has rows row_start[j] .. row_start[j + 1] - 1, without
     it each has the same number.  They are the last tokens of their slots.
-    Index tensors may also be given as lists (copied to the device).
+    Index tensors may also be given as lists (copied to the device).  Calls run on
+    the cache's GPU, whichever is the current one.
     """
 
     def __init__(self, pages: int, page_size: int, kv_heads: int, head_dim: int, *, layers: int = 1, max_seqs: int = 1,
@@ -144,7 +145,12 @@ class KVCache:
         return self._torch.cuda.current_stream(self._dev).cuda_stream
 
     def _call(self, name, *args) -> None:
-        st = self._c[name](self._h, *args)
+        cuda = self._torch.cuda
+        if cuda.current_device() == self._dev:
+            st = self._c[name](self._h, *args)
+        else:  # the library works on the current GPU
+            with cuda.device(self._dev):
+                st = self._c[name](self._h, *args)
         if st:
             self._check(st)
 

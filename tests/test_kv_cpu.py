@@ -3,8 +3,10 @@ constants against include/qgkv.h, and the oracle's own pins (closed forms, brute
 force and invariants of the page operations)."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import re
+import types
 
 import numpy as np
 import pytest
@@ -187,3 +189,26 @@ def test_append_after_a_refused_extend():
     c.info[0] = 0
     c.append(0, [1], [1], k[:1], k[:1])
     assert (c.tokens(1, 0, 0)[7] == 1).all()
+
+
+@pytest.mark.parametrize("current", [0, 1])
+def test_calls_run_on_the_caches_gpu(current):
+    """The library works on the current GPU: a call makes the cache's the current one for its time."""
+    class Cuda:
+        at = current
+
+        def current_device(self):
+            return self.at
+
+        @contextlib.contextmanager
+        def device(self, i):
+            before, self.at = self.at, i
+            yield
+            self.at = before
+
+    cuda, seen = Cuda(), []
+    kv = Q.KVCache.__new__(Q.KVCache)
+    kv._h, kv._dev, kv._torch = None, 1, types.SimpleNamespace(cuda=cuda)
+    kv._c = {"compact": lambda h, st: seen.append((cuda.at, st)) or 0}
+    kv._call("compact", 7)
+    assert seen == [(1, 7)] and cuda.at == current
