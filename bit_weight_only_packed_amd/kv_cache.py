@@ -67,6 +67,10 @@ class KVCache:
     slots; with ``row_start`` (int32 [n + 1], with ``max_rows`` at least the
     largest count) entry j has rows row_start[j] .. row_start[j + 1] - 1, without
     it each has the same number.  They are the last tokens of their slots.
+    With neither, n is the smaller of the number of rows and ``max_seqs``: up to
+    ``max_seqs`` rows are one new token each of slots 0, 1, ..., more of them are
+    rows / max_seqs each of all slots.  So the rows of one slot of several need
+    ``seqs=[slot]``.
     Index tensors may also be given as lists (copied to the device).  Calls run on
     the cache's GPU, whichever is the current one.
     """
@@ -231,7 +235,8 @@ class KVCache:
         self._call("compact", self._on(stream))
 
     def append(self, k, v, *, layer: int = 0, seqs=None, row_start=None, max_rows: int = None, stream=None) -> None:
-        """Write the rows' keys and values, [rows][kv_heads][head_dim] each."""
+        """Write the rows' keys and values, [rows][kv_heads][head_dim] each.  Which
+        slots: see the class; one slot takes one entry of a call."""
         st = self._on(stream)
         _, ka, va = self._args
         rows, _ = self._rows(ka, "k", k, self.kv_heads)
@@ -246,7 +251,7 @@ class KVCache:
         """Attention of q [rows][q_heads][head_dim] over the cached tokens of one
         layer; returns out of the same shape.  scale: default head_dim ** -0.5.
         window: a row sees its last ``window`` tokens (0: all) and the first
-        ``sinks`` of its slot."""
+        ``sinks`` of its slot.  Which slots the rows are of: see the class."""
         st = self._on(stream)
         _, qa, oa = self._args
         rows, heads = self._rows(qa, "q", q)

@@ -135,13 +135,13 @@ qg_status qgkv_destroy(qg_kv_handle h);
 qg_status qgkv_extend(qg_kv_handle h, const int32_t* n_new, void* stream);
 
 /* dst[i] becomes a second name of src[i]'s tokens: same pages, refs + 1, no
- * copy (device int32 [n], n <= max_seqs).  An entry is refused if an index is
+ * copy (device int32 [n], 1 <= n <= max_seqs).  An entry is refused if an index is
  * out of range, dst is not empty or was named by an earlier entry, or src is
  * also a dst of the call. */
 qg_status qgkv_fork(qg_kv_handle h, const int32_t* src, const int32_t* dst, int32_t n, void* stream);
 
 /* Cut slot seqs[i] to its first min(keep[i], lens) tokens (keep NULL or <= 0:
- * free it): pages past them are let go, refs - 1.  An entry is refused if its
+ * free it): pages past them are let go, refs - 1; 1 <= n <= max_seqs.  An entry is refused if its
  * index is out of range or was named by an earlier entry. */
 qg_status qgkv_trim(qg_kv_handle h, const int32_t* seqs, const int32_t* keep, int32_t n, void* stream);
 
@@ -151,7 +151,7 @@ qg_status qgkv_trim(qg_kv_handle h, const int32_t* seqs, const int32_t* keep, in
 qg_status qgkv_compact(qg_kv_handle h, void* stream);
 
 /* Write the rows' keys and values of one layer into their pages: k and v are
- * [rows][kv_heads][head_dim].  Writes nothing while a refused qgkv_extend
+ * [rows][kv_heads][head_dim]; a slot takes one entry of the call at most.  Writes nothing while a refused qgkv_extend
  * stands (see there): the rows' places are then other tokens'. */
 qg_status qgkv_append(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const qg_kv_rows* k, const qg_kv_rows* v,
                       void* stream);
