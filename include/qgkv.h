@@ -141,8 +141,8 @@ qg_status qgkv_extend(qg_kv_handle h, const int32_t* n_new, void* stream);
 qg_status qgkv_fork(qg_kv_handle h, const int32_t* src, const int32_t* dst, int32_t n, void* stream);
 
 /* Cut slot seqs[i] to its first min(keep[i], lens) tokens (keep NULL or <= 0:
- * free it): pages past them are let go, refs - 1; 1 <= n <= max_seqs.  An entry is refused if its
- * index is out of range or was named by an earlier entry. */
+ * free it): pages past them are let go, refs - 1; 1 <= n <= max_seqs.  An entry
+ * is refused if its index is out of range or was named by an earlier entry. */
 qg_status qgkv_trim(qg_kv_handle h, const int32_t* seqs, const int32_t* keep, int32_t n, void* stream);
 
 /* Move the live pages together: with m live pages, those with id >= m, in
@@ -151,8 +151,9 @@ qg_status qgkv_trim(qg_kv_handle h, const int32_t* seqs, const int32_t* keep, in
 qg_status qgkv_compact(qg_kv_handle h, void* stream);
 
 /* Write the rows' keys and values of one layer into their pages: k and v are
- * [rows][kv_heads][head_dim]; a slot takes one entry of the call at most.  Writes nothing while a refused qgkv_extend
- * stands (see there): the rows' places are then other tokens'. */
+ * [rows][kv_heads][head_dim]; a slot takes one entry of the call at most.
+ * Writes nothing while a refused qgkv_extend stands (see there): the rows'
+ * places are then other tokens'. */
 qg_status qgkv_append(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const qg_kv_rows* k, const qg_kv_rows* v,
                       void* stream);
 

@@ -1,4 +1,5 @@
-"""Attention calls as large as their arguments may be: more blocks than a launch holds."""
+"""Attention calls as large as their arguments may be: more blocks than a launch holds, more entries than a workgroup has
+threads, prompts and long single tokens in one call."""
 from __future__ import annotations
 
 import numpy as np
@@ -7,7 +8,8 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from _kv import UNIT, np64, rand  # noqa: E402
+from _kv import UNIT, Pair, np64  # noqa: E402
+from test_gpu_kv_attend import run  # noqa: E402
 from oracle import kv_oracle as KO  # noqa: E402
 import bit_weight_only_packed_amd as Q  # noqa: E402
 
@@ -46,3 +48,19 @@ def test_more_blocks_than_a_launch_holds():
                 es = 66 * 2.0 ** -24 * np.abs(x).sum() * np.abs(k).max() * 0.125
                 tol = np.abs(v).max() * (u + 2 * es + (length + 64) * 2.0 ** -23) + u * np.abs(ref) + 2.0 ** -24
                 assert (np.abs(np64(out[r, h]) - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("n,D,rows,G", [(257, 256, 1, 2), (512, 64, 2, 2), (513, 128, 1, 1), (700, 64, 1, 3), (1024, 64, 1, 1),
+                                        (600, 64, 5, 7)])
+def test_entries_past_the_threads_of_a_workgroup(n, D, rows, G):
+    """The list of entries is made in several passes: 256 or 512 at a time (the last case: the many-row kernel)."""
+    lens = [(29 * i) % 70 for i in range(n)]
+    slots = [int(s) for s in np.random.default_rng(n).permutation(n)]
+    run(Pair(lens, "f16", 16, 1, D), [rows] * n, G, slots=slots, uniform=True)
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "f16"), (128, "bf16"), (256, "f16")])
+def test_prompts_and_long_single_tokens_in_one_call(D, dtype):
+    """A chunk of a prompt beside decoding slots, some far longer than it, and an idle one."""
+    run(Pair([200, 9001, 3, 0, 2500, 170], dtype, 32, 2, D), [140, 1, 1, 1, 1, 0], 3)
+    run(Pair([9001, 200, 3, 0, 70], dtype, 32, 1, D), [1, 140, 3, 1, 70], 4, window=700, sinks=5)
