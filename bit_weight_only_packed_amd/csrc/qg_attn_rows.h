@@ -115,6 +115,7 @@ template <int D> struct RowsState {
   at_f16 O[S::ND];
   float m, l;   // m: in units of q . k
   int pos;      // this lane's row's position
+  bool large;   // (the same for the wave) some row's c m is 2^20 or more
 };
 
 // its scores with a tile, and their weights
@@ -187,6 +188,7 @@ __device__ __forceinline__ void rw_softmax(RowsWeights<D>& P, RowsScores<D>& s, 
     const float mn = fmaxf(r.m, mx);
     const float f = at_exp2((r.m - at_safe(mn)) * a.scale_log2);
     r.m = mn;
+    r.large = __any(fabsf(at_safe(mn) * a.scale_log2) >= 0x1p20f);
     r.l *= f;
 #pragma unroll
     for (int x = 0; x < S::ND; ++x)
@@ -196,8 +198,8 @@ __device__ __forceinline__ void rw_softmax(RowsWeights<D>& P, RowsScores<D>& s, 
   float ms = at_safe(r.m) * a.scale_log2 - RW_BIAS<BF>;
   // c s - ms, rounded once, is off by the rounding of ms: by 2^-5 at most below 2^20.  Scores so
   // large that it could overflow the weights are subtracted first (taken everywhere that
-  // costs 8,191 tokens 709 against 694 us; the look costs nothing there).
-  if (__builtin_expect(__any(fabsf(ms) >= 0x1p20f), 0)) {
+  // costs 8,191 tokens 709 against 694 us).
+  if (__builtin_expect(r.large, 0)) {
 #pragma unroll
     for (int g = 0; g < S::NT; ++g)
 #pragma unroll
@@ -339,7 +341,7 @@ void k_attn_rows(AttnArgs a) {
   for (int x = 0; x < S::ND; ++x)
 #pragma unroll
     for (int i = 0; i < 16; ++i) r.O[x][i] = 0.0f;
-  r.m = -__builtin_inff(), r.l = 0.0f;
+  r.m = -__builtin_inff(), r.l = 0.0f, r.large = false;
 
   if (tid == 0) odd_at = 0;
   const int nt = t1 - t0;
