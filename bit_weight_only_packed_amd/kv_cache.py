@@ -149,13 +149,13 @@ class KVCache:
         return self._torch.cuda.current_stream(self._dev).cuda_stream
 
     def _call(self, name, *args) -> None:
-        cuda = self._torch.cuda
-        if cuda.current_device() == self._dev:
-            st = self._c[name](self._h, *args)
-        else:  # the library works on the current GPU
-            with cuda.device(self._dev):
-                st = self._c[name](self._h, *args)
+        st = self._c[name](self._h, *args)
         if st:
+            # the library refuses, before all else, a cache that is not on the current GPU
+            cuda = self._torch.cuda
+            if cuda.current_device() != self._dev:
+                with cuda.device(self._dev):
+                    st = self._c[name](self._h, *args)
             self._check(st)
 
     def _index(self, name, x, n=None, stream=None):

@@ -193,7 +193,8 @@ def test_append_after_a_refused_extend():
 
 @pytest.mark.parametrize("current", [0, 1])
 def test_calls_run_on_the_caches_gpu(current):
-    """The library works on the current GPU: a call makes the cache's the current one for its time."""
+    """The library refuses a cache that is not on the current GPU: a call then makes the cache's the current one for its
+    time."""
     class Cuda:
         at = current
 
@@ -209,6 +210,14 @@ def test_calls_run_on_the_caches_gpu(current):
     cuda, seen = Cuda(), []
     kv = Q.KVCache.__new__(Q.KVCache)
     kv._h, kv._dev, kv._torch = None, 1, types.SimpleNamespace(cuda=cuda)
-    kv._c = {"compact": lambda h, st: seen.append((cuda.at, st)) or 0}
+    kv._check = lambda st: seen.append(st) if st else None
+
+    def compact(h, st):
+        seen.append((cuda.at, st))
+        return Q.QG_OK if cuda.at == 1 and st == 7 else Q.QG_ERR_INVALID_ARG
+
+    kv._c = {"compact": compact}
     kv._call("compact", 7)
-    assert seen == [(1, 7)] and cuda.at == current
+    assert seen == [(0, 7)] * (current == 0) + [(1, 7)] and cuda.at == current
+    kv._call("compact", 8)
+    assert seen[-1] == Q.QG_ERR_INVALID_ARG and cuda.at == current
