@@ -9,11 +9,14 @@
 //   M = max m_i,  o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
 // A range in which a row sees nothing has m = -inf and contributes 0.
 //
-// Weights meet the values on the matrix cores as fp16 or bf16, one rounding each.  fp16
-// would lose those below 2^-14 of the largest bit by bit and those below 2^-25 whole:
-// behind one token that takes nearly all the weight (a sink with a value of 0) that can be
-// all of the output.  So in fp16 every weight, in o and in l alike, is larger by a fixed power
-// of two, which the division by l takes away again: the largest reach 2^AT_FP16_TOP.
+// Weights meet the values on the matrix cores as fp16 or bf16, one rounding each: in 32
+// bits that product would run at a sixteenth of the rate, and in two parts at half of it, to
+// take a whole output from 2.6e-4 off (fp16; bf16 2.3e-3) to the 2.0e-4 (1.7e-3) of its own
+// rounding.  fp16 would lose those below 2^-14 of the largest bit by bit and those below
+// 2^-25 whole: behind one token that takes nearly all the weight (a sink with a value of
+// 0) that can be all of the output.  So in fp16 every weight, in o and in l alike, is larger
+// by a fixed power of two, which the division by l takes away again: the largest reach
+// 2^AT_FP16_TOP.
 #pragma once
 #include "qg_kv.h"
 

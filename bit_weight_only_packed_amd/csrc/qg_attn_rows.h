@@ -3,9 +3,10 @@
 //
 // Bound.  4 D flops per visible (row, q head, token) on the matrix cores, and one
 // exponential per 4 D flops beside them.  8,191 prompt tokens, 40 q and 8 kv heads of
-// 128 (687 GFLOP): 691 us, 994 TFLOP/s, where the card's best fp16 matrix product
-// reaches 1,154; the last 4,096 rows of 16,411 tokens through a window of 2,048 with 8
-// sinks (bf16, 172 GFLOP): 217 us, 793 TFLOP/s.
+// 128 (687 GFLOP): 707 to 731 us by card, 940 to 972 TFLOP/s, where the card's best fp16
+// matrix product reaches 1,154; the last 4,096 rows of 16,411 tokens through a window of
+// 2,048 with 8 sinks (bf16, 172 GFLOP): 217 to 220 us, 782 to 793 TFLOP/s (1,280 blocks of one
+// length on 512 places: 2.5 rounds in the time of 3; 7 % is computed past the window's edges).
 //
 // A block is 32 rows per wave of one (entry, kv head): row r is new token r / G, q
 // head r % G of the group, so the q heads that share a kv head share its tokens,
@@ -34,7 +35,7 @@
 //
 // The running maximum is raised, and what has been summed rescaled, only where a
 // row's new maximum is more than RW_SLACK above it in the exponent, so the rescaling of
-// the accumulators almost never runs.  In fp16 that is 2^4 (level with 2^8 in time) and
+// the accumulators almost never runs.  In fp16 that is 2^4 (8,191 tokens: 731 us, 734 at 2^8) and
 // weights are carried 2^11 times larger: up to 2^15, and only those below 2^-36 of the row's
 // largest are lost.
 #pragma once

@@ -2,8 +2,8 @@
 // sequence, or the rows of a verify batch.
 //
 // Bound.  Every cached token's key and value are read once per kv head,
-// 4 D bytes, for 4 D G R flops (G q heads per kv head, R new rows: 5 to 160 at
-// the shapes met) -- HBM, with matrix-core work to spare.  So the G * R rows that
+// 4 D bytes, for 4 D G R flops (G q heads per kv head, R new rows: up to 32 of
+// them together) -- HBM, with matrix-core work to spare.  So the G * R rows that
 // share a kv head are packed into tiles of 16 (MT of them, one or two) and
 // all served by one read of the tokens, and the kernel is built to keep reads in
 // flight.
@@ -33,7 +33,10 @@
 // TB/s: one row of 131,071 tokens 103 us (537 MB, 5.2 TB/s); of 48 sequences of 3 to
 // 24,577 tokens each (bf16) 108 us (578 MB, 5.3 TB/s); one row of 1,025 tokens 11 to 13
 // us, a chain of some eight memory round trips (entry, table, keys, join).  16 q and 2 kv
-// heads of 256, 32 sequences, window 4,096: 50 us (204 MB, 4.1 TB/s).
+// heads of 256, 32 sequences, window 4,096: 50 us (204 MB, 4.1 TB/s; 256 vector and 74
+// accumulation registers, one wave a SIMD).
+// The scalar registers run out: 51 (heads of 64), 56 (128) and 68 (256) values are kept in
+// lanes of vector registers, and some are moved there and back every tile.
 #pragma once
 #include "qg_attn.h"
 

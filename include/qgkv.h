@@ -160,7 +160,10 @@ qg_status qgkv_append(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const
 /* out = attention of q over the cached tokens of one layer: q and out are
  * [rows][q_heads][head_dim], q_heads a multiple of kv_heads; scale > 0;
  * window >= 0 and sinks >= 0 as above.  out overlaps neither q nor itself
- * (refused where it can be told from pointers and equal strides). */
+ * (refused where it can be told from pointers and equal strides).  One call takes
+ * entries of any row counts, but is made for those near max_rows: long slots with
+ * few rows are better attended in a call of their own (one new row in each of 47 slots
+ * of 3 to 24,577 tokens beside 512 rows of another: 458 us, in two calls 212). */
 qg_status qgkv_attend(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const qg_kv_rows* q, const qg_kv_rows* out,
                       int32_t q_heads, float scale, int32_t window, int32_t sinks, void* stream);
 
