@@ -28,11 +28,11 @@
  * slot j) with R_j new rows, rows row_start[j] .. row_start[j + 1] - 1 of the
  * call's `rows` rows (NULL: rows / n each).  They are the LAST R_j tokens of the
  * slot, whose length already counts them: row i stands at position
- * p = lens - R_j + i (of more than max_rows rows the later ones are left out:
- * not written, no output; the others keep their positions).  seqs and row_start are device memory and may change
- * between replays of a captured call.  A slot index out of range acts as an
- * empty slot.  A row at a position before 0 (an idle slot, length 0) is
- * not written by append and sees nothing in attend: its output is 0.
+ * p = lens - R_j + i.  Of more than max_rows rows the later ones are left out (not
+ * written, no output); the others keep their positions.  seqs and row_start are
+ * device memory and may change between replays of a captured call.  A slot index
+ * out of range acts as an empty slot.  A row at a position before 0 (an idle slot,
+ * length 0) is not written by append and sees nothing in attend: its output is 0.
  *
  * Attention.  With h' = h / (q_heads / kv_heads) and s_t = scale * q_h . k_t,h',
  *   out_h = sum_t exp(s_t) v_t,h' / sum_t exp(s_t)
