@@ -1,7 +1,8 @@
 """Packed low-bit weight-only GEMV / verify GEMM for MI355X (gfx950).
 
 Thin Python binding of ``libqgemv.so`` (C ABI in ``include/qgemv.h``, and for
-the paged key-value cache and its attention ``include/qgkv.h``): it only
+the paged key-value cache and its attention ``include/qgkv.h``, for the rows
+between the products ``include/qgstep.h``): it only
 marshals arguments -- device pointers of PyTorch tensors and the current HIP
 stream -- into the library, where every step of the computation runs in HIP
 kernels.  PyTorch is used for device memory and streams only.  There is no CPU
@@ -16,16 +17,18 @@ from typing import Optional
 
 import numpy as np
 
-from . import kv_cache
+from . import kv_cache, step_ops
 from .kv_cache import KVCache
+from .step_ops import Rotary, rms_norm, sample, sample_workspace
 
-__all__ = ["QGError", "lib", "QLinear", "mlp", "run_batch", "stream_read", "KVCache", "declared_symbols", "LIB_PATH",
-           "HEADER_PATH", "KV_HEADER_PATH"]
+__all__ = ["QGError", "lib", "QLinear", "mlp", "run_batch", "stream_read", "KVCache", "Rotary", "rms_norm", "sample",
+           "sample_workspace", "declared_symbols", "LIB_PATH", "HEADER_PATH", "KV_HEADER_PATH", "STEP_HEADER_PATH"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqgemv.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "qgemv.h")
 KV_HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "qgkv.h")
+STEP_HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "qgstep.h")
 
 QG_OK, QG_ERR_INVALID_ARG, QG_ERR_UNSUPPORTED, QG_ERR_DEVICE, QG_ERR_OOM = 0, -1, -2, -3, -4
 FMT_UNIFORM, FMT_TRELLIS3, FMT_MXFP4, FMT_MXFP6 = 0, 1, 2, 3
@@ -88,14 +91,15 @@ def lib() -> ctypes.CDLL:
               "qgemv_debug_unpack", "qgemv_debug_dequant", "qgemv_debug_operand", "qgemv_debug_trellis"):
         getattr(L, f).restype = ctypes.c_int
     kv_cache.bind(L)
+    step_ops.bind(L)
     _lib = L
     return L
 
 
 def declared_symbols() -> list:
-    """Function names declared in include/qgemv.h and include/qgkv.h."""
+    """Function names declared in include/qgemv.h, include/qgkv.h and include/qgstep.h."""
     text = ""
-    for path in (HEADER_PATH, KV_HEADER_PATH):
+    for path in (HEADER_PATH, KV_HEADER_PATH, STEP_HEADER_PATH):
         with open(path) as f:
             text += f.read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)

@@ -1,0 +1,49 @@
+// k_sample.hip -- launchers of the sampling kernels (qg_sample.h).
+#include "qg_sample.h"
+
+namespace qg {
+
+namespace {
+
+template <int TY> hipError_t go(const SampleArgs& a, hipStream_t st) {
+  for (int at = 0; at < a.rows; at += SAMPLE_ROWS) {
+    const unsigned rows = (unsigned)(a.rows - at < SAMPLE_ROWS ? a.rows - at : SAMPLE_ROWS);
+    SampleArgs b = a;
+    b.logits = reinterpret_cast<const char*>(a.logits) + (int64_t)at * a.stride * (TY == QGS_F32 ? 4 : 2);
+    b.u += at, b.tokens += at;
+    if (b.probs) b.probs += at;
+    if (b.temperature) b.temperature += at;
+    if (b.top_k) b.top_k += at;
+    if (b.top_p) b.top_p += at;
+    if (b.min_p) b.min_p += at;
+    const dim3 grid((unsigned)a.parts, rows);
+    k_sample_max<TY><<<grid, SM_T, 0, st>>>(b);
+    if (a.cuts) {
+      k_sample_hist<TY><<<grid, SM_T, 0, st>>>(b);
+      k_sample_cut<TY><<<rows, SM_CUT, 0, st>>>(b);
+    }
+    k_sample_pick<TY><<<grid, SM_T, 0, st>>>(b);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// A part is 2,048 tokens at least, one load of a thread; as many parts as give each CU some
+// workgroups, 64 at most.
+void sample_parts(int rows, int vocab, int* parts, int* len) {
+  int p = (vocab + 2047) / 2048;
+  const int most = rows >= 2048 ? 1 : 2048 / rows;
+  p = p < most ? p : most;
+  p = p < 64 ? p : 64;
+  *len = ((vocab + p - 1) / p + 7) / 8 * 8;
+  *parts = (vocab + *len - 1) / *len;
+}
+
+hipError_t launch_sample(const SampleArgs& a, int type, hipStream_t st) {
+  if (type == QGS_F16) return go<QGS_F16>(a, st);
+  if (type == QGS_BF16) return go<QGS_BF16>(a, st);
+  return go<QGS_F32>(a, st);
+}
+
+}  // namespace qg

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "qg_step.h"
+
 namespace qg {
 
 constexpr int KV_MAX_SEQS = 1024;
@@ -93,6 +95,18 @@ hipError_t launch_kv_compact(const KvPool& p, int cus, hipStream_t st);
 // refused, info: KvPool's head + 2 and info
 hipError_t launch_kv_append(const KvDev& c, const KvBatchDev& b, const KvRows& k, const KvRows& v, const int32_t* refused,
                             const int32_t* info, int D, hipStream_t st);
+
+// ---- rows on their way into the pages, rotated ----
+struct RotAppend {
+  KvDev c;
+  KvBatchDev b;
+  KvRows q, out, k, v;
+  RotDev r;
+  const int32_t *refused, *info;
+  int q_heads;
+  int slots;  // threads that share a row's heads
+};
+hipError_t launch_kv_append_rotary(const RotAppend& a, int D, bool bf16, int cus, hipStream_t st);
 
 // ---- attention ---------------------------------------------------------------
 struct AttnArgs {

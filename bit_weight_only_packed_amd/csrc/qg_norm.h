@@ -1,0 +1,211 @@
+// qg_norm.h -- root-mean-square norm of rows, with the residual's addition before it
+// and, if wanted, its output in 8 bits with scales.
+//
+//   h = round(x + r),  y = h w / sqrt(mean h^2 + eps),  codes round(y / s), s = max |y| / top
+//
+// Bound.  HBM where rows are many: each operand is read once and each output written
+// once, and a row lives in registers between its sum and its outputs.  Where rows are few, the
+// call: one round trip to memory, one sum over the workgroup, one store.
+#pragma once
+#include "qg_attn.h"
+#include "qg_step.h"
+
+namespace qg {
+
+typedef uint32_t nm_u4 __attribute__((ext_vector_type(4), aligned(2)));  // 16 bytes of 16-bit elements, where they are
+typedef uint32_t nm_u2 __attribute__((ext_vector_type(2), aligned(1)));  // 8 codes
+
+template <bool BF> __device__ __forceinline__ float nm_f32(uint32_t h) {
+  if constexpr (BF) return __builtin_bit_cast(float, h << 16);
+  else return (float)__builtin_bit_cast(_Float16, (uint16_t)h);
+}
+// 8 elements at p of which `left` are there; the others are 0
+__device__ __forceinline__ kv_u4 nm_load(const uint16_t* p, int left) {
+  if (left >= 8) return *reinterpret_cast<const nm_u4*>(p);
+  kv_u4 w = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < left) w[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
+  return w;
+}
+__device__ __forceinline__ void nm_store(uint16_t* p, kv_u4 w, int left) {
+  if (left >= 8) {
+    *reinterpret_cast<nm_u4*>(p) = w;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < left) p[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+}
+template <bool BF> __device__ __forceinline__ float nm_at(kv_u4 w, int i) { return nm_f32<BF>((w[i / 2] >> (16 * (i & 1))) & 0xFFFFu); }
+
+// sum or maximum over the workgroup, in a fixed order; lds: a float per wave
+template <bool MAX> __device__ __forceinline__ float nm_all(float x, float* lds) {
+  const auto op = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+#pragma unroll
+  for (int o = 32; o; o >>= 1) x = op(x, __shfl_xor(x, o));
+  const int waves = blockDim.x >> 6;
+  if (waves == 1) return x;
+  __syncthreads();  // the last use's readers are done
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
+  __syncthreads();
+  float t = lds[0];
+  for (int w = 1; w < waves; ++w) t = op(t, lds[w]);
+  return t;
+}
+
+// codes of 8 values: v / s rounded to nearest even.  |v| / s is at most the type's largest but
+// for the rounding of s, which the rounding of the code takes away.
+template <int CODES> __device__ __forceinline__ kv_u2 nm_codes(const float (&v)[8], float s) {
+  kv_u2 w = {0, 0};
+  if (!(s > 0.0f)) return w;  // zeros, or a NaN scale
+  float c[8];
+  const float r = 1.0f / s;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = s < 0x1p-100f ? v[i] / s : v[i] * r;  // (1 / s may overflow below that)
+  if constexpr (CODES == QGS_INT8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i / 4] |= ((uint32_t)(int)rintf(c[i]) & 0xFFu) << (8 * (i & 3));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      int x = __builtin_amdgcn_cvt_pk_fp8_f32(c[4 * i], c[4 * i + 1], 0, false);
+      w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[4 * i + 2], c[4 * i + 3], x, true);
+    }
+  }
+  return w;
+}
+
+// One row per workgroup; thread t holds chunks t, t + blockDim, ... of 8 elements, as the
+// 16-bit values that they are.
+template <bool BF, int C, int CODES> __global__ __launch_bounds__(1024) void k_rms_norm(NormArgs a) {
+  __shared__ float lds[16];
+  const int64_t row = a.first + (int64_t)blockIdx.x;
+  const int T = blockDim.x;
+  const auto place = [&](int c) { return (c * T + (int)threadIdx.x) * 8; };
+  const uint16_t* x = a.x + row * a.x_stride;
+  kv_u4 h[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) h[c] = nm_load(x + place(c), a.n - place(c));
+  if (a.residual) {
+    uint16_t* res = a.residual + row * a.residual_stride;
+    kv_u4 r[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) r[c] = nm_load(res + place(c), a.n - place(c));
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        h[c][i] = at_pack<BF>(nm_at<BF>(h[c], 2 * i) + nm_at<BF>(r[c], 2 * i), nm_at<BF>(h[c], 2 * i + 1) + nm_at<BF>(r[c], 2 * i + 1));
+      nm_store(res + place(c), h[c], a.n - place(c));
+    }
+  }
+  float ss = 0.0f;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(nm_at<BF>(h[c], i), nm_at<BF>(h[c], i), ss);
+  ss = nm_all<false>(ss, lds);
+  const float n = (float)a.n;
+  float rs = 1.0f / sqrtf(ss / n + a.eps);
+  int e = 0;  // the row is taken times 2^-e
+  if (__builtin_expect(!(ss < __builtin_inff()), 0)) {
+    // squares that overflow fp32 (bf16 values past 2^63)
+    float top = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float v = fabsf(nm_at<BF>(h[c], i));
+        top = fmaxf(top, v == v ? v : __builtin_inff());
+      }
+    top = nm_all<true>(top, lds);
+    if (top < __builtin_inff()) {  // (NaN and infinities stay as the formula has them)
+      e = ilogbf(top);
+      ss = 0.0f;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float v = ldexpf(nm_at<BF>(h[c], i), -e);
+          ss = __builtin_fmaf(v, v, ss);
+        }
+      ss = nm_all<false>(ss, lds);
+      rs = 1.0f / sqrtf(ss / n + ldexpf(a.eps, -2 * e));
+    }
+  }
+  const auto normed = [&](float (&y)[8], int c) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = nm_at<BF>(h[c], i);
+    if (__builtin_expect(e != 0, 0)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = ldexpf(y[i], -e);
+    }
+    if (a.weight) {
+      const kv_u4 w = nm_load(a.weight + place(c), a.n - place(c));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = y[i] * rs * nm_at<BF>(w, i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] *= rs;
+    }
+  };
+  if constexpr (CODES == QGS_SAME) {
+    uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + row * a.out_stride;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      float y[8];
+      normed(y, c);
+      kv_u4 w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = at_pack<BF>(y[2 * i], y[2 * i + 1]);
+      nm_store(out + place(c), w, a.n - place(c));
+    }
+  } else {
+    constexpr float TOP = CODES == QGS_INT8 ? 127.0f : 448.0f;
+    uint8_t* out = reinterpret_cast<uint8_t*>(a.out) + row * a.out_stride;
+    // the largest magnitudes; a NaN counts as infinity
+    const auto largest = [](const float (&v)[8], float m) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, v[i] == v[i] ? fabsf(v[i]) : __builtin_inff());
+      return m;
+    };
+    float all = 0.0f;
+    if (a.group == 0) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        float y[8];
+        normed(y, c);
+        all = largest(y, all);
+      }
+      all = nm_all<true>(all, lds);
+    }
+    const int per = a.group ? (a.n + a.group - 1) / a.group : 1;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int at = place(c);
+      float y[8];
+      normed(y, c);
+      float m = all;
+      if (a.group) {  // 4, 8 or 16 lanes share a group
+        m = largest(y, 0.0f);
+        m = fmaxf(m, __shfl_xor(m, 1));
+        m = fmaxf(m, __shfl_xor(m, 2));
+        if (a.group > 32) m = fmaxf(m, __shfl_xor(m, 4));
+        if (a.group > 64) m = fmaxf(m, __shfl_xor(m, 8));
+      }
+      const float s = m < __builtin_inff() ? m / TOP : __builtin_nanf("");
+      if (at < a.n && (a.group ? at % a.group == 0 : at == 0)) a.scales[row * per + (a.group ? at / a.group : 0)] = s;
+      const kv_u2 w = nm_codes<CODES>(y, s);
+      if (at + 8 <= a.n) {
+        *reinterpret_cast<nm_u2*>(out + at) = w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (at + i < a.n) out[at + i] = (uint8_t)(w[i / 4] >> (8 * (i & 3)));
+      }
+    }
+  }
+}
+
+}  // namespace qg

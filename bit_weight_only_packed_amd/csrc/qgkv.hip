@@ -9,6 +9,7 @@
 #include <new>
 
 #include "../../include/qgkv.h"
+#include "qg_check.h"
 #include "qg_error.h"
 #include "qg_kv.h"
 #include "qg_launch.h"
@@ -110,46 +111,8 @@ qg_status batch_of(const qg_kv* h, int layer, const qg_kv_batch* b, KvDev* c, Kv
 qg_status rows_of(const qg_kv_rows* r, const char* name, int64_t rows, int64_t heads, KvRows* out) {
   if (!r || !r->ptr) return fail(QG_ERR_INVALID_ARG, "%s is NULL", name);
   if (!aligned16(r->ptr)) return fail(QG_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
-  const int64_t row = rows > 1 ? r->row_stride : 0, head = heads > 1 ? r->head_stride : 0;
-  if (row % 8 || head % 8 || row < 0 || head < 0)
-    return fail(QG_ERR_INVALID_ARG, "%s: strides %lld, %lld are not multiples of 8 elements", name,
-                (long long)r->row_stride, (long long)r->head_stride);
-  *out = KvRows{static_cast<const uint16_t*>(r->ptr), row, head};
-  return QG_OK;
-}
-
-// Whether two of the D-element runs that begin at r * row + h * head (r < rows, h < heads)
-// and at those places + ofs share elements; with ofs 0 two runs of the same kind.
-bool runs_meet(int64_t row, int64_t head, int64_t rows, int64_t heads, int64_t D, int64_t ofs) {
-  if (ofs == 0 && rows > 1 && row < D) return true;
-  for (int64_t dh = 1 - heads; dh < heads; ++dh) {
-    if (ofs == 0 && dh == 0) continue;
-    const int64_t to = ofs + dh * head;  // less the dr rows that come nearest to it
-    const int64_t dr = row > 0 ? std::clamp(to / row, 1 - rows, rows - 1) : 0;
-    for (int64_t x = std::max(dr - 1, 1 - rows); x <= std::min(dr + 1, rows - 1); ++x)
-      if (std::abs(to - x * row) < D) return true;
-  }
-  return false;
-}
-
-// out [rows][heads][D] against itself and against q of the same shape.  What is plainly apart
-// is not looked into: rows that hold their heads, operands in different memory or in columns of
-// one tensor's rows.  (Operands of different strides that share memory are left to the caller.)
-qg_status check_overlap(const KvRows& q, const KvRows& out, int64_t rows, int64_t heads, int64_t D) {
-  const int64_t ow = (heads - 1) * out.head + D, qw = (heads - 1) * q.head + D;  // a row's extent
-  const bool nested = (heads == 1 || out.head >= D) && (rows == 1 || out.row >= ow);
-  if (!nested && runs_meet(out.row, out.head, rows, heads, D, 0))
-    return fail(QG_ERR_INVALID_ARG, "out: strides %lld, %lld: rows or heads overlap", (long long)out.row, (long long)out.head);
-  const int64_t ofs = (int64_t)((intptr_t)out.ptr - (intptr_t)q.ptr) / 2;
-  if (ofs >= (rows - 1) * q.row + qw || -ofs >= (rows - 1) * out.row + ow) return QG_OK;
-  if (rows > 1 && q.row == out.row && q.row > 0) {
-    const int64_t at = (ofs % q.row + q.row) % q.row;
-    if (at >= qw && at + ow <= q.row) return QG_OK;
-  }
-  if (ofs == 0 || ((rows == 1 || q.row == out.row) && (heads == 1 || q.head == out.head) &&
-                   runs_meet(q.row, q.head, rows, heads, D, ofs)))
-    return fail(QG_ERR_INVALID_ARG, "out overlaps q");
-  return QG_OK;
+  *out = KvRows{static_cast<const uint16_t*>(r->ptr), rows > 1 ? r->row_stride : 0, heads > 1 ? r->head_stride : 0};
+  return check_strides(name, out->row, out->head);
 }
 
 }  // namespace
@@ -291,6 +254,42 @@ qg_status qgkv_append(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const
   return done(h, launch_kv_append(c, bd, kr, vr, h->pool.head + 2, h->pool.info, h->d.head_dim, st), st);
 }
 
+qg_status qgkv_append_rotary(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const qg_kv_rows* k, const qg_kv_rows* v,
+                             const qg_kv_rows* q, const qg_kv_rows* q_out, int32_t q_heads, const qgs_rotary* rotary,
+                             void* stream) {
+  qg_status s = check_handle(h);
+  RotAppend a{};
+  if (s == QG_OK) s = batch_of(h, layer, b, &a.c, &a.b);
+  if (s == QG_OK) s = rotary_of(rotary, h->d.head_dim, &a.r);
+  if (s == QG_OK && q_heads < 0) s = fail(QG_ERR_INVALID_ARG, "q_heads = %d is negative", q_heads);
+  if (s == QG_OK && a.b.rows == 0) return QG_OK;
+  const int D = h ? h->d.head_dim : 0;
+  const int64_t rows = a.b.rows, kvh = a.c.kv_heads;
+  if (s == QG_OK) s = rows_of(k, "k", rows, kvh, &a.k);
+  if (s == QG_OK) s = rows_of(v, "v", rows, kvh, &a.v);
+  if (s == QG_OK && q_heads > 0) {
+    s = rows_of(q, "q", rows, q_heads, &a.q);
+    if (s == QG_OK) s = rows_of(q_out, "q_out", rows, q_heads, &a.out);
+    if (s == QG_OK) {
+      // in place, or apart; and never over k or v, which other workgroups read
+      if (a.q.ptr == a.out.ptr && a.q.row == a.out.row && a.q.head == a.out.head)
+        s = check_nested(a.out, rows, q_heads, D);
+      else
+        s = check_overlap(a.q, a.out, rows, q_heads, D, "q_out overlaps q");
+    }
+    if (s == QG_OK && (!apart(a.out, q_heads, a.k, kvh, rows, D) || !apart(a.out, q_heads, a.v, kvh, rows, D)))
+      s = fail(QG_ERR_INVALID_ARG, "q_out overlaps k or v");
+  }
+  if (s != QG_OK) return s;
+  a.q_heads = q_heads;
+  if ((int64_t)a.b.max_rows * (D / 16) * (q_heads + 2 * kvh) >= (int64_t)1 << 31)
+    return fail(QG_ERR_UNSUPPORTED, "%d rows of %d heads in one call", a.b.max_rows, q_heads + 2 * (int)kvh);
+  a.refused = h->pool.head + 2;
+  a.info = h->pool.info;
+  hipStream_t st = (hipStream_t)stream;
+  return done(h, launch_kv_append_rotary(a, D, h->d.dtype == QG_KV_BF16, h->cus, st), st);
+}
+
 qg_status qgkv_attend(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const qg_kv_rows* q, const qg_kv_rows* out,
                       int32_t q_heads, float scale, int32_t window, int32_t sinks, void* stream) {
   qg_status s = check_handle(h);
@@ -307,7 +306,7 @@ qg_status qgkv_attend(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const
   a.G = q_heads / a.c.kv_heads;
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
   if (!std::isfinite(a.scale_log2)) return fail(QG_ERR_INVALID_ARG, "scale = %g is too large", scale);
-  s = check_overlap(a.q, a.out, a.b.rows, q_heads, h->d.head_dim);
+  s = check_overlap(a.q, a.out, a.b.rows, q_heads, h->d.head_dim, "out overlaps q");
   if (s != QG_OK) return s;
   a.window = window;
   a.sinks = sinks;

@@ -43,9 +43,10 @@ def bind(L) -> None:
     L.qgkv_trim.argtypes = [vp, vp, vp, i32, vp]
     L.qgkv_compact.argtypes = [vp, vp]
     L.qgkv_append.argtypes = [vp, i32, ctypes.POINTER(_KvBatch), ctypes.POINTER(_KvRows), ctypes.POINTER(_KvRows), vp]
+    L.qgkv_append_rotary.argtypes = [vp, i32, ctypes.POINTER(_KvBatch)] + [ctypes.POINTER(_KvRows)] * 4 + [i32, vp, vp]
     L.qgkv_attend.argtypes = [vp, i32, ctypes.POINTER(_KvBatch), ctypes.POINTER(_KvRows), ctypes.POINTER(_KvRows), i32,
                               ctypes.c_float, i32, i32, vp]
-    for f in ("create", "destroy", "extend", "fork", "trim", "compact", "append", "attend"):
+    for f in ("create", "destroy", "extend", "fork", "trim", "compact", "append", "append_rotary", "attend"):
         getattr(L, "qgkv_" + f).restype = ctypes.c_int
 
 
@@ -125,13 +126,14 @@ class KVCache:
         # what a call needs besides its tensors, made once: the bound functions, the
         # argument blocks (calls on one cache are ordered by the caller), the device
         L = lib()
-        self._c = {n: getattr(L, "qgkv_" + n) for n in ("extend", "fork", "trim", "compact", "append", "attend")}
+        self._c = {n: getattr(L, "qgkv_" + n) for n in ("extend", "fork", "trim", "compact", "append", "append_rotary",
+                                                         "attend")}
         self._check = _check
         self._torch = torch
         self._dev = pool.get_device()
         self._dtype = pool.dtype
         self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        self._args = (_KvBatch(), _KvRows(), _KvRows())
+        self._args = (_KvBatch(), _KvRows(), _KvRows(), _KvRows(), _KvRows())
         self._refs = tuple(ctypes.byref(x) for x in self._args)
 
     @property
@@ -238,13 +240,40 @@ class KVCache:
         """Write the rows' keys and values, [rows][kv_heads][head_dim] each.  Which
         slots: see the class; one slot takes one entry of a call."""
         st = self._on(stream)
-        _, ka, va = self._args
+        _, ka, va = self._args[:3]
         rows, _ = self._rows(ka, "k", k, self.kv_heads)
         self._rows(va, "v", v, self.kv_heads, rows)
         held = self._batch(rows, seqs, row_start, max_rows, stream)
-        rb, rk, rv = self._refs
+        rb, rk, rv = self._refs[:3]
         self._call("append", layer, rb, rk, rv, st)
         del held
+
+    def append_rotated(self, q, k, v, rotary, *, layer: int = 0, seqs=None, row_start=None, max_rows: int = None, out=None,
+                       stream=None):
+        """``append`` with rotary positions: each row's k is rotated to its position in its
+        slot on its way into the page, and its q [rows][q_heads][head_dim] into out, which
+        is returned (out may be q; q None: keys and values only).  rotary: a ``Rotary`` on
+        the cache's GPU.  out of a row at a position before 0 (an idle slot's) is 0."""
+        st = self._on(stream)
+        _, ka, va, qa, oa = self._args
+        rows, _ = self._rows(ka, "k", k, self.kv_heads)
+        self._rows(va, "v", v, self.kv_heads, rows)
+        if rotary.turns.get_device() != self._dev:
+            raise ValueError(f"the frequencies are on {rotary.turns.device}, the cache on {self.pool.device}")
+        heads = 0
+        if q is not None:
+            _, heads = self._rows(qa, "q", q, None, rows)
+            if out is None:
+                with _on(stream):
+                    out = self._torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            self._rows(oa, "out", out, heads, rows)
+        elif out is not None:
+            raise ValueError("out without q")
+        held = self._batch(rows, seqs, row_start, max_rows, stream)
+        rb, rk, rv, rq, ro = self._refs
+        self._call("append_rotary", layer, rb, rk, rv, rq, ro, heads, rotary._ref, st)
+        del held
+        return out
 
     def attend(self, q, *, layer: int = 0, seqs=None, row_start=None, max_rows: int = None, scale: float = None,
                window: int = 0, sinks: int = 0, out=None, stream=None):
@@ -253,14 +282,14 @@ class KVCache:
         window: a row sees its last ``window`` tokens (0: all) and the first
         ``sinks`` of its slot.  Which slots the rows are of: see the class."""
         st = self._on(stream)
-        _, qa, oa = self._args
+        _, qa, oa = self._args[:3]
         rows, heads = self._rows(qa, "q", q)
         if out is None:
             with _on(stream):
                 out = self._torch.empty(q.shape, dtype=q.dtype, device=q.device)
         self._rows(oa, "out", out, heads, rows)
         held = self._batch(rows, seqs, row_start, max_rows, stream)
-        rb, rq, ro = self._refs
+        rb, rq, ro = self._refs[:3]
         self._call("attend", layer, rb, rq, ro, heads, self.head_dim ** -0.5 if scale is None else scale, window, sinks, st)
         del held
         return out

@@ -63,6 +63,7 @@
 #define QGKV_H
 
 #include "qgemv.h"
+#include "qgstep.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -156,6 +157,17 @@ qg_status qgkv_compact(qg_kv_handle h, void* stream);
  * places are then other tokens'. */
 qg_status qgkv_append(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const qg_kv_rows* k, const qg_kv_rows* v,
                       void* stream);
+
+/* The same with rotary positions (qgstep.h): a row's k is rotated to its position on its
+ * way into the page, v written as it is, and its q (q_heads heads; 0: none, q and q_out are not
+ * looked at) rotated into q_out, [rows][q_heads][head_dim].  q_out may be q (same
+ * pointer and strides), and otherwise overlaps neither q nor itself; it never
+ * overlaps k or v, but may lie in other columns of the same rows.  q_out of a row at a
+ * position before 0 is 0; rows of no entry, or left out by max_rows, keep theirs.  While a
+ * refused qgkv_extend stands only q_out is written. */
+qg_status qgkv_append_rotary(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const qg_kv_rows* k, const qg_kv_rows* v,
+                             const qg_kv_rows* q, const qg_kv_rows* q_out, int32_t q_heads, const qgs_rotary* rotary,
+                             void* stream);
 
 /* out = attention of q over the cached tokens of one layer: q and out are
  * [rows][q_heads][head_dim], q_heads a multiple of kv_heads; scale > 0;
