@@ -23,6 +23,10 @@
 namespace qg {
 
 constexpr float AT_FP16_TOP = 15.0f;
+// many rows: the exponent that a weight may reach above the running maximum, and what is added to it
+// for the matrix cores' sake (AT_FP16_TOP)
+template <bool BF> constexpr float RW_SLACK = BF ? 8.0f : 4.0f;
+template <bool BF> constexpr float RW_BIAS = BF ? 0.0f : AT_FP16_TOP - RW_SLACK<BF>;
 
 typedef _Float16 at_h8 __attribute__((ext_vector_type(8)));
 typedef __bf16 at_b8 __attribute__((ext_vector_type(8)));
@@ -159,6 +163,38 @@ __device__ __forceinline__ void at_store(const AttnArgs& a, const KvEntry& e, in
   }
 }
 
+// The result of an entry's shared tokens, as a partial: row r of a kv head is at place
+// row + r among the blocks' rows, (block * heads + head) the slot of the block.  add: what
+// the exponents of this kernel's weights have more than those of the many-row kernel
+// that made it, so that both mean the same.
+struct AtNoExtra {
+  static constexpr bool some = false;
+  __device__ __forceinline__ at_f2 ml(int) const { return at_f2{0, 0}; }
+  __device__ __forceinline__ at_f4 o(int, int) const { return at_f4{0, 0, 0, 0}; }
+};
+template <int D> struct AtPrefix {
+  static constexpr bool some = true;
+  __amdgpu_buffer_rsrc_t rs;
+  int row, heads, head;
+  float add;
+  bool there;  // else the entry shares nothing
+  __device__ __forceinline__ AtPrefix(const AttnArgs& a, const ShareEntry& s, int head_, float add_)
+      : rs(at_slots(a.prefix, a.prefix_floats)), row(s.row), heads(a.c.kv_heads), head(head_), add(add_), there(s.tokens > 0) {}
+  __device__ __forceinline__ uint32_t slot(int r) const {
+    return ((uint32_t)((row + r) / ROWS_BLOCK) * heads + head) * (uint32_t)rows_slot(D);
+  }
+  __device__ __forceinline__ at_f2 ml(int r) const {
+    at_f2 v = {-__builtin_inff(), 0.0f};
+    if (there) v = at_ld2(rs, slot(r) + ROWS_BLOCK * D + 2 * ((row + r) % ROWS_BLOCK));
+    return at_f2{v.x + add, v.y};
+  }
+  __device__ __forceinline__ at_f4 o(int r, int c) const {
+    at_f4 v = {0, 0, 0, 0};
+    if (there) v = at_ld4(rs, slot(r) + (uint32_t)((row + r) % ROWS_BLOCK) * D + c);
+    return v;
+  }
+};
+
 // Join n partials of rows f0 .. f0 + nrows - 1 of a block of (entry, head) that begins
 // with row r0; slot(k) is where the k-th lies (in floats): [ld][D] fp32, then (m, l) of each row.  Every sum runs in an
 // order that n fixes.
@@ -169,9 +205,12 @@ __device__ __forceinline__ void at_store(const AttnArgs& a, const KvEntry& e, in
 // of four columns, each with a contiguous part of the partials.
 // fac, tot, part: AT_JOIN_CAP floats of LDS each; n <= AT_JOIN_CAP.
 constexpr int AT_JOIN_CAP = 2720;  // (row, partial) pairs at a time; 4 floats of 512 threads fit as well
-template <bool BF, int D, int THREADS, class F>
+//
+// extra: a partial of the rows' shared tokens comes to these, the last one of the order.
+template <bool BF, int D, int THREADS, class F, class X = AtNoExtra>
 __device__ __forceinline__ void at_join(const AttnArgs& a, __amdgpu_buffer_rsrc_t rs, const KvEntry& e, int head, int r0, int f0,
-                                        int nrows, int ld, int n, float* fac, float* tot, float* part, F slot) {
+                                        int nrows, int ld, int own, float* fac, float* tot, float* part, F slot, X extra = X()) {
+  const int n = own + (X::some ? 1 : 0);
   constexpr int NB = 16, NW = THREADS / 64;
   static_assert(4 * THREADS <= AT_JOIN_CAP, "part");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -183,7 +222,9 @@ __device__ __forceinline__ void at_join(const AttnArgs& a, __amdgpu_buffer_rsrc_
     __syncthreads();
     for (int x = tid; x < rows * n; x += THREADS) {
       const int r = x / n, k = x - r * n;
-      const at_f2 ml = at_ld2(rs, slot(k) + (uint32_t)ld * D + 2 * (rb + r));
+      at_f2 ml;
+      if (X::some && k == own) ml = extra.ml(r0 + rb + r);
+      else ml = at_ld2(rs, slot(k) + (uint32_t)ld * D + 2 * (rb + r));
       fac[x] = ml.x;
       tot[x] = ml.y;
     }
@@ -218,7 +259,10 @@ __device__ __forceinline__ void at_join(const AttnArgs& a, __amdgpu_buffer_rsrc_
           at_f4 po[NB];
 #pragma unroll
           for (int k = 0; k < NB; ++k)
-            if (kb + k < k1) po[k] = at_ld4(rs, at + slot(kb + k));
+            if (kb + k < k1) {
+              if (X::some && kb + k == own) po[k] = extra.o(r0 + rb + r, c);
+              else po[k] = at_ld4(rs, at + slot(kb + k));
+            }
 #pragma unroll
           for (int k = 0; k < NB; ++k)
             if (kb + k < k1) {
@@ -260,6 +304,8 @@ template <int TK> struct TileRange {
     n = max(end - skip, 0);
   }
   __device__ __forceinline__ int at(int j) const { return j < ns ? j : j + skip; }
+  // how many of the tiles lie before tile t of the slot
+  __device__ __forceinline__ int before(int t) const { return min(t <= ns ? t : max(ns, t - skip), n); }
 };
 
 // does the row at position pos see token t?

@@ -53,10 +53,6 @@ __host__ __device__ constexpr int rw_parts(int tiles, int splits1) {
   const int few = tiles / RW_MIN_TILES < splits1 ? tiles / RW_MIN_TILES : splits1;
   return few > tiles / RW_LONG_TILES ? few : tiles / RW_LONG_TILES;
 }
-// the exponent that a weight may reach above the running maximum, and what is added to it
-// for the matrix cores' sake (AT_FP16_TOP)
-template <bool BF> constexpr float RW_SLACK = BF ? 8.0f : 4.0f;
-template <bool BF> constexpr float RW_BIAS = BF ? 0.0f : AT_FP16_TOP - RW_SLACK<BF>;
 // operands read from LDS ahead of the product that takes them: 4 where there are
 // registers for them (8,191 tokens, heads of 128: 691 us at 4, 689 at 2, 728 at 1), 1 where
 // there are none (8,192 tokens, 16 q and 4 kv heads of 256: 661 us at 1, 685 at 2, 742 at
@@ -278,15 +274,18 @@ __device__ __forceinline__ void rw_products(RowsState<D>& r, const RowsWeights<D
 // A block of the call.  Longest first: the last block of every (entry, kv head), then
 // the one before, ...; kv heads fastest, so that with 8 of them (or a multiple) a
 // head's blocks meet its tokens in one XCD's L2.
-template <int D> struct RowsBlock {
+enum { RW_WHOLE = 0, RW_PREFIX = 1, RW_REST = 2 };  // all tokens; a group's shared ones; an entry's others
+template <int D, int MODE = RW_WHOLE> struct RowsBlock {
   using S = RowsShape<D>;
   int head, rb, total, r0, nrows, pe, p0, p1, parts;  // rb < 0: none; parts that share its tiles
+  int cut = 0;  // tiles of the list that are others' to compute
   KvEntry e;
+  ShareEntry shared;
   TileRange<S::KT> tr;
   __device__ __forceinline__ RowsBlock(const AttnArgs& a, int id) : tr(-1, -1, 0, 0) {
     head = id % a.c.kv_heads;
-    const int back = id / (a.c.kv_heads * a.b.n);
-    e = kv_entry(a.c, a.b, (id / a.c.kv_heads) % a.b.n);
+    const int back = id / (a.c.kv_heads * a.b.n), j = (id / a.c.kv_heads) % a.b.n;
+    e = kv_entry(a.c, a.b, j);
     total = e.rows * a.G;
     rb = (total + S::BM - 1) / S::BM - 1 - back;
     if (rb < 0) return;
@@ -294,11 +293,35 @@ template <int D> struct RowsBlock {
     pe = e.pos;
     p0 = pe + r0 / a.G, p1 = pe + (r0 + nrows - 1) / a.G;
     tr = TileRange<S::KT>(p0, p1, a.window, a.sinks);
+    if constexpr (MODE == RW_REST) {
+      shared = a.share[j];
+      cut = tr.before(shared.tokens / S::KT);
+    }
+    parts = max(min(a.splits, rw_parts(tr.n - cut, a.splits1)), 1);
+  }
+};
+// a block of a group's rows with its shared tokens
+template <int D> struct RowsBlock<D, RW_PREFIX> {
+  using S = RowsShape<D>;
+  int head, rb, total, r0, nrows, pe, p0, p1, parts;
+  static constexpr int cut = 0;
+  KvEntry e;
+  TileRange<S::KT> tr;
+  __device__ __forceinline__ RowsBlock(const AttnArgs& a, int id) : tr(-1, -1, 0, 0) {
+    head = id % a.c.kv_heads;
+    const ShareBlock s = a.share_blocks[id / a.c.kv_heads];
+    rb = s.tokens > 0 ? 0 : -1;
+    if (rb < 0) return;
+    r0 = s.r0, total = s.total, nrows = min(total - r0, S::BM);
+    pe = 0, p0 = s.p0, p1 = s.p1;
+    e = KvEntry{s.slot, 0, s.row0, total / a.G};
+    tr = TileRange<S::KT>(p0, p1, a.window, a.sinks);
+    tr.n = tr.before(s.tokens / S::KT);
     parts = max(min(a.splits, rw_parts(tr.n, a.splits1)), 1);
   }
 };
 
-template <int D, bool BF>
+template <int D, bool BF, int MODE = RW_WHOLE>
 __global__ __launch_bounds__(64 * ROWS_WAVES) __attribute__((amdgpu_waves_per_eu(D == 64 ? 3 : 2)))
 void k_attn_rows(AttnArgs a) {
   using S = RowsShape<D>;
@@ -314,12 +337,13 @@ void k_attn_rows(AttnArgs a) {
   // 36 with parts fastest)
   const unsigned blocks = gridDim.x / (unsigned)a.splits;
   const int z = blockIdx.x / blocks;
-  const RowsBlock<D> blk(a, a.first + (int)(blockIdx.x - z * blocks));
+  const RowsBlock<D, MODE> blk(a, a.first + (int)(blockIdx.x - z * blocks));
   if (blk.rb < 0 || z >= blk.parts) return;
   const KvEntry& e = blk.e;
   const TileRange<S::KT>& tr = blk.tr;
   const int head = blk.head, total = blk.total, r0 = blk.r0, pe = blk.pe, p0 = blk.p0, p1 = blk.p1, parts = blk.parts;
-  const int t0 = (int)((int64_t)tr.n * z / parts), t1 = (int)((int64_t)tr.n * (z + 1) / parts);
+  const int tiles = tr.n - blk.cut;
+  const int t0 = blk.cut + (int)((int64_t)tiles * z / parts), t1 = blk.cut + (int)((int64_t)tiles * (z + 1) / parts);
   const int32_t* table = a.c.tables + (int64_t)e.slot * a.c.max_pages;
 
   // this wave's rows
@@ -327,8 +351,17 @@ void k_attn_rows(AttnArgs a) {
   const int rw = r0 + wave * 32 + col;
   const bool live = rw < total, alive = r0 + wave * 32 < total;
   const int ri = live ? rw / a.G : 0;
-  r.pos = live ? pe + ri : -1;
-  const int pw0 = pe + (r0 + wave * 32) / a.G, pw1 = min(pe + (r0 + wave * 32 + 31) / a.G, p1);
+  int pw0, pw1;  // first and last position of the wave's rows
+  if constexpr (MODE == RW_PREFIX) {  // rows of many entries: -1 for those that see nothing
+    r.pos = live ? min(max(a.share_pos[e.row0 + ri], -1), p1) : -1;  // (a row that max_rows leaves out has none)
+    pw0 = live ? r.pos : 0x7FFFFFFF, pw1 = r.pos;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) pw0 = min(pw0, __shfl_xor(pw0, o)), pw1 = max(pw1, __shfl_xor(pw1, o));
+    pw0 = __builtin_amdgcn_readfirstlane(pw0), pw1 = __builtin_amdgcn_readfirstlane(pw1);
+  } else {
+    r.pos = live ? pe + ri : -1;
+    pw0 = pe + (r0 + wave * 32) / a.G, pw1 = min(pe + (r0 + wave * 32 + 31) / a.G, p1);
+  }
   {
     const uint16_t* qp = a.q.ptr + (int64_t)(e.row0 + ri) * a.q.row +
                          (int64_t)(head * a.G + (live ? rw - ri * a.G : 0)) * a.q.head + h * 8;
@@ -464,8 +497,23 @@ void k_attn_rows(AttnArgs a) {
   }
 
   r.l += __shfl_xor(r.l, 32);
-  if (parts == 1) {
+  if (MODE != RW_PREFIX && parts == 1) {
     if (live) {
+      if constexpr (MODE == RW_REST) {
+        const AtPrefix<D> p(a, blk.shared, head, 0.0f);
+        const at_f2 ml = p.ml(rw);
+        const float m = r.m * a.scale_log2, M = at_safe(fmaxf(m, ml.x));
+        const float f = at_exp2(m - M), g = at_exp2(ml.x - M);
+        r.l = f * r.l + g * ml.y;
+#pragma unroll
+        for (int x = 0; x < S::ND; ++x)
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const at_f4 v = p.o(rw, x * 32 + 2 * i + 4 * h);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) r.O[x][i + k] = f * r.O[x][i + k] + g * v[k];
+          }
+      }
 #pragma unroll
       for (int x = 0; x < S::ND; ++x)
 #pragma unroll
@@ -494,17 +542,22 @@ void k_attn_rows(AttnArgs a) {
 // of a block's partials alone.  The last 16 rows of 16,384 tokens, 40 q and 8 kv heads of
 // 128: 40 us against 97 in the same parts; a prompt of 1,024 tokens: 33 against 94.
 constexpr int RJ_ROWS = 8, RJ_THREADS = 256;
-template <int D, bool BF> __global__ __launch_bounds__(RJ_THREADS) void k_attn_rows_join(AttnArgs a) {
+template <int D, bool BF, int MODE = RW_WHOLE> __global__ __launch_bounds__(RJ_THREADS) void k_attn_rows_join(AttnArgs a) {
   using S = RowsShape<D>;
   __shared__ __align__(16) float lds[3 * AT_JOIN_CAP];
   constexpr int PER = S::BM / RJ_ROWS;
   const unsigned id = blockIdx.x / PER, blocks = gridDim.x / PER;
-  const RowsBlock<D> b(a, id);
+  const RowsBlock<D, MODE> b(a, id);
   const int f0 = (blockIdx.x % PER) * RJ_ROWS;
   if (b.rb < 0 || b.parts == 1 || f0 >= b.nrows) return;
-  at_join<BF, D, RJ_THREADS>(a, at_slots(a.partial, a.partial_floats), b.e, b.head, b.r0, f0, min(b.nrows - f0, RJ_ROWS), S::BM,
-                             b.parts, lds, lds + AT_JOIN_CAP, lds + 2 * AT_JOIN_CAP,
-                             [&](int k) { return (k * blocks + id) * (uint32_t)rows_slot(D); });
+  const auto slot = [&](int k) { return (k * blocks + id) * (uint32_t)rows_slot(D); };
+  const int n = min(b.nrows - f0, RJ_ROWS);
+  if constexpr (MODE == RW_REST)
+    at_join<BF, D, RJ_THREADS>(a, at_slots(a.partial, a.partial_floats), b.e, b.head, b.r0, f0, n, S::BM, b.parts, lds,
+                               lds + AT_JOIN_CAP, lds + 2 * AT_JOIN_CAP, slot, AtPrefix<D>(a, b.shared, b.head, 0.0f));
+  else
+    at_join<BF, D, RJ_THREADS>(a, at_slots(a.partial, a.partial_floats), b.e, b.head, b.r0, f0, n, S::BM, b.parts, lds,
+                               lds + AT_JOIN_CAP, lds + 2 * AT_JOIN_CAP, slot);
 }
 
 }  // namespace qg

@@ -49,6 +49,8 @@ constexpr int ST_TK = 32;  // tokens of a tile
 constexpr int ST_COST = 16;
 // added to a weight's exponent, at most 0, for the matrix cores' sake
 template <bool BF> constexpr float ST_BIAS = BF ? 0.0f : AT_FP16_TOP;
+// and what that is more than the many-row kernel's, whose results of shared tokens are joined
+template <bool BF> constexpr float AT_SHARE_ADD = ST_BIAS<BF> - RW_BIAS<BF>;
 
 template <int D, int MT = 1> struct StepShape {
   static constexpr int NW = step_waves(D);       // waves of a workgroup
@@ -157,7 +159,9 @@ template <int D> __device__ __forceinline__ int step_col(int q, int i, int x) {
   return (x / (S::VB / 2)) * 128 + (q * 4 + i) * (S::VB / 2) + x % (S::VB / 2);
 }
 
-template <int D, bool BF, int MT>
+// SH: the tokens that an entry shares with its group are not computed here, but their
+// result (qg_attn_share.h) is joined with that of its other tokens.
+template <int D, bool BF, int MT, bool SH>
 __global__ __launch_bounds__(64 * step_waves(D)) __attribute__((amdgpu_waves_per_eu(step_waves(D) / 4)))
 void k_attn_step(AttnArgs a) {
   using S = StepShape<D, MT>;
@@ -189,7 +193,11 @@ void k_attn_step(AttnArgs a) {
       if (j < n) {
         const KvEntry e = kv_entry(a.c, a.b, j);
         list[j] = e;
-        if (e.rows > 0) t = ST_COST + max(TileRange<ST_TK>(e.pos, e.pos + e.rows - 1, a.window, a.sinks).n, 1);
+        if (e.rows > 0) {
+          const TileRange<ST_TK> tr(e.pos, e.pos + e.rows - 1, a.window, a.sinks);
+          if constexpr (SH) t = ST_COST + max(tr.n - tr.before(a.share[j].tokens / ST_TK), 1);
+          else t = ST_COST + max(tr.n, 1);
+        }
       }
       int x = t;
 #pragma unroll
@@ -241,6 +249,13 @@ void k_attn_step(AttnArgs a) {
     e.row0 = __builtin_amdgcn_readfirstlane(e.row0), e.rows = __builtin_amdgcn_readfirstlane(e.rows);
     const int p0 = e.pos, p1 = p0 + e.rows - 1, nrows = e.rows * a.G;
     const TileRange<ST_TK> tr(p0, p1, a.window, a.sinks);
+    ShareEntry shared{};
+    int cut = 0;  // tiles of shared tokens
+    if constexpr (SH) {
+      shared = a.share[j];
+      shared.tokens = __builtin_amdgcn_readfirstlane(shared.tokens), shared.row = __builtin_amdgcn_readfirstlane(shared.row);
+      cut = tr.before(shared.tokens / ST_TK);
+    }
     const int32_t* table = a.c.tables + (int64_t)e.slot * a.c.max_pages;
 
     // the rows of this kv head: row r is new token r / G, q head head * G + r % G
@@ -274,8 +289,8 @@ void k_attn_step(AttnArgs a) {
     int tl = t0 + wave;
     StepPages pg;
     StepIds ids;  // of the tile after the one whose keys and values are on their way
-    const bool any = tr.n > 0;  // else the one tile of an entry that sees nothing
-    const auto token = [&](int i) { return tr.at(min(i, t1 - 1)) * ST_TK; };
+    const bool any = tr.n > cut;  // else the one tile of an entry that sees nothing (more)
+    const auto token = [&](int i) { return tr.at(min(i, t1 - 1) + cut) * ST_TK; };
     if (any && tl < t1) {
       ids = step_ids(a.c, table, token(tl), p1);
       pg = step_pages(a.c, ids, token(tl), head, D, true);
@@ -442,6 +457,17 @@ void k_attn_step(AttnArgs a) {
       const int r = mt * 16 + row;
       if (r < nrows) {
         float M = -__builtin_inff(), L = 0.0f, o[CW];
+        at_f2 pml = {-__builtin_inff(), 0.0f};
+        at_f4 po[(CW + 3) / 4];
+        if constexpr (SH) {
+          if (whole) {
+            const AtPrefix<D> pre(a, shared, head, AT_SHARE_ADD<BF>);
+            pml = pre.ml(r);
+            M = pml.x;
+#pragma unroll
+            for (int x = 0; x < CW; x += 4) po[x / 4] = pre.o(r, c0 + x - (CW < 4 ? c0 & 3 : 0));
+          }
+        }
 #pragma unroll
         for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[(w * 16 + row) * 2]);
 #pragma unroll
@@ -454,6 +480,12 @@ void k_attn_step(AttnArgs a) {
           for (int x = 0; x < CW; ++x) o[x] = __builtin_fmaf(f, buf[(w * 16 + row) * S::LD + c0 + x], o[x]);
         }
         if (whole) {
+          if constexpr (SH) {
+            const float f = at_exp2(pml.x - at_safe(M));
+            L += f * pml.y;
+#pragma unroll
+            for (int x = 0; x < CW; ++x) o[x] = __builtin_fmaf(f, po[x / 4][CW < 4 ? (c0 & 3) + x : x & 3], o[x]);
+          }
           at_store<BF, CW>(a, e, head, r, c0, o, L);
         } else {
 #pragma unroll
@@ -470,9 +502,12 @@ void k_attn_step(AttnArgs a) {
     // several workgroups share (entry, head): the last to arrive joins them, in list order
     const int w0 = tile0 / per, parts = (tile0 + nt - 1) / per - w0 + 1;
     if (!at_last(a.counters + j * heads + head, parts, flag)) continue;
-    at_join<BF, D, 64 * NW>(a, rs, e, head, 0, 0, nrows, MT * 16, parts, buf, buf + AT_JOIN_CAP, buf + 2 * AT_JOIN_CAP, [&](int k) {
-      return (uint32_t)(2 * (w0 + k) + (k == 0 ? 1 : 0)) * (uint32_t)step_slot(MT, D);
-    });
+    const auto part = [&](int k) { return (uint32_t)(2 * (w0 + k) + (k == 0 ? 1 : 0)) * (uint32_t)step_slot(MT, D); };
+    if constexpr (SH)
+      at_join<BF, D, 64 * NW>(a, rs, e, head, 0, 0, nrows, MT * 16, parts, buf, buf + AT_JOIN_CAP, buf + 2 * AT_JOIN_CAP, part,
+                              AtPrefix<D>(a, shared, head, AT_SHARE_ADD<BF>));
+    else
+      at_join<BF, D, 64 * NW>(a, rs, e, head, 0, 0, nrows, MT * 16, parts, buf, buf + AT_JOIN_CAP, buf + 2 * AT_JOIN_CAP, part);
     __syncthreads();  // the join's use of the buffer is over
   }
 }

@@ -109,6 +109,20 @@ struct RotAppend {
 hipError_t launch_kv_append_rotary(const RotAppend& a, int D, bool bf16, int cus, hipStream_t st);
 
 // ---- attention ---------------------------------------------------------------
+// What the entries of a group share, as the plan kernel (qg_attn_share.h) has found it.
+struct ShareEntry {
+  int tokens;  // the entry's first tokens that its group's blocks cover (0: none)
+  int row;     // place of its first (row, q head of a kv head) among the blocks' rows
+};
+struct ShareBlock {  // ROWS_BLOCK of a group's rows of a kv head
+  int tokens;  // 0: no block
+  int slot;    // whose table names the shared pages
+  int row0;    // the group's first row of the call
+  int r0;      // the block's first place among the group's rows, of
+  int total;   // (rows) * (q heads per kv head)
+  int p0, p1;  // first and last position of rows that see something
+};
+
 struct AttnArgs {
   KvDev c;
   KvBatchDev b;
@@ -123,7 +137,30 @@ struct AttnArgs {
   int min_run;         // and places of their list that each takes at least
   int splits, splits1; // many rows: workgroups that may share a block's tiles, however many it has; and if few
   int first;           // many rows: the launch's first block (0 where blocks are shared)
+  // shared tokens: what the plan has found, the rows' positions, and the blocks' results
+  const ShareEntry* share;
+  const ShareBlock* share_blocks;
+  const int* share_pos;
+  float* prefix;
+  size_t prefix_floats;
 };
+
+// the plan of a call whose entries share tokens
+struct ShareArgs {
+  KvDev c;
+  KvBatchDev b;
+  const int32_t* groups;  // first entries of the groups and n (NULL: one group)
+  int ngroups, G, blocks; // blocks: ShareBlocks that the call has room for
+  ShareEntry* share;
+  ShareBlock* share_blocks;
+  int* pos;               // [row]
+  int2* want;             // [entry] tokens that the entry has in common with its group's first, and its group
+  int* counter;           // zero between launches
+};
+constexpr int SHARE_ROWS = 1 << 16;  // rows of a call that share tokens at most
+// shared tokens come in whole tiles of both kernels, and few of them are left to the entries
+constexpr int SHARE_TILE = 64, SHARE_MIN = 256;
+hipError_t launch_share_plan(const ShareArgs& a, hipStream_t st);
 
 // Rows of one kv head that the few-row kernel takes, (new rows) * (q heads per kv head).
 // us of the few-row and of the many-row kernel, fp16, 8 kv heads of 128 (2 of 256):
@@ -144,7 +181,8 @@ __host__ __device__ constexpr int step_waves(int D) { return D == 256 ? 4 : 8; }
 constexpr int STEP_MIN_RUN = 12;
 // fp32 words of one partial of MT row tiles: o, then (max, sum) of each row
 __host__ __device__ constexpr size_t step_slot(int MT, int D) { return (size_t)MT * 16 * (D + 2); }
-hipError_t launch_attn_step(const AttnArgs& a, int D, bool bf16, int MT, hipStream_t st);
+// shared: the entries' first tokens are in a.prefix
+hipError_t launch_attn_step(const AttnArgs& a, int D, bool bf16, int MT, bool shared, hipStream_t st);
 
 // the many-row kernel: waves of a workgroup, rows of a block (32 a wave), fp32 words of
 // its partial
@@ -152,7 +190,9 @@ constexpr int ROWS_WAVES = 4, ROWS_BLOCK = 32 * ROWS_WAVES;
 __host__ __device__ constexpr size_t rows_slot(int D) { return (size_t)ROWS_BLOCK * (D + 2); }
 // parts of a block that sees every token of a slot that holds cap
 int rows_parts(int D, int cap, int splits1);
-hipError_t launch_attn_rows(const AttnArgs& a, int D, bool bf16, unsigned blocks, hipStream_t st);
+hipError_t launch_attn_rows(const AttnArgs& a, int D, bool bf16, unsigned blocks, bool shared, hipStream_t st);
+// the tokens that groups share, for all their rows, into a.prefix (blocks * splits slots of it)
+hipError_t launch_attn_prefix(const AttnArgs& a, int D, bool bf16, unsigned blocks, hipStream_t st);
 hipError_t attn_step_allow_lds();
 
 }  // namespace qg

@@ -26,6 +26,11 @@ struct qg_kv {
   int* counters = nullptr;    // arrivals, zero between launches
   int32_t* lists = nullptr;   // head | from | to | place of the page operations
   int ncounters = 0;
+  // attention of shared tokens: its blocks' results and plan
+  float* prefix = nullptr;
+  size_t prefix_floats = 0;
+  int* plan = nullptr;
+  ShareArgs share{};
 };
 
 namespace {
@@ -35,6 +40,11 @@ constexpr int kMaxPages = 1 << 20;
 // of 256 CUs where the parts are long, one where they are short
 constexpr int kRowsSlots = 512;
 
+// arrival counter | blocks | what each entry wants | entries | rows' positions
+size_t plan_bytes(int max_seqs) {
+  return 16 + kRowsSlots * sizeof(ShareBlock) + (size_t)max_seqs * (sizeof(int2) + sizeof(ShareEntry)) + SHARE_ROWS * sizeof(int);
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -43,6 +53,8 @@ void free_kv(qg_kv* h) {
   if (h->partial) hipFree(h->partial);
   if (h->counters) hipFree(h->counters);
   if (h->lists) hipFree(h->lists);
+  if (h->prefix) hipFree(h->prefix);
+  if (h->plan) hipFree(h->plan);
   delete h;
 }
 
@@ -115,6 +127,59 @@ qg_status rows_of(const qg_kv_rows* r, const char* name, int64_t rows, int64_t h
   return check_strides(name, out->row, out->head);
 }
 
+// the checked arguments of an attention call
+qg_status attn_of(qg_kv* h, int layer, const qg_kv_batch* b, const qg_kv_rows* q, const qg_kv_rows* out, int q_heads, float scale,
+                  int window, int sinks, AttnArgs* to) {
+  qg_status s = check_handle(h);
+  AttnArgs& a = *to;
+  if (s == QG_OK) s = batch_of(h, layer, b, &a.c, &a.b);
+  if (s == QG_OK && a.b.rows == 0) return QG_OK;
+  if (s == QG_OK) s = rows_of(q, "q", a.b.rows, q_heads, &a.q);
+  if (s == QG_OK) s = rows_of(out, "out", a.b.rows, q_heads, &a.out);
+  if (s != QG_OK) return s;
+  if (q_heads < 1 || q_heads % a.c.kv_heads)
+    return fail(QG_ERR_INVALID_ARG, "q_heads = %d is not a positive multiple of kv_heads = %d", q_heads, a.c.kv_heads);
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(QG_ERR_INVALID_ARG, "scale = %g is not positive and finite", scale);
+  if (window < 0 || sinks < 0) return fail(QG_ERR_INVALID_ARG, "window = %d, sinks = %d: negative", window, sinks);
+  a.G = q_heads / a.c.kv_heads;
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  if (!std::isfinite(a.scale_log2)) return fail(QG_ERR_INVALID_ARG, "scale = %g is too large", scale);
+  s = check_overlap(a.q, a.out, a.b.rows, q_heads, h->d.head_dim, "out overlaps q");
+  if (s != QG_OK) return s;
+  a.window = window;
+  a.sinks = sinks;
+  a.partial = h->partial;
+  a.partial_floats = h->partial_floats;
+  a.counters = h->counters;
+  return QG_OK;
+}
+
+// shared: the entries' first tokens have been attended to
+qg_status attend(qg_kv* h, AttnArgs& a, bool shared, hipStream_t st) {
+  const int D = h->d.head_dim;
+  const bool bf16 = h->d.dtype == QG_KV_BF16;
+  const int64_t rows = (int64_t)a.b.max_rows * a.G;  // rows of a kv head
+  if (rows >= (int64_t)1 << 30) return fail(QG_ERR_UNSUPPORTED, "%d rows of %d heads in one call", a.b.max_rows, a.G);
+  if (rows <= step_max_rows(D)) {
+    const int MT = (int)(rows + 15) / 16;
+    // places of the few-row kernel's list
+    if ((int64_t)(a.c.cap / 32 + 32) * a.b.n * a.c.kv_heads >= (int64_t)1 << 30)
+      return fail(QG_ERR_UNSUPPORTED, "%d entries of up to %d tokens and %d kv heads in one call", a.b.n, a.c.cap, a.c.kv_heads);
+    a.workers = h->cus;
+    a.min_run = STEP_MIN_RUN;
+    return done(h, launch_attn_step(a, D, bf16, MT, shared, st), st);
+  }
+  // A call of few blocks is split over the tokens until it covers the chip: once for parts
+  // of few tiles, twice for parts of many (the last 512 rows of 65,536 tokens, 40 q and 8
+  // kv heads of 128: 741 us with two, 1,507 with one; the last 16 of each of 4 slots of
+  // 8,192: 53 and 47).  A cache whose slots hold too little for parts saves the join.
+  const int64_t blocks = (rows + ROWS_BLOCK - 1) / ROWS_BLOCK * a.b.n * a.c.kv_heads;
+  a.splits1 = (int)std::max<int64_t>(1, kRowsSlots / 2 / blocks);
+  a.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kRowsSlots / blocks, rows_parts(D, a.c.cap, a.splits1)));
+  if (blocks * a.splits >= (int64_t)1 << 31) return fail(QG_ERR_UNSUPPORTED, "%lld blocks in one call", (long long)blocks);
+  return done(h, launch_attn_rows(a, D, bf16, (unsigned)blocks, shared, st), st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -165,20 +230,29 @@ qg_status qgkv_create(qg_kv_handle* out, const qg_kv_desc* d, void* stream) {
   h->partial_floats = std::max(step, rows);
   if (hipMalloc(&h->partial, h->partial_floats * sizeof(float)) != hipSuccess ||
       hipMalloc(&h->counters, (size_t)h->ncounters * sizeof(int)) != hipSuccess ||
-      hipMalloc(&h->lists, (4 + 3 * entries) * sizeof(int32_t)) != hipSuccess) {
+      hipMalloc(&h->lists, (4 + 3 * entries) * sizeof(int32_t)) != hipSuccess ||
+      hipMalloc(&h->prefix, rows * sizeof(float)) != hipSuccess || hipMalloc(&h->plan, plan_bytes(d->max_seqs)) != hipSuccess) {
     (void)hipGetLastError();
     s = fail(QG_ERR_OOM, "workspace allocation failed");
   }
   if (s == QG_OK && attn_step_allow_lds() != hipSuccess)
     s = fail(QG_ERR_DEVICE, "cannot raise the LDS limit of the kernels");
   if (s == QG_OK && (launch_fill_zero(h->counters, (int64_t)h->ncounters * sizeof(int), st) != hipSuccess ||
-                     launch_fill_zero(h->lists, 4 * sizeof(int32_t), st) != hipSuccess))
+                     launch_fill_zero(h->lists, 4 * sizeof(int32_t), st) != hipSuccess ||
+                     launch_fill_zero(h->plan, 16, st) != hipSuccess))
     s = fail(QG_ERR_DEVICE, "workspace initialisation failed");
   if (hipStreamSynchronize(st) != hipSuccess && s == QG_OK) s = fail(QG_ERR_DEVICE, "stream synchronisation failed");
   if (s != QG_OK) {
     free_kv(h);
     return s;
   }
+  h->prefix_floats = rows;
+  char* at = reinterpret_cast<char*>(h->plan);
+  h->share.counter = reinterpret_cast<int*>(at);
+  h->share.share_blocks = reinterpret_cast<ShareBlock*>(at += 16);
+  h->share.want = reinterpret_cast<int2*>(at += kRowsSlots * sizeof(ShareBlock));
+  h->share.share = reinterpret_cast<ShareEntry*>(at += d->max_seqs * sizeof(int2));
+  h->share.pos = reinterpret_cast<int*>(at += d->max_seqs * sizeof(ShareEntry));
   KvPool& p = h->pool;
   p.pool = static_cast<uint16_t*>(d->pool);
   p.tables = d->tables;
@@ -292,50 +366,49 @@ qg_status qgkv_append_rotary(qg_kv_handle h, int32_t layer, const qg_kv_batch* b
 
 qg_status qgkv_attend(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const qg_kv_rows* q, const qg_kv_rows* out,
                       int32_t q_heads, float scale, int32_t window, int32_t sinks, void* stream) {
-  qg_status s = check_handle(h);
   AttnArgs a{};
-  if (s == QG_OK) s = batch_of(h, layer, b, &a.c, &a.b);
-  if (s == QG_OK && a.b.rows == 0) return QG_OK;
-  if (s == QG_OK) s = rows_of(q, "q", a.b.rows, q_heads, &a.q);
-  if (s == QG_OK) s = rows_of(out, "out", a.b.rows, q_heads, &a.out);
-  if (s != QG_OK) return s;
-  if (q_heads < 1 || q_heads % a.c.kv_heads)
-    return fail(QG_ERR_INVALID_ARG, "q_heads = %d is not a positive multiple of kv_heads = %d", q_heads, a.c.kv_heads);
-  if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(QG_ERR_INVALID_ARG, "scale = %g is not positive and finite", scale);
-  if (window < 0 || sinks < 0) return fail(QG_ERR_INVALID_ARG, "window = %d, sinks = %d: negative", window, sinks);
-  a.G = q_heads / a.c.kv_heads;
-  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
-  if (!std::isfinite(a.scale_log2)) return fail(QG_ERR_INVALID_ARG, "scale = %g is too large", scale);
-  s = check_overlap(a.q, a.out, a.b.rows, q_heads, h->d.head_dim, "out overlaps q");
-  if (s != QG_OK) return s;
-  a.window = window;
-  a.sinks = sinks;
-  a.partial = h->partial;
-  a.partial_floats = h->partial_floats;
-  a.counters = h->counters;
-  const int D = h->d.head_dim;
-  const bool bf16 = h->d.dtype == QG_KV_BF16;
-  const int64_t rows = (int64_t)a.b.max_rows * a.G;  // rows of a kv head
-  if (rows >= (int64_t)1 << 30) return fail(QG_ERR_UNSUPPORTED, "%d rows of %d heads in one call", a.b.max_rows, a.G);
+  qg_status s = attn_of(h, layer, b, q, out, q_heads, scale, window, sinks, &a);
+  if (s != QG_OK || a.b.rows == 0) return s;
+  return attend(h, a, false, (hipStream_t)stream);
+}
+
+qg_status qgkv_attend_shared(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const qg_kv_rows* q, const qg_kv_rows* out,
+                             int32_t q_heads, float scale, int32_t window, int32_t sinks, const int32_t* groups,
+                             int32_t n_groups, void* stream) {
+  AttnArgs a{};
+  qg_status s = attn_of(h, layer, b, q, out, q_heads, scale, window, sinks, &a);
+  if (s != QG_OK || a.b.rows == 0) return s;
+  if (!aligned4(groups)) return fail(QG_ERR_INVALID_ARG, "groups must be 4-byte aligned");
+  if (groups && (n_groups < 1 || n_groups > a.b.n)) return fail(QG_ERR_INVALID_ARG, "n_groups = %d is not in [1, n = %d]", n_groups, a.b.n);
+  if (!groups) n_groups = 1;
   hipStream_t st = (hipStream_t)stream;
-  if (rows <= step_max_rows(D)) {
-    const int MT = (int)(rows + 15) / 16;
-    // places of the few-row kernel's list
-    if ((int64_t)(a.c.cap / 32 + 32) * a.b.n * a.c.kv_heads >= (int64_t)1 << 30)
-      return fail(QG_ERR_UNSUPPORTED, "%d entries of up to %d tokens and %d kv heads in one call", a.b.n, a.c.cap, a.c.kv_heads);
-    a.workers = h->cus;
-    a.min_run = STEP_MIN_RUN;
-    return done(h, launch_attn_step(a, D, bf16, MT, st), st);
-  }
-  // A call of few blocks is split over the tokens until it covers the chip: once for parts
-  // of few tiles, twice for parts of many (the last 512 rows of 65,536 tokens, 40 q and 8
-  // kv heads of 128: 741 us with two, 1,507 with one; the last 16 of each of 4 slots of
-  // 8,192: 53 and 47).  A cache whose slots hold too little for parts saves the join.
-  const int64_t blocks = (rows + ROWS_BLOCK - 1) / ROWS_BLOCK * a.b.n * a.c.kv_heads;
-  a.splits1 = (int)std::max<int64_t>(1, kRowsSlots / 2 / blocks);
-  a.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kRowsSlots / blocks, rows_parts(D, a.c.cap, a.splits1)));
-  if (blocks * a.splits >= (int64_t)1 << 31) return fail(QG_ERR_UNSUPPORTED, "%lld blocks in one call", (long long)blocks);
-  return done(h, launch_attn_rows(a, D, bf16, (unsigned)blocks, st), st);
+  // a group of k blocks holds more than 128 (k - 1) rows of a kv head
+  const int64_t blocks = (int64_t)a.b.rows * a.G / ROWS_BLOCK + n_groups, grid = blocks * a.c.kv_heads;
+  // without two entries in a group there is nothing to share; and calls of more rows than the
+  // workspace has slots for are made of blocks that read the tokens many times either way
+  if (n_groups == a.b.n || a.b.rows > SHARE_ROWS || grid > kRowsSlots) return attend(h, a, false, st);
+  ShareArgs p = h->share;
+  p.c = a.c;
+  p.b = a.b;
+  p.groups = groups;
+  p.ngroups = n_groups;
+  p.G = a.G;
+  p.blocks = (int)blocks;
+  hipError_t e = launch_share_plan(p, st);
+  if (e != hipSuccess) return done(h, e, st);
+  a.share = p.share;
+  a.share_blocks = p.share_blocks;
+  a.share_pos = p.pos;
+  a.prefix = h->prefix;
+  a.prefix_floats = h->prefix_floats;
+  AttnArgs x = a;
+  x.partial = h->prefix;
+  x.partial_floats = h->prefix_floats;
+  x.splits1 = (int)std::max<int64_t>(1, kRowsSlots / 2 / grid);
+  x.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kRowsSlots / grid, rows_parts(h->d.head_dim, a.c.cap, x.splits1)));
+  e = launch_attn_prefix(x, h->d.head_dim, h->d.dtype == QG_KV_BF16, (unsigned)grid, st);
+  if (e != hipSuccess) return done(h, e, st);
+  return attend(h, a, true, st);
 }
 
 }  // extern "C"

@@ -46,7 +46,9 @@ def bind(L) -> None:
     L.qgkv_append_rotary.argtypes = [vp, i32, ctypes.POINTER(_KvBatch)] + [ctypes.POINTER(_KvRows)] * 4 + [i32, vp, vp]
     L.qgkv_attend.argtypes = [vp, i32, ctypes.POINTER(_KvBatch), ctypes.POINTER(_KvRows), ctypes.POINTER(_KvRows), i32,
                               ctypes.c_float, i32, i32, vp]
-    for f in ("create", "destroy", "extend", "fork", "trim", "compact", "append", "append_rotary", "attend"):
+    L.qgkv_attend_shared.argtypes = L.qgkv_attend.argtypes[:-1] + [vp, i32, vp]
+    for f in ("create", "destroy", "extend", "fork", "trim", "compact", "append", "append_rotary", "attend",
+              "attend_shared"):
         getattr(L, "qgkv_" + f).restype = ctypes.c_int
 
 
@@ -127,7 +129,7 @@ class KVCache:
         # argument blocks (calls on one cache are ordered by the caller), the device
         L = lib()
         self._c = {n: getattr(L, "qgkv_" + n) for n in ("extend", "fork", "trim", "compact", "append", "append_rotary",
-                                                         "attend")}
+                                                         "attend", "attend_shared")}
         self._check = _check
         self._torch = torch
         self._dev = pool.get_device()
@@ -281,6 +283,23 @@ class KVCache:
         layer; returns out of the same shape.  scale: default head_dim ** -0.5.
         window: a row sees its last ``window`` tokens (0: all) and the first
         ``sinks`` of its slot.  Which slots the rows are of: see the class."""
+        return self._attend("attend", (), q, layer, seqs, row_start, max_rows, scale, window, sinks, out, stream)
+
+    def attend_shared(self, q, *, groups=None, layer: int = 0, seqs=None, row_start=None, max_rows: int = None,
+                      scale: float = None, window: int = 0, sinks: int = 0, out=None, stream=None):
+        """``attend`` where entries share their first tokens (forked answers to a prompt): the
+        pages that all entries of a group name alike are read once for all of them.
+        groups: int32 [g + 1], the entries at which groups begin, and n (default: all
+        entries are one group).  Nothing else need be told: the tables are looked at on
+        the device."""
+        if groups is None:
+            more = (None, 1)
+        else:
+            groups = self._index("groups", groups, None, stream)
+            more = (groups.data_ptr(), groups.numel() - 1)
+        return self._attend("attend_shared", more, q, layer, seqs, row_start, max_rows, scale, window, sinks, out, stream)
+
+    def _attend(self, name, more, q, layer, seqs, row_start, max_rows, scale, window, sinks, out, stream):
         st = self._on(stream)
         _, qa, oa = self._args[:3]
         rows, heads = self._rows(qa, "q", q)
@@ -290,7 +309,7 @@ class KVCache:
         self._rows(oa, "out", out, heads, rows)
         held = self._batch(rows, seqs, row_start, max_rows, stream)
         rb, rq, ro = self._refs[:3]
-        self._call("attend", layer, rb, rq, ro, heads, self.head_dim ** -0.5 if scale is None else scale, window, sinks, st)
+        self._call(name, layer, rb, rq, ro, heads, self.head_dim ** -0.5 if scale is None else scale, window, sinks, *more, st)
         del held
         return out
 

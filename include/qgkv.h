@@ -179,6 +179,21 @@ qg_status qgkv_append_rotary(qg_kv_handle h, int32_t layer, const qg_kv_batch* b
 qg_status qgkv_attend(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const qg_kv_rows* q, const qg_kv_rows* out,
                       int32_t q_heads, float scale, int32_t window, int32_t sinks, void* stream);
 
+/* qgkv_attend for entries that share tokens: the same outputs, to their roundings, but
+ * the tokens that all entries of a group have in common are read once for the group and
+ * not once for each.  Entries groups[g] .. groups[g + 1] - 1 are group g (device int32
+ * [n_groups + 1], ascending from 0 to n, may change between replays of a captured
+ * call; NULL: all entries are one group).  What a group shares is found in the tables: the
+ * leading pages that all its entries name alike (those of qgkv_fork), up to the first
+ * of their rows, in whole multiples of 64 tokens, 256 at least; entries that see nothing are left
+ * aside.  Groups that share nothing are attended to as by qgkv_attend, and so are
+ * calls of very many rows (more than some 512 / kv_heads blocks of 128 rows and q heads of a kv
+ * head).  The split of tokens depends on the group, so a row's bits may differ
+ * from qgkv_attend's. */
+qg_status qgkv_attend_shared(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const qg_kv_rows* q, const qg_kv_rows* out,
+                             int32_t q_heads, float scale, int32_t window, int32_t sinks, const int32_t* groups,
+                             int32_t n_groups, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
