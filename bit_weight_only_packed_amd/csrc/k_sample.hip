@@ -20,7 +20,7 @@ template <int TY> hipError_t go(const SampleArgs& a, hipStream_t st) {
     k_sample_max<TY><<<grid, SM_T, 0, st>>>(b);
     if (a.cuts) {
       k_sample_hist<TY><<<grid, SM_T, 0, st>>>(b);
-      k_sample_cut<TY><<<rows, SM_CUT, 0, st>>>(b);
+      k_sample_list<TY><<<grid, SM_T, 0, st>>>(b);
     }
     k_sample_pick<TY><<<grid, SM_T, 0, st>>>(b);
   }
@@ -33,7 +33,7 @@ template <int TY> hipError_t go(const SampleArgs& a, hipStream_t st) {
 // workgroups, 64 at most.
 void sample_parts(int rows, int vocab, int* parts, int* len) {
   int p = (vocab + 2047) / 2048;
-  const int most = rows >= 2048 ? 1 : 2048 / rows;
+  const int most = rows >= 4096 ? 1 : 4096 / rows;
   p = p < most ? p : most;
   p = p < 64 ? p : 64;
   *len = ((vocab + p - 1) / p + 7) / 8 * 8;

@@ -10,12 +10,17 @@
 //
 // The order is never made whole.  A row's logits fall into SM_BUCKETS buckets by their distance
 // from the largest (log2 of the weight in steps of 44 / SM_BUCKETS); counts and masses of the buckets
-// say in which one the k-th token lies, and in which one p of the mass is reached; only
-// that bucket's few logits are put in order.  So four launches, each over (part of the row, row):
+// say in which ones the k-th token lies and p of the mass is reached.  The tokens of these buckets, or,
+// where they are few, all kept ones, come together in a list that is sorted in LDS.  Four launches, each
+// over (part of the row, row), of which a row takes what it needs; the last part of a row to
+// arrive does what is done once a row:
 //   k_sample_max   the parts' largest logits
-//   k_sample_hist  counts and masses of the buckets (rows with top-k or top-p)
-//   k_sample_cut   the last kept token (rows with top-k or top-p; one workgroup a row)
-//   k_sample_pick  masses of the kept tokens by part; the last part of a row to arrive picks
+//   k_sample_hist  rows with top-k or top-p: the buckets' counts and masses; which of them are listed
+//   k_sample_list  the same rows: the list; the last kept token, and if all kept ones are listed, the
+//                  picked one.  (A list that overflows, as of thousands of equal logits: the
+//                  row is gone through again by one workgroup, in as many passes as it takes.)
+//   k_sample_pick  the other rows, and those with more kept tokens than a list: masses of the parts,
+//                  then the part that holds the picked one
 #pragma once
 #include "qg_attn.h"
 #include "qg_step.h"
@@ -24,9 +29,11 @@ namespace qg {
 
 constexpr int SM_BUCKETS = SAMPLE_BUCKETS;
 constexpr int SM_BITS = 43;         // weights are multiples of 2^-SM_BITS: 2^20 of them stay below 2^63
-constexpr int SM_LIST = 512;        // tokens put in order against each other
-constexpr int SM_T = 256;           // threads of the kernels over parts
-constexpr int SM_CUT = 1024;        // threads of k_sample_cut
+constexpr int SM_LIST = 512;        // tokens ranked against each other where a list has overflowed
+constexpr int SM_CAP = SAMPLE_LIST; // tokens of a list
+constexpr int SM_WHOLE = 512;       // kept tokens that are listed all
+constexpr int SM_RANK = 512;        // words sorted by counting
+constexpr int SM_T = 256;           // threads of a workgroup
 
 typedef uint32_t sm_u4 __attribute__((ext_vector_type(4), aligned(2)));
 typedef unsigned long long sm_u64;
@@ -113,15 +120,20 @@ struct SmScale {
   __device__ __forceinline__ sm_u64 weight(float l) const { return bucket(l) < SM_BUCKETS ? fixed(share(l)) : 0; }
 };
 
-// a row's largest logit, from its parts' (every thread calls it)
+// a row's largest logit and where it first stands, from its parts' (64 at most: a lane each)
+__device__ __forceinline__ bool sm_better(float x, int i, float y, int j) { return y > x || (y == x && j < i); }
 __device__ __forceinline__ float sm_top(const SampleArgs& a, int row, int* arg = nullptr) {
+  const int lane = threadIdx.x & 63;
   float m = -__builtin_inff();
-  int at = 0;
-  for (int p = 0; p < a.parts; ++p) {  // the same addresses for all lanes
-    const float x = a.part_max[(int64_t)row * a.parts + p];
-    if (x > m) m = x, at = p;
+  int at = 0x7FFFFFFF;
+  if (lane < a.parts) m = a.part_max[(int64_t)row * a.parts + lane], at = a.part_arg[(int64_t)row * a.parts + lane];
+#pragma unroll
+  for (int o = 32; o; o >>= 1) {
+    const float y = __shfl_xor(m, o);
+    const int j = __shfl_xor(at, o);
+    if (sm_better(m, at, y, j)) m = y, at = j;
   }
-  if (arg) *arg = a.part_arg[(int64_t)row * a.parts + at];
+  if (arg) *arg = at;
   return m;
 }
 template <int TY> __device__ __forceinline__ const void* sm_row(const SampleArgs& a, int row) {
@@ -139,7 +151,7 @@ template <int TY> __global__ __launch_bounds__(SM_T) void k_sample_max(SampleArg
     a.counts[(int64_t)row * SM_BUCKETS + b] = 0;
     a.masses[(int64_t)row * SM_BUCKETS + b] = 0;
   }
-  if (part == 0 && tid == 0) a.arrived[row] = 0;
+  if (part == 0 && tid < 4) a.arrived[4 * row + tid] = 0;
   float m = -__builtin_inff();
   int arg = a0;
   for (int at = a0 + tid * 8; at < a1; at += SM_T * 8) {
@@ -149,31 +161,116 @@ template <int TY> __global__ __launch_bounds__(SM_T) void k_sample_max(SampleArg
     for (int i = 0; i < 8; ++i)
       if (v[i] > m) m = v[i], arg = at + i;
   }
-  const auto better = [](float x, int i, float y, int j) { return y > x || (y == x && j < i); };
 #pragma unroll
   for (int o = 32; o; o >>= 1) {
     const float y = __shfl_xor(m, o);
     const int j = __shfl_xor(arg, o);
-    if (better(m, arg, y, j)) m = y, arg = j;
+    if (sm_better(m, arg, y, j)) m = y, arg = j;
   }
   if ((tid & 63) == 0) lm[tid >> 6] = m, la[tid >> 6] = arg;
   __syncthreads();
   if (tid == 0) {
     for (int w = 1; w < SM_T / 64; ++w)
-      if (better(m, arg, lm[w], la[w])) m = lm[w], arg = la[w];
+      if (sm_better(m, arg, lm[w], la[w])) m = lm[w], arg = la[w];
     a.part_max[(int64_t)row * a.parts + part] = m;
     a.part_arg[(int64_t)row * a.parts + part] = arg;
   }
 }
 
+// inclusive sums over the workgroup; lds: a T per wave
+template <class T> __device__ __forceinline__ T sm_scan(T v, T* lds) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const T y = __shfl_up(v, o);
+    if (lane >= o) v += y;
+  }
+  __syncthreads();
+  if (lane == 63) lds[wave] = v;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < SM_T / 64; ++w)
+    if (w < wave) v += lds[w];
+  return v;
+}
+
+// a token's place in the order: larger is earlier
+__device__ __forceinline__ sm_u64 sm_place(uint32_t key, int index) { return (sm_u64)key << 32 | (uint32_t)~index; }
+__device__ __forceinline__ float sm_logit(uint32_t key) {
+  return __builtin_bit_cast(float, (key >> 31) ? key ^ 0x80000000u : ~key);
+}
+
+// Counts and masses of the buckets, SM_PER consecutive ones a thread, and where they cross.
+constexpr int SM_PER = SM_BUCKETS / SM_T;
+struct SmScanLds {
+  sm_u64 sums[SM_T / 64], mass;
+  int counts[SM_T / 64], at, count, own;
+};
+struct SmAt {
+  int bucket;    // SM_BUCKETS: none
+  int count;     // tokens in the buckets before it,
+  sm_u64 mass;   // their mass,
+  int own;       // and its own tokens
+};
+struct SmBuckets {
+  int c[SM_PER], c0;       // c0, w0: of the buckets before this thread's
+  sm_u64 w[SM_PER], w0;
+  __device__ __forceinline__ void scan(SmScanLds& s) {
+    int ct = 0;
+    sm_u64 wt = 0;
+#pragma unroll
+    for (int i = 0; i < SM_PER; ++i) ct += c[i], wt += w[i];
+    c0 = sm_scan(ct, s.counts) - ct;
+    w0 = sm_scan(wt, s.sums) - wt;
+  }
+  // the first bucket with tokens at whose end hit(count, mass) holds
+  template <class F> __device__ __forceinline__ SmAt cross(SmScanLds& s, F hit) const {
+    int mine = SM_BUCKETS, own = 0, cc = c0, cb = 0;
+    sm_u64 ww = w0, wb = 0;
+#pragma unroll
+    for (int i = 0; i < SM_PER; ++i) {
+      if (mine == SM_BUCKETS && c[i] > 0 && hit(cc + c[i], ww + w[i])) mine = SM_PER * threadIdx.x + i, cb = cc, wb = ww, own = c[i];
+      cc += c[i], ww += w[i];
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) s.at = SM_BUCKETS, s.count = 0, s.mass = 0, s.own = 0;
+    __syncthreads();
+    if (mine < SM_BUCKETS) atomicMin(&s.at, mine);
+    __syncthreads();
+    if (mine < SM_BUCKETS && mine == s.at) s.count = cb, s.mass = wb, s.own = own;
+    __syncthreads();
+    return SmAt{s.at, s.count, s.mass, s.own};
+  }
+  __device__ __forceinline__ sm_u64 all(SmScanLds& s) const {  // the whole mass
+    sm_u64 t = w0;
+#pragma unroll
+    for (int i = 0; i < SM_PER; ++i) t += w[i];
+    __syncthreads();
+    if (threadIdx.x == SM_T - 1) s.mass = t;
+    __syncthreads();
+    return s.mass;
+  }
+};
+
+// What a row's buckets have said.
+enum { SM_PICK = 0, SM_ALL = 1, SM_SOME = 2, SM_SLOW = 3, SM_DONE = 4 };
+
 template <int TY> __global__ __launch_bounds__(SM_T) void k_sample_hist(SampleArgs a) {
   __shared__ uint32_t cnt[SM_BUCKETS];
   __shared__ sm_u64 mass[SM_BUCKETS];
+  __shared__ SmScanLds s;
+  __shared__ int flag;
   const int part = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
   const SmRow r(a, row);
   if (!r.cut) return;
   const SmScale sc(sm_top(a, row), r.heat);
-  const bool masses = r.p < 1.0f || r.k > 0;
+  SmPlan& plan = a.plan[row];
+  if (sc.top == -__builtin_inff()) {
+    if (part == 0 && tid == 0) plan = SmPlan{SM_PICK};
+    return;
+  }
+  // the masses say nothing that a list of all tokens down to the k-th would not
+  const bool masses = r.p < 1.0f && !(r.k > 0 && r.k <= SM_WHOLE / 2);
   for (int b = tid; b < SM_BUCKETS; b += SM_T) cnt[b] = 0, mass[b] = 0;
   __syncthreads();
   const void* x = sm_row<TY>(a, row);
@@ -190,68 +287,114 @@ template <int TY> __global__ __launch_bounds__(SM_T) void k_sample_hist(SampleAr
     }
   }
   __syncthreads();
-  for (int b = tid; b < SM_BUCKETS; b += SM_T)
-    if (cnt[b]) {
-      atomicAdd(&a.counts[(int64_t)row * SM_BUCKETS + b], cnt[b]);
-      if (masses) atomicAdd(&a.masses[(int64_t)row * SM_BUCKETS + b], mass[b]);
-    }
-}
-
-// inclusive sums over the SM_CUT threads; lds: a T per wave
-template <class T> __device__ __forceinline__ T sm_scan(T v, T* lds) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  // Of a part that holds k tokens alone, the buckets past its own k-th have none of the row's first k.
+  int upto = SM_BUCKETS - 1;
+  SmBuckets h;
+  if (r.k > 0 && r.k < a1 - a0) {
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const T y = __shfl_up(v, o);
-    if (lane >= o) v += y;
+    for (int i = 0; i < SM_PER; ++i) h.c[i] = (int)cnt[SM_PER * tid + i], h.w[i] = 0;
+    h.scan(s);
+    upto = min(h.cross(s, [&](int c, sm_u64) { return c >= r.k; }).bucket, upto);
   }
-  __syncthreads();
-  if (lane == 63) lds[wave] = v;
-  __syncthreads();
-  for (int w = 0; w < waves; ++w)
-    if (w < wave) v += lds[w];
-  return v;
-}
-// the lowest thread for which it holds, or blockDim.x
-__device__ __forceinline__ int sm_first(bool hit, int* lds) {
-  __syncthreads();
-  if (threadIdx.x == 0) *lds = blockDim.x;
-  __syncthreads();
-  if (hit) atomicMin(lds, (int)threadIdx.x);
-  __syncthreads();
-  return *lds;
+  uint32_t* counts = a.counts + (int64_t)row * SM_BUCKETS;
+  sm_u64* sums = a.masses + (int64_t)row * SM_BUCKETS;
+  for (int b = tid; b <= upto; b += SM_T)
+    if (cnt[b]) {
+      atomicAdd(&counts[b], cnt[b]);
+      if (masses) atomicAdd(&sums[b], mass[b]);
+    }
+  if (!at_last(a.arrived + 4 * row, a.parts, &flag)) return;
+#pragma unroll
+  for (int i = 0; i < SM_PER; ++i) {
+    h.c[i] = (int)__hip_atomic_load(&counts[SM_PER * tid + i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    h.w[i] = masses ? __hip_atomic_load(&sums[SM_PER * tid + i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+  }
+  h.scan(s);
+  SmPlan p{SM_PICK};
+  p.k_bucket = SM_BUCKETS, p.hi = SM_BUCKETS - 1;
+  bool bounded = false;  // whether something of weight is cut off by top-k
+  if (r.k > 0) {
+    const SmAt k = h.cross(s, [&](int c, sm_u64) { return c >= r.k; });
+    bounded = k.bucket < SM_BUCKETS;  // (else the k-th token has a weight of 0)
+    if (bounded) {
+      p.k_bucket = k.bucket, p.k_count = k.count, p.k_mass = k.mass;
+      p.mode = k.count + k.own <= SM_WHOLE ? SM_ALL : r.p < 1.0f ? (masses ? SM_SOME : SM_SLOW) : k.own <= SM_CAP ? SM_SOME : SM_SLOW;
+      p.lo = p.hi = k.bucket, p.lo_mass = k.mass;
+      if (p.mode == SM_ALL) p.lo = 0;
+      if (p.mode == SM_SOME && r.p < 1.0f) {
+        // p of the mass lies between p of it without the k-th token's bucket and p of it with
+        const sm_u64 most = h.cross(s, [&](int c, sm_u64) { return c > k.count + k.own; }).mass;  // up to that bucket's end
+        const sm_u64 upto = most > 0 ? most : h.all(s);
+        const double from = (double)r.p * (double)k.mass, to = (double)r.p * (double)upto;
+        const SmAt l = h.cross(s, [&](int, sm_u64 w) { return (double)w >= from; });
+        const SmAt e = h.cross(s, [&](int, sm_u64 w) { return (double)w >= to; });
+        p.lo = l.bucket, p.lo_mass = l.mass;
+        p.hi = min(e.bucket, k.bucket);
+        const int n = e.count + e.own - l.count + (p.hi < k.bucket ? k.own : 0);
+        if (n > SM_CAP) p.mode = SM_SLOW;
+      }
+    }
+  }
+  if (!bounded && r.p < 1.0f) {
+    if (!masses) {
+      p.mode = SM_ALL;  // fewer than k tokens have any weight
+      p.lo = 0;
+    } else {
+      const double goal = (double)r.p * (double)h.all(s);
+      const SmAt e = h.cross(s, [&](int, sm_u64 w) { return (double)w >= goal; });
+      p.mode = e.count + e.own <= SM_WHOLE ? SM_ALL : e.own <= SM_CAP ? SM_SOME : SM_SLOW;
+      p.lo = p.mode == SM_ALL ? 0 : e.bucket, p.hi = e.bucket;
+      p.lo_mass = p.mode == SM_ALL ? 0 : e.mass;
+    }
+  }
+  p.total = masses ? h.all(s) : 0;
+  if (tid == 0) plan = p;
 }
 
-// a token's place in the order: larger is earlier
-__device__ __forceinline__ sm_u64 sm_place(uint32_t key, int index) { return (sm_u64)key << 32 | (uint32_t)~index; }
+// ---- a list that has overflowed: one workgroup, as many passes over the row as it takes ----
 
-struct SmCutLds {
+struct SmSlowLds {
   uint32_t cnt[SM_BUCKETS];
   sm_u64 mass[SM_BUCKETS];
   sm_u64 list[SM_LIST], weight[SM_LIST];
-  sm_u64 sums[SM_CUT / 64];
-  int counts[SM_CUT / 64];
   int n, first;
   uint32_t lo, hi;
-  sm_u64 last, got, taken;
+  sm_u64 last, got;
 };
 
 // every token of the row: f(logit, index)
 template <int TY, class F> __device__ __forceinline__ void sm_each(const SampleArgs& a, const void* x, F f) {
-  for (int at = threadIdx.x * 8; at < a.vocab; at += SM_CUT * 8) {
+  for (int at = threadIdx.x * 8; at < a.vocab; at += SM_T * 8) {
     float v[8];
     sm_load<TY>(v, x, at, a.vocab - at);
 #pragma unroll
     for (int i = 0; i < 8; ++i) f(v[i], at + i);
   }
 }
+// counts and masses of the tokens by which(logit, index), SM_BUCKETS or more: none
+template <int TY, class F>
+__device__ __forceinline__ void sm_count(SmBuckets& h, const SampleArgs& a, const void* x, const SmScale& sc, SmSlowLds& s, SmScanLds& t, F which) {
+  __syncthreads();
+  for (int b = threadIdx.x; b < SM_BUCKETS; b += SM_T) s.cnt[b] = 0, s.mass[b] = 0;
+  __syncthreads();
+  sm_each<TY>(a, x, [&](float l, int i) {
+    const int b = which(l, i);
+    if (b >= SM_BUCKETS) return;
+    atomicAdd(&s.cnt[b], 1u);
+    atomicAdd(&s.mass[b], sc.weight(l));
+  });
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < SM_PER; ++i) h.c[i] = (int)s.cnt[SM_PER * threadIdx.x + i], h.w[i] = s.mass[SM_PER * threadIdx.x + i];
+  h.scan(t);
+}
 
 // The last kept token's place among those of a bucket that lie at `limit` or before it in the
 // order: the need-th of them (need > 0), or the first at which `before` and their weights reach
 // `goal`.  kept: the mass of the bucket's kept tokens.
 template <int TY>
-__device__ sm_u64 sm_refine(const SampleArgs& a, const void* x, const SmScale& sc, int bucket, sm_u64 limit, int need,
-                            sm_u64 before, double goal, SmCutLds& s, sm_u64* kept) {
+__device__ __forceinline__ sm_u64 sm_refine(const SampleArgs& a, const void* x, const SmScale& sc, int bucket, sm_u64 limit, int need,
+                                            sm_u64 before, double goal, SmSlowLds& s, SmScanLds& t, sm_u64* kept) {
   const int tid = threadIdx.x;
   uint32_t lo = 0, hi = 0xFFFFFFFFu;
   int skipped = 0;     // tokens of the bucket that lie before the range, and their mass
@@ -279,8 +422,8 @@ __device__ sm_u64 sm_refine(const SampleArgs& a, const void* x, const SmScale& s
     if (n <= SM_LIST) {
       if (tid == 0) s.last = ~0ull, s.got = 0;
       __syncthreads();
-      if (tid < n) {
-        const sm_u64 mine = s.list[tid];
+      for (int e = tid; e < n; e += SM_T) {
+        const sm_u64 mine = s.list[e];
         int rank = 0;
         sm_u64 mass = passed;
         for (int j = 0; j < n; ++j) {
@@ -288,10 +431,10 @@ __device__ sm_u64 sm_refine(const SampleArgs& a, const void* x, const SmScale& s
           rank += early;
           mass += early ? s.weight[j] : 0;
         }
-        const bool in = need > 0 ? skipped + rank < need : (before + mass == 0) || (double)(before + mass) < goal;
+        const bool in = need > 0 ? skipped + rank < need : before + mass == 0 || (double)(before + mass) < goal;
         if (in) {
           atomicMin(&s.last, mine);
-          atomicMax(&s.got, mass + s.weight[tid]);
+          atomicMax(&s.got, mass + s.weight[e]);
         }
       }
       __syncthreads();
@@ -300,12 +443,7 @@ __device__ sm_u64 sm_refine(const SampleArgs& a, const void* x, const SmScale& s
     }
     if (lo == hi) {
       // equal logits: so many of them, by index
-      float l = 0.0f;
-      {
-        const uint32_t b = (lo >> 31) ? lo ^ 0x80000000u : ~lo;
-        l = __builtin_bit_cast(float, b);
-      }
-      const sm_u64 w = sc.weight(l);
+      const sm_u64 w = sc.weight(sm_logit(lo));
       int m = need > 0 ? need - skipped : n;
       if (need <= 0 && w > 0) {
         const double left = (goal - (double)(before + passed)) / (double)w;
@@ -314,25 +452,23 @@ __device__ sm_u64 sm_refine(const SampleArgs& a, const void* x, const SmScale& s
       }
       // the index of the m-th
       int seen = 0, index = a.vocab;
-      for (int at0 = 0; at0 < a.vocab; at0 += SM_CUT * 8) {
+      for (int at0 = 0; at0 < a.vocab; at0 += SM_T * 8) {
         const int at = at0 + tid * 8;
         float v[8];
         sm_load<TY>(v, x, at, a.vocab - at);
         int c = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) c += at + i < a.vocab && sm_key(v[i]) == lo && sm_place(lo, at + i) >= limit;
-        const int upto = seen + sm_scan(c, s.counts);
-        if (tid == SM_CUT - 1) s.n = upto;
+        const int upto = seen + sm_scan(c, t.counts);
+        if (tid == SM_T - 1) s.n = upto;
         if (upto >= m && upto - c < m) {
-          int k = upto - c;
+          int k = upto - c, found = -1;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             k += at + i < a.vocab && sm_key(v[i]) == lo && sm_place(lo, at + i) >= limit;
-            if (k == m) {
-              s.first = at + i;
-              break;
-            }
+            if (found < 0 && k == m) found = at + i;
           }
+          s.first = found;
         }
         __syncthreads();
         seen = s.n;
@@ -348,85 +484,233 @@ __device__ sm_u64 sm_refine(const SampleArgs& a, const void* x, const SmScale& s
     // cut the range into SM_BUCKETS pieces
     int shift = 0;
     while (((hi - lo) >> shift) >= SM_BUCKETS) ++shift;
-    s.cnt[tid] = 0, s.mass[tid] = 0;
-    __syncthreads();
-    sm_each<TY>(a, x, [&](float l, int i) {
-      if (!inside(l, i)) return;
-      const int b = (int)((hi - sm_key(l)) >> shift);
-      atomicAdd(&s.cnt[b], 1u);
-      atomicAdd(&s.mass[b], sc.weight(l));
-    });
-    __syncthreads();
-    const int c = (int)s.cnt[tid];
-    const sm_u64 w = s.mass[tid];
-    const int cc = skipped + sm_scan(c, s.counts);
-    const sm_u64 ww = passed + sm_scan(w, s.sums);
-    int b = sm_first(c > 0 && (need > 0 ? cc >= need : (double)(before + ww) >= goal), &s.first);
-    if (b >= SM_BUCKETS) b = (int)((hi - lo) >> shift);  // (the goal lies past a rounding: the last)
-    __syncthreads();
-    if (tid == b) s.n = cc - c, s.taken = ww - w;
-    __syncthreads();
-    skipped = s.n, passed = s.taken;
-    const uint32_t top = hi - ((uint32_t)b << shift), span = (1u << shift) - 1;
+    SmBuckets h;
+    sm_count<TY>(h, a, x, sc, s, t, [&](float l, int i) { return inside(l, i) ? (int)((hi - sm_key(l)) >> shift) : SM_BUCKETS; });
+    SmAt b = h.cross(t, [&](int c, sm_u64 w) { return need > 0 ? skipped + c >= need : (double)(before + passed + w) >= goal; });
+    if (b.bucket >= SM_BUCKETS) {  // (the goal lies past a rounding: the last)
+      const int end = (int)((hi - lo) >> shift);
+      b = h.cross(t, [&](int c, sm_u64) { return c == n; });
+      b.bucket = end;
+    }
+    skipped += b.count, passed += b.mass;
+    const uint32_t top = hi - ((uint32_t)b.bucket << shift), span = (1u << shift) - 1;
     lo = top - lo > span ? top - span : lo;
     hi = top;
   }
 }
 
-template <int TY> __global__ __launch_bounds__(SM_CUT) void k_sample_cut(SampleArgs a) {
-  __shared__ SmCutLds s;
-  const int row = blockIdx.x, tid = threadIdx.x;
-  const SmRow r(a, row);
-  sm_u64 last = 0;  // everything is kept
-  if (r.cut) {
-    const SmScale sc(sm_top(a, row), r.heat);
-    if (sc.top > -__builtin_inff()) {
-      const void* x = sm_row<TY>(a, row);
-      const int c = (int)a.counts[(int64_t)row * SM_BUCKETS + tid];
-      const sm_u64 w = a.masses[(int64_t)row * SM_BUCKETS + tid];
-      const int cc = sm_scan(c, s.counts);
-      const sm_u64 ww = sm_scan(w, s.sums);
-      __syncthreads();
-      if (tid == SM_CUT - 1) s.taken = ww;
-      __syncthreads();
-      sm_u64 all = s.taken;
-      int bk = SM_BUCKETS;
-      if (r.k > 0) {
-        bk = sm_first(cc >= r.k, &s.first);
-        if (bk < SM_BUCKETS) {  // (else the k-th token has a weight of 0: nothing of weight is cut)
-          __syncthreads();
-          if (tid == bk) s.n = cc - c, s.taken = ww - w;
-          __syncthreads();
-          const int need = r.k - s.n;
-          const sm_u64 before = s.taken;
-          sm_u64 kept;
-          last = sm_refine<TY>(a, x, sc, bk, 0, need, before, 0.0, s, &kept);
-          all = before + kept;
-        }
-      }
-      if (r.p < 1.0f) {
-        const double goal = (double)r.p * (double)all;
-        const int bp = min(sm_first((double)ww >= goal && c > 0, &s.first), bk);
-        if (bp < SM_BUCKETS) {
-          __syncthreads();
-          if (tid == bp) s.taken = ww - w;
-          __syncthreads();
-          const sm_u64 before = s.taken;
-          sm_u64 kept;
-          last = sm_refine<TY>(a, x, sc, bp, bp == bk ? last : 0, 0, before, goal, s, &kept);
-        }
+template <int TY>
+__device__ __forceinline__ sm_u64 sm_slow(const SampleArgs& a, const void* x, const SmRow& r, const SmScale& sc, SmSlowLds& s, SmScanLds& t) {
+  SmBuckets h;
+  sm_u64 last = 0, all = 0, kept;
+  int bk = SM_BUCKETS;
+#pragma unroll 1
+  for (int stage = 0; stage < 2; ++stage) {  // top-k, then top-p of what that leaves
+    if (stage == 0 ? r.k <= 0 : r.p >= 1.0f) continue;
+    sm_count<TY>(h, a, x, sc, s, t, [&](float l, int) { return sc.bucket(l); });
+    if (bk == SM_BUCKETS) all = h.all(t);
+    const double goal = (double)r.p * (double)all;
+    const SmAt e = h.cross(t, [&](int c, sm_u64 w) { return stage == 0 ? c >= r.k : (double)w >= goal; });
+    if (e.bucket >= SM_BUCKETS) continue;
+    last = sm_refine<TY>(a, x, sc, e.bucket, stage == 1 && e.bucket == bk ? last : 0, stage == 0 ? r.k - e.count : 0, e.mass, goal, s, t, &kept);
+    if (stage == 0) bk = e.bucket, all = e.mass + kept;
+  }
+  return last;
+}
+
+// ---- lists ----
+
+// n distinct words in LDS, falling.  Up to SM_RANK of them each thread counts the words above
+// its own, all reads on their way at once and the same for all lanes (64 words: 0.3 us, where the 21
+// dependent steps of a sorting network take 4.6); above that the network.
+__device__ __forceinline__ void sm_sort(sm_u64* list, int n) {
+  constexpr int E = SM_RANK / SM_T;
+  __syncthreads();
+  if (n <= SM_RANK) {
+    sm_u64 mine[E];
+    int rank[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) mine[e] = threadIdx.x + e * SM_T < n ? list[threadIdx.x + e * SM_T] : ~0ull, rank[e] = 0;
+    if (n <= SM_T) {
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) rank[0] += list[j] > mine[0];
+    } else {
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const sm_u64 x = list[j];
+#pragma unroll
+        for (int e = 0; e < E; ++e) rank[e] += x > mine[e];
       }
     }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (threadIdx.x + e * SM_T < n) list[rank[e]] = mine[e];
+  } else {
+    int size = SM_RANK;
+    while (size < n) size <<= 1;
+    for (int i = n + threadIdx.x; i < size; i += SM_T) list[i] = 0;  // (no word is 0)
+    for (int k = 2; k <= size; k <<= 1)
+      for (int j = k >> 1; j; j >>= 1) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < size / 2; i += SM_T) {
+          const int x = 2 * i - (i & (j - 1));
+          const sm_u64 u = list[x], v = list[x + j];
+          if ((u < v) == ((x & k) == 0)) list[x] = v, list[x + j] = u;
+        }
+      }
   }
-  if (tid == 0) a.last[row] = last;
+  __syncthreads();
+}
+
+// the multiple of 2^-SM_BITS that u of a total is, held to [0, total)
+__device__ __forceinline__ sm_u64 sm_goal(float u, sm_u64 total) {
+  const sm_u64 g = u > 0.0f ? (sm_u64)fmin((double)u * (double)total, 9.2e18) : 0;
+  return g < total ? g : total - 1;
+}
+
+template <int TY> __global__ __launch_bounds__(SM_T) void k_sample_list(SampleArgs a) {
+  __shared__ union {
+    sm_u64 list[SM_CAP];
+    SmSlowLds slow;
+  } m;
+  __shared__ SmScanLds t;
+  __shared__ int flag, cut;
+  __shared__ sm_u64 mass;
+  const int part = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
+  const SmRow r(a, row);
+  if (!r.cut) return;
+  const SmPlan plan = a.plan[row];
+  if (plan.mode == SM_PICK) {
+    if (part == 0 && tid == 0) a.last[row] = 0;
+    return;
+  }
+  const SmScale sc(sm_top(a, row), r.heat);
+  const void* x = sm_row<TY>(a, row);
+  if (plan.mode == SM_SLOW) {
+    if (part > 0) return;
+    const sm_u64 last = sm_slow<TY>(a, x, r, sc, m.slow, t);
+    if (tid == 0) a.last[row] = last;
+    return;
+  }
+  sm_u64* list = a.list + (int64_t)row * SM_CAP;
+  int* length = a.arrived + 4 * row + 3;
+  const int a0 = part * a.part_len, a1 = min(a0 + a.part_len, a.vocab);
+  if (tid == 0) cut = 0;
+  __syncthreads();
+  for (int at = a0 + tid * 8; at < a1; at += SM_T * 8) {
+    float v[8];
+    sm_load<TY>(v, x, at, a1 - at);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int b = sc.bucket(v[i]);
+      if (((b < plan.lo) | (b > plan.hi)) & (b != plan.k_bucket) | (b >= SM_BUCKETS)) continue;
+      const int to = atomicAdd(&cut, 1);  // (the part's: the list's places are asked for once a part)
+      if (to < SM_CAP) m.list[to] = sm_place(sm_key(v[i]), at + i);
+    }
+  }
+  __syncthreads();
+  const int mine = min(cut, SM_CAP);
+  if (tid == 0 && mine > 0) flag = atomicAdd(length, mine);
+  __syncthreads();
+  for (int i = tid; i < mine; i += SM_T)
+    if (flag + i < SM_CAP) __hip_atomic_store(&list[flag + i], m.list[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (!at_last(a.arrived + 4 * row + 1, a.parts, &flag)) return;
+  const int n = min(__hip_atomic_load(length, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT), SM_CAP);
+  for (int i = tid; i < n; i += SM_T) m.list[i] = __hip_atomic_load(&list[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  sm_sort(m.list, n);
+  // this thread's consecutive tokens, their weights, and the mass before them
+  constexpr int MOST = SM_CAP / SM_T;
+  const int per = (n + SM_T - 1) / SM_T, i0 = tid * per;
+  sm_u64 w[MOST], before;
+  const auto masses = [&](auto weight) {
+    sm_u64 sum = 0;
+#pragma unroll
+    for (int e = 0; e < MOST; ++e) {
+      w[e] = e < per && i0 + e < n ? weight(i0 + e) : 0;
+      sum += w[e];
+    }
+    before = sm_scan(sum, t.sums) - sum;
+  };
+  const auto logit = [&](int i) { return sm_logit((uint32_t)(m.list[i] >> 32)); };
+  masses([&](int i) { return sc.weight(logit(i)); });
+  // the first token of the list at which hit(index, mass up to and with it) holds (n: none), and that mass
+  const auto first = [&](auto hit, int none, sm_u64* upto) {
+    __syncthreads();
+    if (tid == 0) cut = none;
+    __syncthreads();
+    sm_u64 run = before;
+#pragma unroll
+    for (int e = 0; e < MOST; ++e) {
+      run += w[e];
+      if (e < per && i0 + e < n && hit(i0 + e, run)) atomicMin(&cut, i0 + e);
+    }
+    __syncthreads();
+    const int at = cut;
+    run = before;
+#pragma unroll
+    for (int e = 0; e < MOST; ++e) {
+      run += w[e];
+      if (e < per && i0 + e == at) mass = run;
+    }
+    __syncthreads();
+    *upto = mass;
+    return at;
+  };
+  int kept = n;       // of the list
+  sm_u64 total, got;  // total: the mass of what top-k leaves
+  if (plan.k_bucket < SM_BUCKETS) {
+    // the tokens before the k-th one's bucket that are listed
+    const int skip = first([&](int i, sm_u64) { return sc.bucket(logit(i)) >= plan.k_bucket; }, n, &got);
+    kept = min(skip + r.k - plan.k_count, n);
+    first([&](int i, sm_u64) { return i == kept - 1; }, kept - 1, &total);
+    if (plan.mode == SM_SOME) {
+      sm_u64 ahead = 0;  // mass of the listed tokens before that bucket
+      if (skip > 0) first([&](int i, sm_u64) { return i == skip - 1; }, skip - 1, &ahead);
+      total = total - ahead + plan.k_mass;
+    }
+  } else if (plan.mode == SM_SOME) {
+    total = plan.total;
+  } else {
+    first([&](int i, sm_u64) { return i == n - 1; }, n - 1, &total);
+    if (plan.total > 0) total = plan.total;  // (the list ends with the bucket that p is reached in)
+  }
+  if (r.p < 1.0f) {
+    const double goal = (double)r.p * (double)total;
+    const sm_u64 base = plan.mode == SM_SOME ? plan.lo_mass : 0;
+    kept = min(kept, first([&](int, sm_u64 run) { return (double)(base + run) >= goal; }, kept - 1, &got) + 1);
+  }
+  if (plan.mode == SM_SOME) {
+    if (tid == 0) a.last[row] = m.list[kept - 1];
+    return;
+  }
+  // everything that is kept is listed: min-p, then the token
+  const double min_p = fmin((double)r.min_p, 1.0);
+  kept = min(kept, first([&](int i, sm_u64) { return sc.share(logit(i)) < min_p; }, n, &got));
+  // by rising index: ~index falls
+  for (int i = tid; i < kept; i += SM_T) m.list[i] = m.list[i] << 32 | m.list[i] >> 32;
+  sm_sort(m.list, kept);
+  const auto logit2 = [&](int i) { return sm_logit((uint32_t)m.list[i]); };
+  masses([&](int i) { return i < kept ? sc.weight(logit2(i)) : 0; });
+  first([&](int i, sm_u64) { return i == kept - 1; }, kept - 1, &total);
+  const sm_u64 goal = sm_goal(a.u[row], total);
+  const int at = first([&](int i, sm_u64 run) { return run > goal; }, kept - 1, &got);
+  if (tid == 0) {
+    const sm_u64 e = m.list[at];
+    a.tokens[row] = (int)~(uint32_t)(e >> 32);
+    if (a.probs) a.probs[row] = (float)((double)sc.weight(sm_logit((uint32_t)e)) / (double)total);
+    a.plan[row].mode = SM_DONE;
+  }
 }
 
 template <int TY> __global__ __launch_bounds__(SM_T) void k_sample_pick(SampleArgs a) {
   __shared__ sm_u64 sums[SM_T / 64];
   __shared__ int flag, found;
   __shared__ sm_u64 mine;
-  const int part = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
+  const int part = blockIdx.x, row = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
   const SmRow r(a, row);
+  if (r.cut && a.plan[row].mode == SM_DONE) return;
   int arg;
   const float top = sm_top(a, row, &arg);
   if (r.greedy || top == -__builtin_inff()) {
@@ -441,11 +725,14 @@ template <int TY> __global__ __launch_bounds__(SM_T) void k_sample_pick(SampleAr
   const sm_u64 last = r.cut ? a.last[row] : 0;
   const uint32_t least = (uint32_t)(last >> 32);
   const double min_p = fmin((double)r.min_p, 1.0);
+  // buckets past which no weight reaches min_p (one more, for the roundings)
+  const int most = min_p > 0.0 ? (int)fmin(1.0 - log2(min_p) * (SM_BUCKETS / 44.0), (double)SM_BUCKETS) : SM_BUCKETS;
   const void* x = sm_row<TY>(a, row);
   // the weight of a kept token, 0 of others
   const auto weight = [&](float l, int i) -> sm_u64 {
     const uint32_t k = sm_key(l);
-    if (k < least || (k == least && sm_place(k, i) < last) || sc.bucket(l) >= SM_BUCKETS) return 0;
+    const int b = sc.bucket(l);
+    if (k < least || (k == least && sm_place(k, i) < last) || b >= SM_BUCKETS || b > most) return 0;
     const double s = sc.share(l);
     return s >= min_p ? sc.fixed(s) : 0;
   };
@@ -462,21 +749,19 @@ template <int TY> __global__ __launch_bounds__(SM_T) void k_sample_pick(SampleAr
   for (int at = a0 + tid * 8; at < a1; at += SM_T * 8) sum += eight(at, a1, w);
   sum = sm_scan(sum, sums);
   if (tid == SM_T - 1) __hip_atomic_store(&a.part_sum[(int64_t)row * a.parts + part], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  if (!at_last(a.arrived + row, a.parts, &flag)) return;
-  // the part that holds the token
-  sm_u64 total = 0;
-  for (int p = 0; p < a.parts; ++p)
-    total += __hip_atomic_load(&a.part_sum[(int64_t)row * a.parts + p], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  const float u = a.u[row];
-  sm_u64 goal = u > 0.0f ? (sm_u64)fmin((double)u * (double)total, 9.2e18) : 0;
-  goal = goal < total ? goal : total - 1;
+  if (!at_last(a.arrived + 4 * row + 2, a.parts, &flag)) return;
+  // the part that holds the token (64 at most: a lane each)
   sm_u64 passed = 0;
-  int p = 0;
-  for (; p < a.parts - 1; ++p) {
-    const sm_u64 t = __hip_atomic_load(&a.part_sum[(int64_t)row * a.parts + p], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (passed + t > goal) break;
-    passed += t;
+  if (lane < a.parts) passed = __hip_atomic_load(&a.part_sum[(int64_t)row * a.parts + lane], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const sm_u64 own = passed;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const sm_u64 y = __shfl_up(passed, o);
+    if (lane >= o) passed += y;
   }
+  const sm_u64 total = __shfl(passed, 63), goal = sm_goal(a.u[row], total);
+  const int p = __builtin_ctzll(__ballot(passed > goal));
+  passed = __shfl(passed - own, p);
   const int b0 = p * a.part_len, b1 = min(b0 + a.part_len, a.vocab);
   if (tid == 0) found = -1;
   for (int at0 = b0; at0 < b1; at0 += SM_T * 8) {

@@ -37,6 +37,16 @@ struct RotArgs {
 };
 hipError_t launch_rotate(const RotArgs& a, bool bf16, int cus, hipStream_t st);
 
+// What the buckets of a row's logits have said (qg_sample.h).
+struct SmPlan {
+  int mode;
+  int lo, hi;                 // buckets to list, and
+  int k_bucket;               // the one that holds the k-th token (SAMPLE_BUCKETS: no such)
+  int k_count;                // tokens in the buckets before that
+  unsigned long long k_mass;  // their mass,
+  unsigned long long lo_mass; // the mass of the buckets before lo,
+  unsigned long long total;   // and of all (0 where it is not known)
+};
 struct SampleArgs {
   const void* logits;
   int64_t stride;
@@ -52,11 +62,13 @@ struct SampleArgs {
   // workspace, of SAMPLE_ROWS rows at most
   float* part_max;      // [row][part]
   int* part_arg;        // [row][part]
-  unsigned long long *part_sum, *masses, *last;  // [row][part], [row][bucket], [row]
+  unsigned long long *part_sum, *masses, *last, *list;  // [row][part], [row][bucket], [row], [row][SAMPLE_LIST]
   uint32_t* counts;     // [row][bucket]
-  int* arrived;         // [row]
+  int* arrived;         // [row][4]: of the parts in three kernels, and the list's length
+  SmPlan* plan;         // [row]
 };
 constexpr int SAMPLE_BUCKETS = 1024;
+constexpr int SAMPLE_LIST = 2048;
 constexpr int SAMPLE_ROWS = 4096;  // rows of a launch: what the workspace holds
 void sample_parts(int rows, int vocab, int* parts, int* len);
 hipError_t launch_sample(const SampleArgs& a, int type, hipStream_t st);

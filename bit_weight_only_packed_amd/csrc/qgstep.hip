@@ -180,8 +180,10 @@ size_t lay_out(SampleArgs* a, int rows, int vocab, char* at) {
   take(a->part_sum, r * a->parts);
   take(a->part_max, r * a->parts);
   take(a->part_arg, r * a->parts);
+  take(a->list, r * SAMPLE_LIST);
+  take(a->plan, r);
   take(a->last, r);
-  take(a->arrived, r);
+  take(a->arrived, 4 * r);
   return used;
 }
 

@@ -68,6 +68,17 @@ def test_large_vocabularies(dtype, vocab):
             get("top_p", 1.0).float().cuda(), get("min_p", 0.0).float().cuda())
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("top_k", [900, 1024, 1025, 2048, 3000, 20000, 65000])
+@pytest.mark.parametrize("top_p", [1.0, 0.999, 0.7, 0.1])
+def test_large_counts_with_shares(dtype, top_k, top_p):
+    """Kept tokens by the thousand: the last of them is found among those of one bucket, of two, or of a few."""
+    x = logits_of(3, 66000, dtype, top_k, 1.2)
+    heat = torch.tensor([1.0, 4.0, 0.4]).cuda()
+    compare(x, draws(3, top_k), heat, top_k, top_p)
+    compare(x, draws(3, top_k + 1), heat, 0, top_p, 0.001)
+
+
 @pytest.mark.parametrize("vocab", [600, 3000, 20000])
 @pytest.mark.parametrize("levels", [1, 2, 5, 40])
 def test_equal_logits(vocab, levels):
