@@ -30,9 +30,10 @@ template <int D, int MODE> hipError_t go(AttnArgs a, bool bf16, unsigned blocks,
 
 }  // namespace
 
-int rows_parts(int D, int cap, int splits1) {
+int rows_parts(int D, int cap, int splits1, bool rest) {
+  const int least = rest ? RW_REST_TILES : RW_MIN_TILES;
   const int kt = D == 256 ? RowsShape<256>::KT : RowsShape<128>::KT;
-  return rw_parts((cap + kt - 1) / kt, splits1);
+  return rw_parts((cap + kt - 1) / kt, splits1, least);
 }
 
 hipError_t launch_attn_rows(const AttnArgs& a, int D, bool bf16, unsigned blocks, bool shared, hipStream_t st) {

@@ -174,23 +174,23 @@ struct AtNoExtra {
 };
 template <int D> struct AtPrefix {
   static constexpr bool some = true;
-  __amdgpu_buffer_rsrc_t rs;
+  const float* from;  // (another launch's: no need to go past the caches)
   int row, heads, head;
   float add;
   bool there;  // else the entry shares nothing
   __device__ __forceinline__ AtPrefix(const AttnArgs& a, const ShareEntry& s, int head_, float add_)
-      : rs(at_slots(a.prefix, a.prefix_floats)), row(s.row), heads(a.c.kv_heads), head(head_), add(add_), there(s.tokens > 0) {}
+      : from(a.prefix), row(s.row), heads(a.c.kv_heads), head(head_), add(add_), there(s.tokens > 0) {}
   __device__ __forceinline__ uint32_t slot(int r) const {
     return ((uint32_t)((row + r) / ROWS_BLOCK) * heads + head) * (uint32_t)rows_slot(D);
   }
   __device__ __forceinline__ at_f2 ml(int r) const {
     at_f2 v = {-__builtin_inff(), 0.0f};
-    if (there) v = at_ld2(rs, slot(r) + ROWS_BLOCK * D + 2 * ((row + r) % ROWS_BLOCK));
+    if (there) v = *reinterpret_cast<const at_f2*>(from + slot(r) + ROWS_BLOCK * D + 2 * ((row + r) % ROWS_BLOCK));
     return at_f2{v.x + add, v.y};
   }
   __device__ __forceinline__ at_f4 o(int r, int c) const {
     at_f4 v = {0, 0, 0, 0};
-    if (there) v = at_ld4(rs, slot(r) + (uint32_t)((row + r) % ROWS_BLOCK) * D + c);
+    if (there) v = *reinterpret_cast<const at_f4*>(from + slot(r) + (uint32_t)((row + r) % ROWS_BLOCK) * D + c);
     return v;
   }
 };

@@ -49,8 +49,14 @@ namespace qg {
 // the second for what a second workgroup of a CU brings over one (2 prompts of 1,500 rows
 // of 3,000 tokens, 8 q heads of 128 and one kv head: 67 us unshared, 76 at 23 tiles a part).
 constexpr int RW_MIN_TILES = 8, RW_LONG_TILES = 32;
-__host__ __device__ constexpr int rw_parts(int tiles, int splits1) {
-  const int few = tiles / RW_MIN_TILES < splits1 ? tiles / RW_MIN_TILES : splits1;
+constexpr int RW_REST_TILES = 3;     // (of an entry's own tokens, which are few)
+// parts of a block with so many shared tokens
+constexpr int RW_PREFIX_PART = 128, RW_PREFIX_LONG = 1024;
+__device__ __forceinline__ int rw_prefix_parts(int tokens, int splits, int splits1) {
+  return max(min(splits, max(min(tokens / RW_PREFIX_PART, splits1), tokens / RW_PREFIX_LONG)), 1);
+}
+__host__ __device__ constexpr int rw_parts(int tiles, int splits1, int least = RW_MIN_TILES) {
+  const int few = tiles / least < splits1 ? tiles / least : splits1;
   return few > tiles / RW_LONG_TILES ? few : tiles / RW_LONG_TILES;
 }
 // operands read from LDS ahead of the product that takes them: 4 where there are
@@ -60,17 +66,21 @@ __host__ __device__ constexpr int rw_parts(int tiles, int splits1) {
 template <int D> constexpr int RW_DEEP = D == 256 ? 1 : 4;
 constexpr int RW_MFMA = 0x8, RW_DS_READ = 0x100;
 
-template <int D> struct RowsShape {
+enum { RW_WHOLE = 0, RW_PREFIX = 1, RW_REST = 2 };  // all tokens; a group's shared ones; an entry's others
+
+template <int D_, int MODE_ = RW_WHOLE> struct RowsShape {
+  static constexpr int D = D_, MODE = MODE_;
   static constexpr int NW = ROWS_WAVES;     // waves of a workgroup
   static constexpr int BM = ROWS_BLOCK;     // rows of a block
-  static constexpr int KT = D == 256 ? 32 : 64;  // tokens of a tile
+  static constexpr int KT = D == 256 || (MODE == RW_PREFIX && D == 128) ? 32 : 64;  // tokens of a tile
   static constexpr int KC = D / 8;          // 16-byte chunks of a token's key or value
   static constexpr int NT = KT / 32;        // 32-token groups
   static constexpr int ND = D / 32;         // 32-column groups
   static constexpr int bytes = KT * D * 2;  // a tile's keys (or values)
   static constexpr int LD = bytes / 1024 / NW;  // 1 KiB copies per wave of them
   static constexpr int RW = KT / NW;        // tokens that a wave copies (they lie in one page)
-  static constexpr int NB = 2;              // tiles of keys, and of values, in LDS
+  static constexpr int NB = MODE == RW_PREFIX ? 4 : 2;  // tiles of keys, and of values, in LDS
+  static constexpr int AHEAD = NB - 1;      // tiles of keys on their way
   static_assert(RW <= 16, "a wave's tokens of a tile lie in one page");
 };
 
@@ -106,9 +116,8 @@ __device__ __forceinline__ void rw_barrier() {
 }
 
 // a wave's 32 rows
-template <int D> struct RowsState {
-  using S = RowsShape<D>;
-  kv_u4 Q[D / 16];
+template <class S> struct RowsState {
+  kv_u4 Q[S::D / 16];
   at_f16 O[S::ND];
   float m, l;   // m: in units of q . k
   int pos;      // this lane's row's position
@@ -116,8 +125,8 @@ template <int D> struct RowsState {
 };
 
 // its scores with a tile, and their weights
-template <int D> using RowsScores = at_f16[RowsShape<D>::NT];
-template <int D> using RowsWeights = kv_u4[2 * RowsShape<D>::NT];
+template <class S> using RowsScores = at_f16[S::NT];
+template <class S> using RowsWeights = kv_u4[2 * S::NT];
 
 // byte of this lane's part of the key reads, and of the value reads, but for what is
 // constant per read: an exclusive-or for the chunk, an immediate for the token
@@ -132,9 +141,9 @@ template <int D> __device__ __forceinline__ int rw_val_byte(int lane) {
 }
 
 // scores of the wave's rows with a tile of keys
-template <int D, bool BF>
-__device__ __forceinline__ void rw_scores(RowsScores<D>& s, const RowsState<D>& r, const char* keys, int lane) {
-  using S = RowsShape<D>;
+template <class S, bool BF>
+__device__ __forceinline__ void rw_scores(RowsScores<S>& s, const RowsState<S>& r, const char* keys, int lane) {
+  constexpr int D = S::D;
   int kb = rw_key_byte<D>(lane);
   asm volatile("" : "+v"(kb));  // one instruction per read, not a register each: they are needed
   constexpr int N = S::NT * (D / 16), DEEP = RW_DEEP<D>;
@@ -159,10 +168,10 @@ __device__ __forceinline__ void rw_scores(RowsScores<D>& s, const RowsState<D>& 
 }
 
 // scores of tile tok .. tok + KT - 1 to weights; masked: some row does not see all of it
-template <int D, bool BF>
-__device__ __forceinline__ void rw_softmax(RowsWeights<D>& P, RowsScores<D>& s, RowsState<D>& r,
+template <class S, bool BF>
+__device__ __forceinline__ void rw_softmax(RowsWeights<S>& P, RowsScores<S>& s, RowsState<S>& r,
                                            const AttnArgs& a, int tok, bool masked, int lane) {
-  using S = RowsShape<D>;
+  constexpr int D = S::D;
   const int h = lane >> 5;
   if (masked) {
     const SeenFrom seen(r.pos, tok + 4 * h, a.window, a.sinks);
@@ -222,10 +231,10 @@ __device__ __forceinline__ void rw_softmax(RowsWeights<D>& P, RowsScores<D>& s, 
 
 // products of the weights of tile tok with its values
 // noted: the tile's values that were not finite and have been taken out, or NULL
-template <int D, bool BF>
-__device__ __forceinline__ void rw_products(RowsState<D>& r, const RowsWeights<D>& P, const AttnArgs& a,
+template <class S, bool BF>
+__device__ __forceinline__ void rw_products(RowsState<S>& r, const RowsWeights<S>& P, const AttnArgs& a,
                                             const char* vals, int tok, const uint8_t* noted, int lane) {
-  using S = RowsShape<D>;
+  constexpr int D = S::D;
   int vb = rw_val_byte<D>(lane);
   asm volatile("" : "+v"(vb));
   const auto val = [&](int x, int k, int b) {  // 32-column group x, 16-token step k, tokens 8 b ..
@@ -274,9 +283,8 @@ __device__ __forceinline__ void rw_products(RowsState<D>& r, const RowsWeights<D
 // A block of the call.  Longest first: the last block of every (entry, kv head), then
 // the one before, ...; kv heads fastest, so that with 8 of them (or a multiple) a
 // head's blocks meet its tokens in one XCD's L2.
-enum { RW_WHOLE = 0, RW_PREFIX = 1, RW_REST = 2 };  // all tokens; a group's shared ones; an entry's others
 template <int D, int MODE = RW_WHOLE> struct RowsBlock {
-  using S = RowsShape<D>;
+  using S = RowsShape<D, MODE>;
   int head, rb, total, r0, nrows, pe, p0, p1, parts;  // rb < 0: none; parts that share its tiles
   int cut = 0;  // tiles of the list that are others' to compute
   KvEntry e;
@@ -297,12 +305,12 @@ template <int D, int MODE = RW_WHOLE> struct RowsBlock {
       shared = a.share[j];
       cut = tr.before(shared.tokens / S::KT);
     }
-    parts = max(min(a.splits, rw_parts(tr.n - cut, a.splits1)), 1);
+    parts = max(min(a.splits, rw_parts(tr.n - cut, a.splits1, MODE == RW_REST ? RW_REST_TILES : RW_MIN_TILES)), 1);
   }
 };
 // a block of a group's rows with its shared tokens
 template <int D> struct RowsBlock<D, RW_PREFIX> {
-  using S = RowsShape<D>;
+  using S = RowsShape<D, RW_PREFIX>;
   int head, rb, total, r0, nrows, pe, p0, p1, parts;
   static constexpr int cut = 0;
   KvEntry e;
@@ -317,14 +325,33 @@ template <int D> struct RowsBlock<D, RW_PREFIX> {
     e = KvEntry{s.slot, 0, s.row0, total / a.G};
     tr = TileRange<S::KT>(p0, p1, a.window, a.sinks);
     tr.n = tr.before(s.tokens / S::KT);
-    parts = max(min(a.splits, rw_parts(tr.n, a.splits1)), 1);
+    parts = rw_prefix_parts(tr.n * S::KT, a.splits, a.splits1);
   }
 };
 
+// The prefix kernel's part and block.  Row blocks of one head and part read the same tokens: they
+// are numbered eight apart, so that they meet in one XCD's L2 whatever the number of heads
+// (the last few (head, part) pairs, where that is no multiple of eight, are not).
+__device__ __forceinline__ void rw_prefix_place(const AttnArgs& a, unsigned blocks, int& z, int& id) {
+  const int heads = a.c.kv_heads, nb = (int)blocks / heads, units = heads * a.splits, whole = units / 8 * 8;
+  const int x = blockIdx.x;
+  int u, b;
+  if (x < whole * nb) {
+    u = x / (8 * nb) * 8 + x % 8;
+    b = x % (8 * nb) / 8;
+  } else {
+    const int y = x - whole * nb;
+    u = whole + y / nb;
+    b = y % nb;
+  }
+  z = u / heads;
+  id = b * heads + u % heads;
+}
+
 template <int D, bool BF, int MODE = RW_WHOLE>
-__global__ __launch_bounds__(64 * ROWS_WAVES) __attribute__((amdgpu_waves_per_eu(D == 64 ? 3 : 2)))
+__global__ __launch_bounds__(64 * ROWS_WAVES) __attribute__((amdgpu_waves_per_eu(D == 64 ? 3 : D == 256 && MODE == RW_PREFIX ? 1 : 2)))
 void k_attn_rows(AttnArgs a) {
-  using S = RowsShape<D>;
+  using S = RowsShape<D, MODE>;
   __shared__ __align__(1024) char keys[S::NB * S::bytes];
   __shared__ __align__(1024) char vals[S::NB * S::bytes];
   __shared__ __align__(16) uint8_t notes[S::bytes / 8];
@@ -336,8 +363,9 @@ void k_attn_rows(AttnArgs a) {
   // those that work do not wait for them (the last 16 rows of 16,384 tokens: 29 us against
   // 36 with parts fastest)
   const unsigned blocks = gridDim.x / (unsigned)a.splits;
-  const int z = blockIdx.x / blocks;
-  const RowsBlock<D, MODE> blk(a, a.first + (int)(blockIdx.x - z * blocks));
+  int z = blockIdx.x / blocks, id = a.first + (int)(blockIdx.x - z * blocks);
+  if constexpr (MODE == RW_PREFIX) rw_prefix_place(a, blocks, z, id);
+  const RowsBlock<D, MODE> blk(a, id);
   if (blk.rb < 0 || z >= blk.parts) return;
   const KvEntry& e = blk.e;
   const TileRange<S::KT>& tr = blk.tr;
@@ -347,13 +375,16 @@ void k_attn_rows(AttnArgs a) {
   const int32_t* table = a.c.tables + (int64_t)e.slot * a.c.max_pages;
 
   // this wave's rows
-  RowsState<D> r;
+  RowsState<S> r;
   const int rw = r0 + wave * 32 + col;
   const bool live = rw < total, alive = r0 + wave * 32 < total;
   const int ri = live ? rw / a.G : 0;
   int pw0, pw1;  // first and last position of the wave's rows
-  if constexpr (MODE == RW_PREFIX) {  // rows of many entries: -1 for those that see nothing
-    r.pos = live ? min(max(a.share_pos[e.row0 + ri], -1), p1) : -1;  // (a row that max_rows leaves out has none)
+  if constexpr (MODE == RW_PREFIX) {
+    // rows of many entries.  What comes of those that see nothing, or that max_rows leaves out and have no
+    // position, is not looked at: a position that masks nothing costs least.
+    const int p = live ? a.share_pos[e.row0 + ri] : -1;
+    r.pos = live ? ((unsigned)p < (unsigned)p1 ? p : p1) : -1;
     pw0 = live ? r.pos : 0x7FFFFFFF, pw1 = r.pos;
 #pragma unroll
     for (int o = 16; o; o >>= 1) pw0 = min(pw0, __shfl_xor(pw0, o)), pw1 = max(pw1, __shfl_xor(pw1, o));
@@ -461,37 +492,41 @@ void k_attn_rows(AttnArgs a) {
     at_tok = token(min(t, nt - 1)) + lane0;
     at_id = kv_table(table, min(at_tok, p1) >> a.c.page_shift);
   };
-  const auto send = [&](int t) {
-    const int to = (t + 1) & (S::NB - 1), to1 = t & (S::NB - 1);
+  constexpr int A = S::AHEAD;
+  const auto send = [&](int t) {  // keys t + A, values t + A - 1
+    const int to = (t + A) & (S::NB - 1), to1 = (t + A - 1) & (S::NB - 1);
     const char* const from = pool0 + kv_page(a.c, at_id) * page_bytes + (at_tok & mask) * (D * 2);
-    if (t + 1 < nt)
+    if (t + A < nt)
 #pragma unroll
       for (int i = 0; i < S::LD; ++i) rw_copy(from, kofs[i], keys + to * S::bytes + (wave * S::LD + i) * 1024);
-    if (t >= 0)
+    if (t + A - 1 >= 0 && (A == 1 || t + A - 1 < nt))
 #pragma unroll
       for (int i = 0; i < S::LD; ++i) rw_copy(before + v_bytes, vofs[i], vals + to1 * S::bytes + (wave * S::LD + i) * 1024);
     before = from;
-    look(t + 2);
+    look(t + A + 1);
   };
   const auto bound = [&](int t) {
-    __builtin_amdgcn_s_waitcnt(at_wait_vm(0));  // this wave's copies of keys t and values t - 1 have landed
+    // this wave's copies of keys t and values t - 1 have landed: all, or all but those of A - 1 sends
+    if (A == 1 || t - 1 + A >= nt) __builtin_amdgcn_s_waitcnt(at_wait_vm(0));
+    else __builtin_amdgcn_s_waitcnt(at_wait_vm((A - 1) * 2 * S::LD));
     rw_barrier();  // everyone's have, and the buffers of the tile before are free
     noted = t > 0 ? mend(t - 1, val_buf(t - 1)) : nullptr;
   };
   if (nt > 0) {
     look(0);
-    send(-1);
+#pragma unroll
+    for (int i = -A; i < 0; ++i) send(i);
     bound(0);
     // (a wave without rows only copies and keeps step)
-    if (alive) rw_scores<D, BF>(s, r, key_buf(0), lane);
+    if (alive) rw_scores<S, BF>(s, r, key_buf(0), lane);
     for (int t = 0; t < nt; ++t) {
       send(t);
-      if (alive) rw_softmax<D, BF>(P, s, r, a, token(t), t < wclear0 || t >= wclear1, lane);
+      if (alive) rw_softmax<S, BF>(P, s, r, a, token(t), t < wclear0 || t >= wclear1, lane);
       bound(t + 1);
       if (!alive) continue;
       __builtin_amdgcn_s_setprio(1);  // a product is one issue in eight: let it have it
-      rw_products<D, BF>(r, P, a, val_buf(t), token(t), noted, lane);
-      if (t + 1 < nt) rw_scores<D, BF>(s, r, key_buf(t + 1), lane);
+      rw_products<S, BF>(r, P, a, val_buf(t), token(t), noted, lane);
+      if (t + 1 < nt) rw_scores<S, BF>(s, r, key_buf(t + 1), lane);
       __builtin_amdgcn_s_setprio(0);
     }
   }
@@ -526,7 +561,7 @@ void k_attn_rows(AttnArgs a) {
   }
   // several workgroups share the block: k_attn_rows_join puts their partials together
   const auto rs = at_slots(a.partial, a.partial_floats);
-  const uint32_t slot = blockIdx.x * (uint32_t)rows_slot(D), row = wave * 32 + col;
+  const uint32_t slot = (MODE == RW_PREFIX ? z * blocks + (unsigned)id : blockIdx.x) * (uint32_t)rows_slot(D), row = wave * 32 + col;
   if (live) {
 #pragma unroll
     for (int x = 0; x < S::ND; ++x)

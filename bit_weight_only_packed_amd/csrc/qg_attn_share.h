@@ -27,12 +27,14 @@ __device__ __forceinline__ int sp_ld(int* p) { return __hip_atomic_load(p, __ATO
 // anything; the last to arrive makes the groups' plans.
 __global__ __launch_bounds__(SP_T) void k_share_plan(ShareArgs a) {
   __shared__ int group, lead, same, flag;
+  __shared__ KvEntry entry[KV_MAX_SEQS];
   __shared__ int g_tokens[KV_MAX_SEQS], g_live[KV_MAX_SEQS], g_lo[KV_MAX_SEQS], g_hi[KV_MAX_SEQS], g_p0[KV_MAX_SEQS],
       g_p1[KV_MAX_SEQS], g_slot[KV_MAX_SEQS], g_base[KV_MAX_SEQS];
   const int j = blockIdx.x, tid = threadIdx.x, n = a.b.n;
   const auto first = [&](int g) { return a.groups ? min(max(a.groups[g], 0), n) : g * n; };
   const auto sees = [](const KvEntry& e) { return e.rows > 0 && e.pos + e.rows > 0; };
   if (tid == 0) group = a.ngroups, lead = n;
+  for (int k = tid; k < n; k += SP_T) entry[k] = kv_entry(a.c, a.b, k);
   __syncthreads();
   for (int g = tid; g < a.ngroups; g += SP_T)
     if (first(g) <= j && j < first(g + 1)) atomicMin(&group, g);
@@ -40,17 +42,17 @@ __global__ __launch_bounds__(SP_T) void k_share_plan(ShareArgs a) {
   const bool grouped = group < a.ngroups;
   if (grouped)
     for (int k = first(group) + tid; k < first(group + 1); k += SP_T)
-      if (sees(kv_entry(a.c, a.b, k))) {
+      if (sees(entry[k])) {
         atomicMin(&lead, k);
         break;
       }
-  const KvEntry e = kv_entry(a.c, a.b, j);
+  const KvEntry e = entry[j];
   for (int i = tid; i < e.rows; i += SP_T) a.pos[e.row0 + i] = e.pos + i;
   __syncthreads();
   // -1: no constraint on the others (an entry that sees nothing)
   int tokens = -1;
   if (grouped && sees(e)) {
-    const KvEntry l = kv_entry(a.c, a.b, lead);
+    const KvEntry l = entry[lead];
     const int pages = min(e.pos + 1, l.pos + 1) >> a.c.page_shift;  // whole pages before both's first rows
     if (tid == 0) same = max(pages, 0);
     __syncthreads();
@@ -78,10 +80,19 @@ __global__ __launch_bounds__(SP_T) void k_share_plan(ShareArgs a) {
   for (int g = tid; g < a.ngroups; g += SP_T)
     g_tokens[g] = 0x7FFFFFFF, g_live[g] = 0, g_lo[g] = 0x7FFFFFFF, g_hi[g] = 0, g_p0[g] = 0x7FFFFFFF, g_p1[g] = -1, g_slot[g] = n;
   __syncthreads();
-  for (int k = tid; k < n; k += SP_T) {
-    const int t = sp_ld(&a.want[k].x), g = sp_ld(&a.want[k].y);
+  constexpr int PER = KV_MAX_SEQS / SP_T;
+  int wt[PER], wg[PER];  // what entries tid, tid + SP_T, ... want
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int k = tid + i * SP_T;
+    wt[i] = -1, wg[i] = -1;
+    if (k < n) wt[i] = sp_ld(&a.want[k].x), wg[i] = sp_ld(&a.want[k].y);
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int k = tid + i * SP_T, t = wt[i], g = wg[i];
     if (g < 0) continue;
-    const KvEntry f = kv_entry(a.c, a.b, k);
+    const KvEntry f = entry[k];
     if (f.rows == 0) continue;
     atomicMin(&g_lo[g], f.row0);
     atomicMax(&g_hi[g], f.row0 + f.rows);
@@ -93,17 +104,25 @@ __global__ __launch_bounds__(SP_T) void k_share_plan(ShareArgs a) {
     atomicMin(&g_slot[g], k);
   }
   __syncthreads();
-  // blocks of the groups, one after another (few groups: one thread)
+  // blocks of the groups, one after another (few groups: one thread); none where all that sharing
+  // would save is less than it costs
   if (tid == 0) {
-    int base = 0;
+    int64_t read = 0;  // tokens that would be read without sharing
     for (int g = 0; g < a.ngroups; ++g) {
       int t = g_live[g] > 1 ? g_tokens[g] / SHARE_TILE * SHARE_TILE : 0;
       if (t < SHARE_MIN) t = 0;
-      const int64_t blocks = t ? ((int64_t)(g_hi[g] - g_lo[g]) * a.G + ROWS_BLOCK - 1) / ROWS_BLOCK : 0;
-      if (blocks > a.blocks - base) t = 0;  // (rows of groups that overlap, which no call that is allowed has)
       g_tokens[g] = t;
+      read += (a.window ? min((int64_t)t, (int64_t)a.window + a.sinks) : t) * g_live[g];
+    }
+    const bool pays = read >= a.least;
+    int base = 0;
+    for (int g = 0; g < a.ngroups; ++g) {
+      const int t = pays ? g_tokens[g] : 0;
+      const int64_t blocks = t ? ((int64_t)(g_hi[g] - g_lo[g]) * a.G + ROWS_BLOCK - 1) / ROWS_BLOCK : 0;
+      const bool fits = blocks <= a.blocks - base;  // (not so where groups overlap, which no allowed call's do)
+      g_tokens[g] = fits ? t : 0;
       g_base[g] = base;
-      base += t ? (int)blocks : 0;
+      base += fits ? (int)blocks : 0;
     }
     same = base;
   }
@@ -114,23 +133,25 @@ __global__ __launch_bounds__(SP_T) void k_share_plan(ShareArgs a) {
       int g = 0;
       while (g + 1 < a.ngroups && g_base[g + 1] <= b) ++g;  // (groups without blocks begin where the next does)
       while (g_tokens[g] == 0) --g;
-      s = ShareBlock{g_tokens[g], kv_entry(a.c, a.b, g_slot[g]).slot, g_lo[g], (b - g_base[g]) * ROWS_BLOCK,
+      s = ShareBlock{g_tokens[g], entry[g_slot[g]].slot, g_lo[g], (b - g_base[g]) * ROWS_BLOCK,
                      (g_hi[g] - g_lo[g]) * a.G, g_p0[g], g_p1[g]};
     }
     a.share_blocks[b] = s;
   }
-  for (int k = tid; k < n; k += SP_T) {
-    const int t = sp_ld(&a.want[k].x), g = sp_ld(&a.want[k].y);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int k = tid + i * SP_T, g = wg[i];
+    if (k >= n) break;
     ShareEntry s{};
-    if (g >= 0 && t >= 0 && g_tokens[g] > 0)
-      s = ShareEntry{g_tokens[g], g_base[g] * ROWS_BLOCK + (kv_entry(a.c, a.b, k).row0 - g_lo[g]) * a.G};
+    if (g >= 0 && wt[i] >= 0 && g_tokens[g] > 0)
+      s = ShareEntry{g_tokens[g], g_base[g] * ROWS_BLOCK + (entry[k].row0 - g_lo[g]) * a.G};
     a.share[k] = s;
   }
 }
 
 // A block's parts, joined in part order into the first one's slot; RJ_ROWS rows a workgroup.
 template <int D> __global__ __launch_bounds__(RJ_THREADS) void k_share_join(AttnArgs a) {
-  using S = RowsShape<D>;
+  using S = RowsShape<D, RW_PREFIX>;
   constexpr int PER = S::BM / RJ_ROWS, MOST = 512;  // (parts of a block: the slots of the workspace at most)
   __shared__ float fac[RJ_ROWS][MOST];
   const unsigned id = blockIdx.x / PER, blocks = gridDim.x / PER;

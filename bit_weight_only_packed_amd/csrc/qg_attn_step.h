@@ -438,6 +438,16 @@ void k_attn_step(AttnArgs a) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       if (mt * 16 >= nrows) break;
+      at_f2 pml = {-__builtin_inff(), 0.0f};
+      at_f4 po[(CW + 3) / 4];
+      if constexpr (SH) {
+        if (whole && mt * 16 + row < nrows) {
+          const AtPrefix<D> pre(a, shared, head, AT_SHARE_ADD<BF>);
+          pml = pre.ml(mt * 16 + row);
+#pragma unroll
+          for (int x = 0; x < CW; x += 4) po[x / 4] = pre.o(mt * 16 + row, c0 + x - (CW < 4 ? c0 & 3 : 0));
+        }
+      }
       float lt = l[mt];
       lt += __shfl_xor(lt, 16);
       lt += __shfl_xor(lt, 32);
@@ -457,17 +467,7 @@ void k_attn_step(AttnArgs a) {
       const int r = mt * 16 + row;
       if (r < nrows) {
         float M = -__builtin_inff(), L = 0.0f, o[CW];
-        at_f2 pml = {-__builtin_inff(), 0.0f};
-        at_f4 po[(CW + 3) / 4];
-        if constexpr (SH) {
-          if (whole) {
-            const AtPrefix<D> pre(a, shared, head, AT_SHARE_ADD<BF>);
-            pml = pre.ml(r);
-            M = pml.x;
-#pragma unroll
-            for (int x = 0; x < CW; x += 4) po[x / 4] = pre.o(r, c0 + x - (CW < 4 ? c0 & 3 : 0));
-          }
-        }
+        if constexpr (SH) M = pml.x;
 #pragma unroll
         for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[(w * 16 + row) * 2]);
 #pragma unroll

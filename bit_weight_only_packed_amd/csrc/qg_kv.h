@@ -151,6 +151,8 @@ struct ShareArgs {
   KvBatchDev b;
   const int32_t* groups;  // first entries of the groups and n (NULL: one group)
   int ngroups, G, blocks; // blocks: ShareBlocks that the call has room for
+  int64_t least;          // (entry, shared token) pairs below which nothing is shared
+  int window, sinks;
   ShareEntry* share;
   ShareBlock* share_blocks;
   int* pos;               // [row]
@@ -160,6 +162,15 @@ struct ShareArgs {
 constexpr int SHARE_ROWS = 1 << 16;  // rows of a call that share tokens at most
 // shared tokens come in whole tiles of both kernels, and few of them are left to the entries
 constexpr int SHARE_TILE = 64, SHARE_MIN = 256;
+// Bytes of shared tokens, each counted once for every entry that reads it, from which on sharing
+// pays: what it costs is three launches and a second pass over the rows' results.  us of qgkv_attend /
+// with shared tokens, caches not warm, one row an entry (the entries' bytes together), and 8 rows an
+// entry for heads of 128, 4 for heads of 256:
+//   40 q, 8 kv heads of 128   8 x 8,192 tokens (273 MB) 36 / 46, 8 x 16,384 (542) 58 / 55, 64 x 4,096 (1,113) 89 / 70,
+//                             64 x 32,768 (8.7 GB) 1,254 / 134;  8 rows: 16 x 4,096 (278) 70 / 73, 32 x 4,096 (557) 95 / 96
+//   16 q, 2 kv heads of 256   8 x 16,384 (271) 54 / 83, 64 x 4,096 (557) 47 / 79; 4 rows: 32 x 4,096 (278) 97 / 99
+//   8 q, 8 kv heads of 64     8 x 16,384 (271) 31 / 41, 64 x 4,096 (557) 48 / 48
+constexpr int64_t SHARE_PAYS = 512 << 20;
 hipError_t launch_share_plan(const ShareArgs& a, hipStream_t st);
 
 // Rows of one kv head that the few-row kernel takes, (new rows) * (q heads per kv head).
@@ -188,8 +199,8 @@ hipError_t launch_attn_step(const AttnArgs& a, int D, bool bf16, int MT, bool sh
 // its partial
 constexpr int ROWS_WAVES = 4, ROWS_BLOCK = 32 * ROWS_WAVES;
 __host__ __device__ constexpr size_t rows_slot(int D) { return (size_t)ROWS_BLOCK * (D + 2); }
-// parts of a block that sees every token of a slot that holds cap
-int rows_parts(int D, int cap, int splits1);
+// parts of a block that sees every token of a slot that holds cap (rest: but for shared ones)
+int rows_parts(int D, int cap, int splits1, bool rest);
 hipError_t launch_attn_rows(const AttnArgs& a, int D, bool bf16, unsigned blocks, bool shared, hipStream_t st);
 // the tokens that groups share, for all their rows, into a.prefix (blocks * splits slots of it)
 hipError_t launch_attn_prefix(const AttnArgs& a, int D, bool bf16, unsigned blocks, hipStream_t st);

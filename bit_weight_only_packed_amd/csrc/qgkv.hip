@@ -175,7 +175,7 @@ qg_status attend(qg_kv* h, AttnArgs& a, bool shared, hipStream_t st) {
   // 8,192: 53 and 47).  A cache whose slots hold too little for parts saves the join.
   const int64_t blocks = (rows + ROWS_BLOCK - 1) / ROWS_BLOCK * a.b.n * a.c.kv_heads;
   a.splits1 = (int)std::max<int64_t>(1, kRowsSlots / 2 / blocks);
-  a.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kRowsSlots / blocks, rows_parts(D, a.c.cap, a.splits1)));
+  a.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kRowsSlots / blocks, rows_parts(D, a.c.cap, a.splits1, shared)));
   if (blocks * a.splits >= (int64_t)1 << 31) return fail(QG_ERR_UNSUPPORTED, "%lld blocks in one call", (long long)blocks);
   return done(h, launch_attn_rows(a, D, bf16, (unsigned)blocks, shared, st), st);
 }
@@ -374,7 +374,7 @@ qg_status qgkv_attend(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const
 
 qg_status qgkv_attend_shared(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const qg_kv_rows* q, const qg_kv_rows* out,
                              int32_t q_heads, float scale, int32_t window, int32_t sinks, const int32_t* groups,
-                             int32_t n_groups, void* stream) {
+                             int32_t n_groups, int64_t least, void* stream) {
   AttnArgs a{};
   qg_status s = attn_of(h, layer, b, q, out, q_heads, scale, window, sinks, &a);
   if (s != QG_OK || a.b.rows == 0) return s;
@@ -386,8 +386,15 @@ qg_status qgkv_attend_shared(qg_kv_handle h, int32_t layer, const qg_kv_batch* b
   const int64_t blocks = (int64_t)a.b.rows * a.G / ROWS_BLOCK + n_groups, grid = blocks * a.c.kv_heads;
   // without two entries in a group there is nothing to share; and calls of more rows than the
   // workspace has slots for are made of blocks that read the tokens many times either way
-  if (n_groups == a.b.n || a.b.rows > SHARE_ROWS || grid > kRowsSlots) return attend(h, a, false, st);
+  const int64_t token = (int64_t)4 * a.c.kv_heads * h->d.head_dim;  // bytes of a token
+  if (least < 0) least = SHARE_PAYS;
+  const int64_t seen = window ? std::min<int64_t>(a.c.cap, (int64_t)window + sinks) : a.c.cap;  // tokens of an entry at most
+  if (n_groups == a.b.n || a.b.rows > SHARE_ROWS || grid > kRowsSlots || a.b.n * seen < least / token)
+    return attend(h, a, false, st);
   ShareArgs p = h->share;
+  p.least = least / token;
+  p.window = window;
+  p.sinks = sinks;
   p.c = a.c;
   p.b = a.b;
   p.groups = groups;
@@ -404,8 +411,9 @@ qg_status qgkv_attend_shared(qg_kv_handle h, int32_t layer, const qg_kv_batch* b
   AttnArgs x = a;
   x.partial = h->prefix;
   x.partial_floats = h->prefix_floats;
-  x.splits1 = (int)std::max<int64_t>(1, kRowsSlots / 2 / grid);
-  x.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kRowsSlots / grid, rows_parts(h->d.head_dim, a.c.cap, x.splits1)));
+  x.splits = (int)(kRowsSlots / (h->d.head_dim == 256 ? 2 : 1) / grid);
+  x.splits1 = std::max(1, (int)(kRowsSlots / 2 / grid));
+  if (x.splits < 1) x.splits = 1;
   e = launch_attn_prefix(x, h->d.head_dim, h->d.dtype == QG_KV_BF16, (unsigned)grid, st);
   if (e != hipSuccess) return done(h, e, st);
   return attend(h, a, true, st);

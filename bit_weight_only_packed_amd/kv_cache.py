@@ -46,7 +46,7 @@ def bind(L) -> None:
     L.qgkv_append_rotary.argtypes = [vp, i32, ctypes.POINTER(_KvBatch)] + [ctypes.POINTER(_KvRows)] * 4 + [i32, vp, vp]
     L.qgkv_attend.argtypes = [vp, i32, ctypes.POINTER(_KvBatch), ctypes.POINTER(_KvRows), ctypes.POINTER(_KvRows), i32,
                               ctypes.c_float, i32, i32, vp]
-    L.qgkv_attend_shared.argtypes = L.qgkv_attend.argtypes[:-1] + [vp, i32, vp]
+    L.qgkv_attend_shared.argtypes = L.qgkv_attend.argtypes[:-1] + [vp, i32, ctypes.c_int64, vp]
     for f in ("create", "destroy", "extend", "fork", "trim", "compact", "append", "append_rotary", "attend",
               "attend_shared"):
         getattr(L, "qgkv_" + f).restype = ctypes.c_int
@@ -285,18 +285,20 @@ class KVCache:
         ``sinks`` of its slot.  Which slots the rows are of: see the class."""
         return self._attend("attend", (), q, layer, seqs, row_start, max_rows, scale, window, sinks, out, stream)
 
-    def attend_shared(self, q, *, groups=None, layer: int = 0, seqs=None, row_start=None, max_rows: int = None,
-                      scale: float = None, window: int = 0, sinks: int = 0, out=None, stream=None):
+    def attend_shared(self, q, *, groups=None, least: int = None, layer: int = 0, seqs=None, row_start=None,
+                      max_rows: int = None, scale: float = None, window: int = 0, sinks: int = 0, out=None, stream=None):
         """``attend`` where entries share their first tokens (forked answers to a prompt): the
         pages that all entries of a group name alike are read once for all of them.
         groups: int32 [g + 1], the entries at which groups begin, and n (default: all
         entries are one group).  Nothing else need be told: the tables are looked at on
-        the device."""
+        the device.  least: bytes of shared tokens, counted for every entry that reads
+        them, from which on it is done and not left to ``attend`` (default: where it was
+        measured to pay; 0: always)."""
         if groups is None:
-            more = (None, 1)
+            more = (None, 1, -1 if least is None else least)
         else:
             groups = self._index("groups", groups, None, stream)
-            more = (groups.data_ptr(), groups.numel() - 1)
+            more = (groups.data_ptr(), groups.numel() - 1, -1 if least is None else least)
         return self._attend("attend_shared", more, q, layer, seqs, row_start, max_rows, scale, window, sinks, out, stream)
 
     def _attend(self, name, more, q, layer, seqs, row_start, max_rows, scale, window, sinks, out, stream):

@@ -186,13 +186,17 @@ qg_status qgkv_attend(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const
  * call; NULL: all entries are one group).  What a group shares is found in the tables: the
  * leading pages that all its entries name alike (those of qgkv_fork), up to the first
  * of their rows, in whole multiples of 64 tokens, 256 at least; entries that see nothing are left
- * aside.  Groups that share nothing are attended to as by qgkv_attend, and so are
- * calls of very many rows (more than some 512 / kv_heads blocks of 128 rows and q heads of a kv
- * head).  The split of tokens depends on the group, so a row's bits may differ
- * from qgkv_attend's. */
+ * aside.
+ *   least  bytes of keys and values from which on it is done: of the shared tokens, each counted once for every
+ *          entry that reads it, over all groups.  Below that the call costs less as
+ *          qgkv_attend, which it then is but for some 11 us that finding out takes (none where
+ *          n slots as long as their tables would hold less).  Negative: the measured 512 MiB; 0: always.
+ * Calls of very many rows (more than 512 / kv_heads blocks of 128 (row, q head of a kv head) pairs) are
+ * qgkv_attend too.  The split of tokens depends on the group, so a row's bits may differ from
+ * qgkv_attend's. */
 qg_status qgkv_attend_shared(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const qg_kv_rows* q, const qg_kv_rows* out,
                              int32_t q_heads, float scale, int32_t window, int32_t sinks, const int32_t* groups,
-                             int32_t n_groups, void* stream);
+                             int32_t n_groups, int64_t least, void* stream);
 
 #ifdef __cplusplus
 }

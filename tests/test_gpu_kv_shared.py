@@ -18,6 +18,13 @@ def _gpu_present():
         pytest.skip("no GPU")
 
 
+class Always(Q.KVCache):
+    """A cache whose attend_shared shares whatever entries have in common, also where that does not pay."""
+
+    def attend_shared(self, q, **kw):
+        return super().attend_shared(q, **{"least": 0, **kw})
+
+
 class Forked(Pair):
     """Prompts of given lengths, each forked to slots that then grow by their own tokens.
     answers: for each prompt the tokens that its slots add; slots in order, the prompts' own slots last."""
@@ -28,6 +35,8 @@ class Forked(Pair):
         longest = max(p + max(a) for p, a in zip(prompts, answers))
         super().__init__([0] * n + list(prompts), dtype, page, heads, D, extra=room, max_pages=-(-longest // page) + 2, seed=seed,
                          fill=fill)
+        g = self.gpu
+        self.gpu = Always.of(g.pool, g.tables, g.lens, g.refs)
         kv, at = self.gpu, 0
         grow = torch.zeros(kv.max_seqs, dtype=torch.int32)
         for i, a in enumerate(answers):
@@ -216,6 +225,25 @@ def test_calls_of_very_many_rows():
     assert torch.equal(a, b)
 
 
+def test_where_it_does_not_pay():
+    """Below `least` the call is attend, bit for bit: by the slots' room on the host, by the shared tokens on the device."""
+    f = Forked([1000], [[3, 40, 20]], "f16", 16, 2, 64, seed=20)
+    q = rand((3, 8, 64), "f16", 16, 1.5)
+    plain, shared = f.gpu.attend(q), f.gpu.attend_shared(q)
+    f.check(q, shared, [0, 1, 2], [1] * 3)
+    token = 2 * 2 * 64 * 2
+    assert torch.equal(f.gpu.attend_shared(q, least=-1), plain)
+    assert torch.equal(f.gpu.attend_shared(q, least=3 * f.gpu.max_pages * 16 * token + token), plain)
+    assert torch.equal(f.gpu.attend_shared(q, least=3 * 960 * token), shared)          # 960 of the 1,000 are shared
+    assert torch.equal(f.gpu.attend_shared(q, least=3 * 960 * token + token), plain)
+    # a group that shares little comes along with one that shares enough
+    two = Forked([1000, 300], [[3, 40], [5, 6]], "f16", 16, 2, 64, seed=21)
+    q = rand((4, 8, 64), "f16", 17, 1.5)
+    both = two.gpu.attend_shared(q, groups=ints(0, 2, 4))
+    assert torch.equal(two.gpu.attend_shared(q, groups=ints(0, 2, 4), least=2 * (960 + 256) * token), both)
+    assert torch.equal(two.gpu.attend_shared(q, groups=ints(0, 2, 4), least=2 * (960 + 256) * token + token), two.gpu.attend(q))
+
+
 def test_strided_operands_and_refusals():
     f = Forked([600], [[3, 4]], "f16", 16, 2, 64, seed=18)
     qkv, out = rand((2, 12, 64), "f16", 14, 1.5), torch.zeros((8, 2, 64), dtype=torch.float16, device="cuda")
@@ -251,7 +279,7 @@ def test_other_streams_and_calls_between():
 
 def test_a_captured_step_follows_the_tables():
     """Replays after forks, trims and growth give what eager calls give: what is shared is found anew each time."""
-    kv = Q.KVCache(200, 16, 2, 64, max_seqs=4, max_pages=60)
+    kv = Always(200, 16, 2, 64, max_seqs=4, max_pages=60)
     kv.extend([600, 0, 0, 0])
     kv.append(rand((600, 2, 64), "f16", 1), rand((600, 2, 64), "f16", 2), seqs=[0])
     kv.fork([0, 0, 0], [1, 2, 3])
