@@ -16,6 +16,10 @@ template <int TY> hipError_t go(const SampleArgs& a, hipStream_t st) {
     if (b.top_k) b.top_k += at;
     if (b.top_p) b.top_p += at;
     if (b.min_p) b.min_p += at;
+    if (a.whole) {
+      k_sample_row<TY><<<rows, SM_ROW_T, 0, st>>>(b);
+      continue;
+    }
     const dim3 grid((unsigned)a.parts, rows);
     k_sample_max<TY><<<grid, SM_T, 0, st>>>(b);
     if (a.cuts) {
@@ -39,6 +43,14 @@ void sample_parts(int rows, int vocab, int* parts, int* len) {
   *len = ((vocab + p - 1) / p + 7) / 8 * 8;
   *parts = (vocab + *len - 1) / *len;
 }
+
+// Whether a workgroup takes a whole row.  us by parts / by rows, top-k 200 and top-p of all rows in bf16,
+// no limits in fp32, and settings of every kind in fp16:
+//   1 row     1,000    29 / 18, 21 / 13, 27 / 16     16,001  30 / 24, 20 / 18, 29 / 23     32,003  30 / 33, 20 / 28, 29 / 31
+//   32 rows   16,001   49 / 39, 20 / 18, 59 / 41     32,003  51 / 58, 20 / 29, 56 / 55
+//   128 rows  32,003   68 / 57, 28 / 29, 67 / 57     65,537  104 / 90, 48 / 53, 90 / 100
+//   256 rows  65,537   132 / 92, 68 / 57, 106 / 103  131,071 156 / 167, 107 / 106, 138 / 199
+bool sample_whole(int rows, int vocab) { return vocab <= 16384 || (vocab <= 65536 && vocab <= 256 * rows); }
 
 hipError_t launch_sample(const SampleArgs& a, int type, hipStream_t st) {
   if (type == QGS_F16) return go<QGS_F16>(a, st);

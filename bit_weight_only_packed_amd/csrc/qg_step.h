@@ -59,6 +59,7 @@ struct SampleArgs {
   float* probs;
   int parts, part_len;  // of a row
   bool cuts;            // some row may have top-k or top-p
+  bool whole;           // a workgroup takes a whole row
   // workspace, of SAMPLE_ROWS rows at most
   float* part_max;      // [row][part]
   int* part_arg;        // [row][part]
@@ -71,6 +72,7 @@ constexpr int SAMPLE_BUCKETS = 1024;
 constexpr int SAMPLE_LIST = 2048;
 constexpr int SAMPLE_ROWS = 4096;  // rows of a launch: what the workspace holds
 void sample_parts(int rows, int vocab, int* parts, int* len);
+bool sample_whole(int rows, int vocab);
 hipError_t launch_sample(const SampleArgs& a, int type, hipStream_t st);
 
 // what qgs_rotate and qgkv_append_rotary check of a qgs_rotary

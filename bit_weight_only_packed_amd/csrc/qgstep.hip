@@ -168,6 +168,7 @@ namespace {
 
 // the workspace's arrays, one after another on 16-byte boundaries
 size_t lay_out(SampleArgs* a, int rows, int vocab, char* at) {
+  if (sample_whole(rows, vocab)) return 16;  // (none, but a pointer is asked for all the same)
   sample_parts(rows, vocab, &a->parts, &a->part_len);
   const size_t r = (size_t)std::min(rows, SAMPLE_ROWS);  // rows of a launch
   size_t used = 0;
@@ -236,6 +237,7 @@ qg_status qgs_sample(const qgs_sampling* d, void* workspace, size_t bytes, void*
   a.tokens = d->tokens, a.probs = d->probs;
   const bool heat = d->temperature || d->temperature1 > 0.0f;
   a.cuts = heat && (d->top_k || d->top_p || (d->top_k1 > 0 && d->top_k1 < d->vocab) || d->top_p1 < 1.0f);
+  a.whole = sample_whole(d->rows, d->vocab);
   hipStream_t st = (hipStream_t)stream;
   return launched(launch_sample(a, d->dtype, st), st);
 }

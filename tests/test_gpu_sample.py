@@ -52,7 +52,7 @@ SETTINGS = [dict(), dict(temperature=0.7), dict(top_k=1), dict(top_k=5), dict(to
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
-@pytest.mark.parametrize("rows,vocab", [(1, 1), (2, 2), (3, 7), (2, 8), (4, 1000), (3, 2049), (2, 5003)])
+@pytest.mark.parametrize("rows,vocab", [(1, 1), (2, 2), (3, 7), (2, 8), (4, 1000), (3, 2049), (2, 5003), (2, 17001)])
 @pytest.mark.parametrize("settings", range(len(SETTINGS)))
 def test_against_the_definition(dtype, rows, vocab, settings):
     compare(logits_of(rows, vocab, dtype, rows * vocab + settings), draws(rows, settings), **SETTINGS[settings])
@@ -192,6 +192,19 @@ def test_many_rows():
     assert torch.equal(torch.cat(parts), t)
 
 
+def test_many_rows_in_parts():
+    """The same where rows go in parts: one row's logits for all of them, a uniform number each."""
+    n, v = 4096 + 70, 66001
+    x, u = logits_of(1, v, "f16", 8), draws(n, 8)
+    t, p = Q.sample(x.expand(n, v), u, temperature=0.8, top_k=40, top_p=0.9, probs=True)
+    order, w = SO.kept_tokens(x[0].double().cpu().numpy(), float(np.float32(0.8)), 40, float(np.float32(0.9)))
+    by = np.argsort(order)
+    run = np.cumsum(w[by])
+    pick = by[np.searchsorted(run, u.double().cpu().numpy() * run[-1], side="right")]
+    assert np.array_equal(t.cpu().numpy(), np.array(order)[pick])
+    assert np.allclose(p.cpu().numpy(), w[pick] / run[-1], rtol=2.0 ** -23, atol=0)
+
+
 def test_refusals():
     x, u = logits_of(3, 100, "f16", 1), draws(3, 1)
     with pytest.raises(ValueError, match="u must"):
@@ -205,7 +218,7 @@ def test_refusals():
     with pytest.raises(ValueError, match="out"):
         Q.sample(x, u, out=torch.zeros(3, dtype=torch.int64).cuda())
     with pytest.raises(Q.QGError, match="workspace"):
-        Q.sample(x, u, workspace=torch.zeros(16, dtype=torch.uint8).cuda())
+        Q.sample(x, u, workspace=torch.zeros(8, dtype=torch.uint8).cuda())
     assert Q.sample(x[:0], u[:0]).shape == (0,)
 
 
