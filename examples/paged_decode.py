@@ -2,12 +2,13 @@
 
     python examples/paged_decode.py
 
-A small random-weight model (grouped-query attention, sliding window with sinks
-on every second layer) takes a prompt in chunks, forks it into several answers,
-decodes one token of each per step from a captured HIP graph, verifies drafted
-tokens in a batch and takes back the refused ones, ends some of the answers and
-moves the pages that are left together.  All products are 3-bit packed weights
-(QLinear, mlp); all keys and values live in one KVCache.
+A small random-weight model (grouped-query attention with rotary positions, sliding
+window with sinks on every second layer) takes a prompt in chunks, forks it into
+several answers, decodes one sampled token of each per step from a captured HIP
+graph, verifies drafted tokens in a batch and takes back the refused ones, ends some
+of the answers and moves the pages that are left together.  All products are 3-bit
+packed weights (QLinear, mlp); all keys and values live in one KVCache; norms,
+rotation and sampling are the library's (rms_norm, Rotary, sample).
 """
 from __future__ import annotations
 
@@ -30,47 +31,51 @@ def packed(n: int, k: int, gen) -> Q.QLinear:
     return Q.QLinear(codes, scales, k, n, bits=3, max_M=MAX_ROWS)
 
 
-def norm(x):
-    return (x * torch.rsqrt(x.float().square().mean(-1, keepdim=True) + 1e-6)).half()
-
-
 class Layer:
-    def __init__(self, index: int, gen):
-        self.index = index
+    def __init__(self, index: int, gen, rotary):
+        self.index, self.rotary = index, rotary
         self.qkv = packed((Q_HEADS + 2 * KV_HEADS) * HEAD_DIM, HIDDEN, gen)
         self.o = packed(HIDDEN, Q_HEADS * HEAD_DIM, gen)
         self.gate, self.up = packed(FFN, HIDDEN, gen), packed(FFN, HIDDEN, gen)
         self.down = packed(HIDDEN, FFN, gen)
         self.mask = dict(window=24, sinks=4) if index % 2 else {}
 
-    def __call__(self, x, kv, rows):
-        y = self.qkv(norm(x)).view(x.shape[0], -1, HEAD_DIM)  # q | k | v, read where they are
+    def __call__(self, x, kv, rows, shared=False):
+        y = self.qkv(Q.rms_norm(x)).view(x.shape[0], -1, HEAD_DIM)  # q | k | v, read where they are
         q, k, v = y.split([Q_HEADS, KV_HEADS, KV_HEADS], dim=1)
-        kv.append(k, v, layer=self.index, **rows)
-        a = kv.attend(q, layer=self.index, out=torch.empty(q.shape, dtype=q.dtype, device=q.device), **self.mask, **rows)
-        x = x + self.o(a.view(x.shape[0], -1))
-        return x + Q.mlp(self.gate, self.up, self.down, norm(x))
+        kv.append_rotated(q, k, v, self.rotary, layer=self.index, out=q, **rows)
+        attend = kv.attend_shared if shared else kv.attend
+        a = attend(q, layer=self.index, out=torch.empty(q.shape, dtype=q.dtype, device=q.device), **self.mask, **rows)
+        y = Q.rms_norm(self.o(a.view(x.shape[0], -1)), residual=x)  # x holds the sum
+        return x + Q.mlp(self.gate, self.up, self.down, y)
 
 
 class Model:
     def __init__(self, layers: int = 2, seed: int = 0):
         gen = torch.Generator().manual_seed(seed)
-        self.layers = [Layer(i, gen) for i in range(layers)]
+        rotary = Q.Rotary(HEAD_DIM)
+        self.layers = [Layer(i, gen, rotary) for i in range(layers)]
         self.embed = torch.randn((VOCAB, HIDDEN), generator=gen).half().cuda()
 
     def cache(self, pages: int = 48, slots: int = 4, cls=Q.KVCache) -> Q.KVCache:
         return cls(pages, 16, KV_HEADS, HEAD_DIM, layers=len(self.layers), max_seqs=slots, max_pages=16)
 
-    def rows(self, tokens, kv, **rows):
-        """Hidden states of new tokens, whose room in the cache has been made."""
+    def rows(self, tokens, kv, shared=False, **rows):
+        """Hidden states of new tokens, whose room in the cache has been made.  shared: the rows' slots may hold
+        the same pages, as forked answers do."""
         x = self.embed[tokens]
         for layer in self.layers:
-            x = layer(x, kv, rows)
+            x = layer(x, kv, rows, shared)
         return x
 
-    def pick(self, x):
-        """The next token of each row."""
-        return (norm(x) @ self.embed.t()).argmax(-1)
+    def logits(self, x):
+        return Q.rms_norm(x) @ self.embed.t()
+
+    def pick(self, x, u=None, **settings):
+        """The next token of each row: the likeliest, or by uniform numbers u and the settings of sample."""
+        if u is None:
+            u, settings = torch.zeros(x.shape[0], device=x.device), dict(temperature=0.0)
+        return Q.sample(self.logits(x), u, **settings).long()
 
 
 def ints(*x):
@@ -88,14 +93,16 @@ def prompt(model, kv, slot: int, tokens):
 
 
 class Decoder:
-    """One token of every listed slot per replay of a captured graph."""
+    """One token of every listed slot per replay of a captured graph: the likeliest, or with settings of ``sample`` by
+    uniform numbers drawn before each."""
 
-    def __init__(self, model, kv, slots, tokens):
+    def __init__(self, model, kv, slots, tokens, **settings):
         self.tokens = tokens.clone()
         self.grow = torch.zeros(kv.max_seqs, dtype=torch.int32, device="cuda")
         self.seqs = ints(*slots)
         self.grow[self.seqs.long()] = 1
-        self.model, self.kv = model, kv
+        self.model, self.kv, self.settings = model, kv, settings
+        self.u = torch.zeros(len(slots), device="cuda") if settings else None
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):  # what is made once (workspaces of the library calls) is made before the capture
@@ -108,9 +115,12 @@ class Decoder:
 
     def eager(self):
         self.kv.extend(self.grow)
-        self.tokens.copy_(self.model.pick(self.model.rows(self.tokens, self.kv, seqs=self.seqs)))
+        x = self.model.rows(self.tokens, self.kv, shared=True, seqs=self.seqs)
+        self.tokens.copy_(self.model.pick(x, self.u, **self.settings))
 
     def step(self):
+        if self.u is not None:
+            self.u.uniform_()
         self.graph.replay()
         return self.tokens
 
@@ -138,7 +148,8 @@ def main():
     first = prompt(model, kv, 0, torch.arange(70, device="cuda") * 37 % VOCAB)
     kv.fork(ints(0, 0, 0), ints(1, 2, 3))  # four answers to one prompt
     tokens = (first + torch.arange(4, device="cuda")) % VOCAB
-    dec = Decoder(model, kv, [0, 1, 2, 3], tokens)
+    torch.manual_seed(0)
+    dec = Decoder(model, kv, [0, 1, 2, 3], tokens, temperature=0.8, top_k=50, top_p=0.95)
     for _ in range(20):
         tokens = dec.step()
     kept, tokens = verify(model, kv, [0, 1, 2, 3], tokens, torch.randint(0, VOCAB, (4, 7), device="cuda"))
