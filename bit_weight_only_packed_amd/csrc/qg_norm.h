@@ -15,6 +15,8 @@ namespace qg {
 typedef uint32_t nm_u4 __attribute__((ext_vector_type(4), aligned(2)));  // 16 bytes of 16-bit elements, where they are
 typedef uint32_t nm_u2 __attribute__((ext_vector_type(2), aligned(1)));  // 8 codes
 
+constexpr int NM_TEAMS = 256;  // threads of a workgroup of several rows
+
 template <bool BF> __device__ __forceinline__ float nm_f32(uint32_t h) {
   if constexpr (BF) return __builtin_bit_cast(float, h << 16);
   else return (float)__builtin_bit_cast(_Float16, (uint16_t)h);
@@ -54,15 +56,29 @@ template <bool MAX> __device__ __forceinline__ float nm_all(float x, float* lds)
   return t;
 }
 
+// the same over the T (a power of two) lanes of a row
+template <bool MAX> __device__ __forceinline__ float nm_team(float x, int T) {
+  for (int o = T >> 1; o; o >>= 1) {
+    const float y = __shfl_xor(x, o);
+    x = MAX ? fmaxf(x, y) : x + y;
+  }
+  return x;
+}
+
 // codes of 8 values: v / s rounded to nearest even.  |v| / s is at most the type's largest but
 // for the rounding of s, which the rounding of the code takes away.
 template <int CODES> __device__ __forceinline__ kv_u2 nm_codes(const float (&v)[8], float s) {
   kv_u2 w = {0, 0};
   if (!(s > 0.0f)) return w;  // zeros, or a NaN scale
   float c[8];
-  const float r = 1.0f / s;
+  if (__builtin_expect(s < 0x1p-100f, 0)) {  // 1 / s may overflow
 #pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = s < 0x1p-100f ? v[i] / s : v[i] * r;  // (1 / s may overflow below that)
+    for (int i = 0; i < 8; ++i) c[i] = v[i] / s;
+  } else {
+    const float r = 1.0f / s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = v[i] * r;
+  }
   if constexpr (CODES == QGS_INT8) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i / 4] |= ((uint32_t)(int)rintf(c[i]) & 0xFFu) << (8 * (i & 3));
@@ -76,13 +92,17 @@ template <int CODES> __device__ __forceinline__ kv_u2 nm_codes(const float (&v)[
   return w;
 }
 
-// One row per workgroup; thread t holds chunks t, t + blockDim, ... of 8 elements, as the
-// 16-bit values that they are.
-template <bool BF, int C, int CODES> __global__ __launch_bounds__(1024) void k_rms_norm(NormArgs a) {
+// Thread t of a row holds its chunks t, t + T, ... of 8 elements, as the 16-bit values that
+// they are.  A row is a workgroup's, or, where it is short (TEAM: the heads of q and k), a.team lanes'
+// of a wave: 60,000 rows of 128 elements @@ us, with a wave each 27.9.
+template <bool BF, int C, int CODES, bool TEAM> __global__ __launch_bounds__(TEAM ? NM_TEAMS : 1024) void k_rms_norm(NormArgs a) {
   __shared__ float lds[16];
-  const int64_t row = a.first + (int64_t)blockIdx.x;
-  const int T = blockDim.x;
-  const auto place = [&](int c) { return (c * T + (int)threadIdx.x) * 8; };
+  const int T = TEAM ? a.team : (int)blockDim.x, tid = TEAM ? (int)threadIdx.x & (T - 1) : (int)threadIdx.x;
+  const int64_t row = a.first + (TEAM ? (int64_t)blockIdx.x * (NM_TEAMS / T) + threadIdx.x / T : (int64_t)blockIdx.x);
+  if (TEAM && row >= a.rows) a.n = 0;  // (its lanes go along for the sums)
+  const auto place = [&](int c) { return (c * T + tid) * 8; };
+  const auto sum = [&](float x) { return TEAM ? nm_team<false>(x, T) : nm_all<false>(x, lds); };
+  const auto most = [&](float x) { return TEAM ? nm_team<true>(x, T) : nm_all<true>(x, lds); };
   const uint16_t* x = a.x + row * a.x_stride;
   kv_u4 h[C];
 #pragma unroll
@@ -105,7 +125,7 @@ template <bool BF, int C, int CODES> __global__ __launch_bounds__(1024) void k_r
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(nm_at<BF>(h[c], i), nm_at<BF>(h[c], i), ss);
-  ss = nm_all<false>(ss, lds);
+  ss = sum(ss);
   const float n = (float)a.n;
   float rs = 1.0f / sqrtf(ss / n + a.eps);
   int e = 0;  // the row is taken times 2^-e
@@ -119,7 +139,7 @@ template <bool BF, int C, int CODES> __global__ __launch_bounds__(1024) void k_r
         const float v = fabsf(nm_at<BF>(h[c], i));
         top = fmaxf(top, v == v ? v : __builtin_inff());
       }
-    top = nm_all<true>(top, lds);
+    top = most(top);
     if (top < __builtin_inff()) {  // (NaN and infinities stay as the formula has them)
       e = ilogbf(top);
       ss = 0.0f;
@@ -130,7 +150,7 @@ template <bool BF, int C, int CODES> __global__ __launch_bounds__(1024) void k_r
           const float v = ldexpf(nm_at<BF>(h[c], i), -e);
           ss = __builtin_fmaf(v, v, ss);
         }
-      ss = nm_all<false>(ss, lds);
+      ss = sum(ss);
       rs = 1.0f / sqrtf(ss / n + ldexpf(a.eps, -2 * e));
     }
   }
@@ -178,7 +198,7 @@ template <bool BF, int C, int CODES> __global__ __launch_bounds__(1024) void k_r
         normed(y, c);
         all = largest(y, all);
       }
-      all = nm_all<true>(all, lds);
+      all = most(all);
     }
     const int per = a.group ? (a.n + a.group - 1) / a.group : 1;
 #pragma unroll
@@ -189,10 +209,9 @@ template <bool BF, int C, int CODES> __global__ __launch_bounds__(1024) void k_r
       float m = all;
       if (a.group) {  // 4, 8 or 16 lanes share a group
         m = largest(y, 0.0f);
-        m = fmaxf(m, __shfl_xor(m, 1));
-        m = fmaxf(m, __shfl_xor(m, 2));
-        if (a.group > 32) m = fmaxf(m, __shfl_xor(m, 4));
-        if (a.group > 64) m = fmaxf(m, __shfl_xor(m, 8));
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1)
+          if (8 * o < a.group && o < T) m = fmaxf(m, __shfl_xor(m, o));
       }
       const float s = m < __builtin_inff() ? m / TOP : __builtin_nanf("");
       if (at < a.n && (a.group ? at % a.group == 0 : at == 0)) a.scales[row * per + (a.group ? at / a.group : 0)] = s;

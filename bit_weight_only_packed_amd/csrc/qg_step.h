@@ -17,9 +17,10 @@ struct NormArgs {
   int64_t x_stride, residual_stride, out_stride;
   int rows, n, group;
   int first;  // the launch's first row
+  int team;   // lanes of a row, a power of two, where a wave has several
   float eps;
 };
-hipError_t launch_rms_norm(const NormArgs& a, bool bf16, int codes, int cus, hipStream_t st);
+hipError_t launch_rms_norm(const NormArgs& a, bool bf16, int codes, hipStream_t st);
 
 struct RotDev {
   const uint64_t* turns;

@@ -122,7 +122,7 @@ qg_status qgs_rms_norm(const qgs_norm* d, void* stream) {
   a.rows = d->rows, a.n = d->n, a.group = d->group;
   a.eps = d->eps;
   hipStream_t st = (hipStream_t)stream;
-  return launched(launch_rms_norm(a, d->dtype == QGS_BF16, d->codes, cus, st), st);
+  return launched(launch_rms_norm(a, d->dtype == QGS_BF16, d->codes, st), st);
 }
 
 qg_status qgs_rotate(const qgs_rows* d, const qgs_rotary* rotary, void* stream) {

@@ -92,6 +92,11 @@ def _empty(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+def _count(name, n) -> None:
+    if n > 2 ** 31 - 1:
+        raise ValueError(f"{name}: {n} in one call")
+
+
 def _matrix(name, t, shape, dtype, dev) -> int:
     """The row stride of [rows][n]."""
     if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
@@ -116,6 +121,7 @@ def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, quant=None, gr
         raise ValueError(f"x must be float16 or bfloat16 [rows][n] on a GPU, not {x.dtype} {list(x.shape)} on {x.device}")
     shape, dtype, dev = x.shape, x.dtype, x.get_device()
     rows, n = shape
+    _count("rows", rows)
     d = _Norm()
     d.x_stride = _matrix("x", x, shape, dtype, dev)
     d.x, d.rows, d.n, d.dtype, d.group, d.eps = x.data_ptr(), rows, n, types[dtype], group, eps
@@ -221,6 +227,7 @@ class Rotary:
         if x.dim() != 3 or x.dtype not in types or not x.is_cuda:
             raise ValueError(f"x must be float16 or bfloat16 [rows][heads][head_dim] on a GPU, not {x.dtype} {list(x.shape)} on {x.device}")
         rows, heads, d = x.shape
+        _count("rows", rows)
         dev = x.get_device()
         if self.turns.get_device() != dev:
             raise ValueError(f"the frequencies are on {self.turns.device}, x on {x.device}")
@@ -256,6 +263,7 @@ def sample(logits, u, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, probs: 
         raise ValueError(f"logits must be float16, bfloat16 or float32 [rows][vocab] on a GPU, not {logits.dtype} "
                          f"{list(logits.shape)} on {logits.device}")
     rows, vocab = logits.shape
+    _count("rows", rows)
     dev = logits.get_device()
     d = _Sampling()
     d.stride = _matrix("logits", logits, logits.shape, logits.dtype, dev)
@@ -272,7 +280,7 @@ def sample(logits, u, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, probs: 
         if isinstance(value, torch.Tensor):
             setattr(d, name, each(name, value, dtype))
         else:
-            setattr(d, name + "1", value)
+            setattr(d, name + "1", min(max(value, 0), 2 ** 31 - 1) if name == "top_k" else value)
     if out is None:
         out = _empty((rows,), torch.int32, logits, stream)
     d.tokens = each("out", out, torch.int32)

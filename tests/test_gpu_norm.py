@@ -38,7 +38,7 @@ def check(y, ref, dtype):
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("rows,n", [(1, 1), (1, 7), (3, 8), (2, 63), (5, 64), (1, 511), (4, 1280), (1, 5120), (33, 5120),
-                                    (2, 8191), (1, 8200), (3, 17408), (1, 32768), (600, 1030), (700, 5120), (1, 32761)])
+                                    (2, 8191), (1, 8200), (3, 17408), (1, 32768), (600, 1030), (700, 5120), (1, 32761), (67, 128), (1001, 72), (9, 200), (7, 257)])
 @pytest.mark.parametrize("residual,weight", [(True, True), (False, True), (True, False), (False, False)])
 def test_against_the_definition(dtype, rows, n, residual, weight):
     x = rand((rows, n), dtype, rows + n)
@@ -54,7 +54,7 @@ def test_against_the_definition(dtype, rows, n, residual, weight):
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
 @pytest.mark.parametrize("rows,n,group", [(1, 1, 0), (3, 5, 32), (2, 128, 128), (5, 1280, 64), (2, 1000, 32), (4, 1001, 128),
-                                          (3, 17408, 128), (2, 17408, 0), (700, 520, 64), (2, 32768, 32), (1, 8191, 0)])
+                                          (3, 17408, 128), (2, 17408, 0), (700, 520, 64), (2, 32768, 32), (1, 8191, 0), (65, 128, 0), (67, 40, 128), (33, 72, 64), (5, 250, 32)])
 def test_codes(dtype, kind, rows, n, group):
     x, res, w = rand((rows, n), dtype, n), rand((rows, n), dtype, n + 1), rand((n,), dtype, n + 2)
     h = summed(x, res)
@@ -140,12 +140,13 @@ def test_non_finite_rows_stay_their_own():
 
 
 def test_rows_do_not_depend_on_the_call():
-    """A row alone and among few has the same bits (both run with as many threads); so has every repeat."""
-    x, w = rand((40, 5120), "f16", 8), rand((5120,), "f16", 9)
-    y = Q.rms_norm(x, w)
-    for i in (0, 17, 39):
-        assert torch.equal(Q.rms_norm(x[i:i + 1], w), y[i:i + 1])
-    assert torch.equal(Q.rms_norm(x, w), y)
+    """A row alone and among few or many has the same bits; so has every repeat."""
+    for n in (128, 200, 500, 5120, 17408):
+        x, w = rand((2100, n), "f16", 8), rand((n,), "f16", 9)
+        y = Q.rms_norm(x, w)
+        for i in (0, 17, 2099):
+            assert torch.equal(Q.rms_norm(x[i:i + 1], w), y[i:i + 1])
+        assert torch.equal(Q.rms_norm(x[:40], w), y[:40]) and torch.equal(Q.rms_norm(x, w), y)
 
 
 def test_refusals():
