@@ -66,21 +66,17 @@ __host__ __device__ constexpr int rw_parts(int tiles, int splits1, int least = R
 template <int D> constexpr int RW_DEEP = D == 256 ? 1 : 4;
 constexpr int RW_MFMA = 0x8, RW_DS_READ = 0x100;
 
-enum { RW_WHOLE = 0, RW_PREFIX = 1, RW_REST = 2 };  // all tokens; a group's shared ones; an entry's others
-
-template <int D_, int MODE_ = RW_WHOLE> struct RowsShape {
-  static constexpr int D = D_, MODE = MODE_;
+template <int D> struct RowsShape {
   static constexpr int NW = ROWS_WAVES;     // waves of a workgroup
   static constexpr int BM = ROWS_BLOCK;     // rows of a block
-  static constexpr int KT = D == 256 || (MODE == RW_PREFIX && D == 128) ? 32 : 64;  // tokens of a tile
+  static constexpr int KT = D == 256 ? 32 : 64;  // tokens of a tile
   static constexpr int KC = D / 8;          // 16-byte chunks of a token's key or value
   static constexpr int NT = KT / 32;        // 32-token groups
   static constexpr int ND = D / 32;         // 32-column groups
   static constexpr int bytes = KT * D * 2;  // a tile's keys (or values)
   static constexpr int LD = bytes / 1024 / NW;  // 1 KiB copies per wave of them
   static constexpr int RW = KT / NW;        // tokens that a wave copies (they lie in one page)
-  static constexpr int NB = MODE == RW_PREFIX ? 4 : 2;  // tiles of keys, and of values, in LDS
-  static constexpr int AHEAD = NB - 1;      // tiles of keys on their way
+  static constexpr int NB = 2;              // tiles of keys, and of values, in LDS
   static_assert(RW <= 16, "a wave's tokens of a tile lie in one page");
 };
 
@@ -116,8 +112,9 @@ __device__ __forceinline__ void rw_barrier() {
 }
 
 // a wave's 32 rows
-template <class S> struct RowsState {
-  kv_u4 Q[S::D / 16];
+template <int D> struct RowsState {
+  using S = RowsShape<D>;
+  kv_u4 Q[D / 16];
   at_f16 O[S::ND];
   float m, l;   // m: in units of q . k
   int pos;      // this lane's row's position
@@ -125,8 +122,8 @@ template <class S> struct RowsState {
 };
 
 // its scores with a tile, and their weights
-template <class S> using RowsScores = at_f16[S::NT];
-template <class S> using RowsWeights = kv_u4[2 * S::NT];
+template <int D> using RowsScores = at_f16[RowsShape<D>::NT];
+template <int D> using RowsWeights = kv_u4[2 * RowsShape<D>::NT];
 
 // byte of this lane's part of the key reads, and of the value reads, but for what is
 // constant per read: an exclusive-or for the chunk, an immediate for the token
@@ -141,9 +138,9 @@ template <int D> __device__ __forceinline__ int rw_val_byte(int lane) {
 }
 
 // scores of the wave's rows with a tile of keys
-template <class S, bool BF>
-__device__ __forceinline__ void rw_scores(RowsScores<S>& s, const RowsState<S>& r, const char* keys, int lane) {
-  constexpr int D = S::D;
+template <int D, bool BF>
+__device__ __forceinline__ void rw_scores(RowsScores<D>& s, const RowsState<D>& r, const char* keys, int lane) {
+  using S = RowsShape<D>;
   int kb = rw_key_byte<D>(lane);
   asm volatile("" : "+v"(kb));  // one instruction per read, not a register each: they are needed
   constexpr int N = S::NT * (D / 16), DEEP = RW_DEEP<D>;
@@ -168,10 +165,10 @@ __device__ __forceinline__ void rw_scores(RowsScores<S>& s, const RowsState<S>& 
 }
 
 // scores of tile tok .. tok + KT - 1 to weights; masked: some row does not see all of it
-template <class S, bool BF>
-__device__ __forceinline__ void rw_softmax(RowsWeights<S>& P, RowsScores<S>& s, RowsState<S>& r,
+template <int D, bool BF>
+__device__ __forceinline__ void rw_softmax(RowsWeights<D>& P, RowsScores<D>& s, RowsState<D>& r,
                                            const AttnArgs& a, int tok, bool masked, int lane) {
-  constexpr int D = S::D;
+  using S = RowsShape<D>;
   const int h = lane >> 5;
   if (masked) {
     const SeenFrom seen(r.pos, tok + 4 * h, a.window, a.sinks);
@@ -231,10 +228,10 @@ __device__ __forceinline__ void rw_softmax(RowsWeights<S>& P, RowsScores<S>& s, 
 
 // products of the weights of tile tok with its values
 // noted: the tile's values that were not finite and have been taken out, or NULL
-template <class S, bool BF>
-__device__ __forceinline__ void rw_products(RowsState<S>& r, const RowsWeights<S>& P, const AttnArgs& a,
+template <int D, bool BF>
+__device__ __forceinline__ void rw_products(RowsState<D>& r, const RowsWeights<D>& P, const AttnArgs& a,
                                             const char* vals, int tok, const uint8_t* noted, int lane) {
-  constexpr int D = S::D;
+  using S = RowsShape<D>;
   int vb = rw_val_byte<D>(lane);
   asm volatile("" : "+v"(vb));
   const auto val = [&](int x, int k, int b) {  // 32-column group x, 16-token step k, tokens 8 b ..
@@ -283,8 +280,9 @@ __device__ __forceinline__ void rw_products(RowsState<S>& r, const RowsWeights<S
 // A block of the call.  Longest first: the last block of every (entry, kv head), then
 // the one before, ...; kv heads fastest, so that with 8 of them (or a multiple) a
 // head's blocks meet its tokens in one XCD's L2.
+enum { RW_WHOLE = 0, RW_PREFIX = 1, RW_REST = 2 };  // all tokens; a group's shared ones; an entry's others
 template <int D, int MODE = RW_WHOLE> struct RowsBlock {
-  using S = RowsShape<D, MODE>;
+  using S = RowsShape<D>;
   int head, rb, total, r0, nrows, pe, p0, p1, parts;  // rb < 0: none; parts that share its tiles
   int cut = 0;  // tiles of the list that are others' to compute
   KvEntry e;
@@ -310,7 +308,7 @@ template <int D, int MODE = RW_WHOLE> struct RowsBlock {
 };
 // a block of a group's rows with its shared tokens
 template <int D> struct RowsBlock<D, RW_PREFIX> {
-  using S = RowsShape<D, RW_PREFIX>;
+  using S = RowsShape<D>;
   int head, rb, total, r0, nrows, pe, p0, p1, parts;
   static constexpr int cut = 0;
   KvEntry e;
@@ -349,9 +347,9 @@ __device__ __forceinline__ void rw_prefix_place(const AttnArgs& a, unsigned bloc
 }
 
 template <int D, bool BF, int MODE = RW_WHOLE>
-__global__ __launch_bounds__(64 * ROWS_WAVES) __attribute__((amdgpu_waves_per_eu(D == 64 ? 3 : D == 256 && MODE == RW_PREFIX ? 1 : 2)))
+__global__ __launch_bounds__(64 * ROWS_WAVES) __attribute__((amdgpu_waves_per_eu(D == 64 ? 3 : 2)))
 void k_attn_rows(AttnArgs a) {
-  using S = RowsShape<D, MODE>;
+  using S = RowsShape<D>;
   __shared__ __align__(1024) char keys[S::NB * S::bytes];
   __shared__ __align__(1024) char vals[S::NB * S::bytes];
   __shared__ __align__(16) uint8_t notes[S::bytes / 8];
@@ -375,7 +373,7 @@ void k_attn_rows(AttnArgs a) {
   const int32_t* table = a.c.tables + (int64_t)e.slot * a.c.max_pages;
 
   // this wave's rows
-  RowsState<S> r;
+  RowsState<D> r;
   const int rw = r0 + wave * 32 + col;
   const bool live = rw < total, alive = r0 + wave * 32 < total;
   const int ri = live ? rw / a.G : 0;
@@ -492,41 +490,37 @@ void k_attn_rows(AttnArgs a) {
     at_tok = token(min(t, nt - 1)) + lane0;
     at_id = kv_table(table, min(at_tok, p1) >> a.c.page_shift);
   };
-  constexpr int A = S::AHEAD;
-  const auto send = [&](int t) {  // keys t + A, values t + A - 1
-    const int to = (t + A) & (S::NB - 1), to1 = (t + A - 1) & (S::NB - 1);
+  const auto send = [&](int t) {
+    const int to = (t + 1) & (S::NB - 1), to1 = t & (S::NB - 1);
     const char* const from = pool0 + kv_page(a.c, at_id) * page_bytes + (at_tok & mask) * (D * 2);
-    if (t + A < nt)
+    if (t + 1 < nt)
 #pragma unroll
       for (int i = 0; i < S::LD; ++i) rw_copy(from, kofs[i], keys + to * S::bytes + (wave * S::LD + i) * 1024);
-    if (t + A - 1 >= 0 && (A == 1 || t + A - 1 < nt))
+    if (t >= 0)
 #pragma unroll
       for (int i = 0; i < S::LD; ++i) rw_copy(before + v_bytes, vofs[i], vals + to1 * S::bytes + (wave * S::LD + i) * 1024);
     before = from;
-    look(t + A + 1);
+    look(t + 2);
   };
   const auto bound = [&](int t) {
-    // this wave's copies of keys t and values t - 1 have landed: all, or all but those of A - 1 sends
-    if (A == 1 || t - 1 + A >= nt) __builtin_amdgcn_s_waitcnt(at_wait_vm(0));
-    else __builtin_amdgcn_s_waitcnt(at_wait_vm((A - 1) * 2 * S::LD));
+    __builtin_amdgcn_s_waitcnt(at_wait_vm(0));  // this wave's copies of keys t and values t - 1 have landed
     rw_barrier();  // everyone's have, and the buffers of the tile before are free
     noted = t > 0 ? mend(t - 1, val_buf(t - 1)) : nullptr;
   };
   if (nt > 0) {
     look(0);
-#pragma unroll
-    for (int i = -A; i < 0; ++i) send(i);
+    send(-1);
     bound(0);
     // (a wave without rows only copies and keeps step)
-    if (alive) rw_scores<S, BF>(s, r, key_buf(0), lane);
+    if (alive) rw_scores<D, BF>(s, r, key_buf(0), lane);
     for (int t = 0; t < nt; ++t) {
       send(t);
-      if (alive) rw_softmax<S, BF>(P, s, r, a, token(t), t < wclear0 || t >= wclear1, lane);
+      if (alive) rw_softmax<D, BF>(P, s, r, a, token(t), t < wclear0 || t >= wclear1, lane);
       bound(t + 1);
       if (!alive) continue;
       __builtin_amdgcn_s_setprio(1);  // a product is one issue in eight: let it have it
-      rw_products<S, BF>(r, P, a, val_buf(t), token(t), noted, lane);
-      if (t + 1 < nt) rw_scores<S, BF>(s, r, key_buf(t + 1), lane);
+      rw_products<D, BF>(r, P, a, val_buf(t), token(t), noted, lane);
+      if (t + 1 < nt) rw_scores<D, BF>(s, r, key_buf(t + 1), lane);
       __builtin_amdgcn_s_setprio(0);
     }
   }

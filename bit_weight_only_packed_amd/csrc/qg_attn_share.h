@@ -151,7 +151,7 @@ __global__ __launch_bounds__(SP_T) void k_share_plan(ShareArgs a) {
 
 // A block's parts, joined in part order into the first one's slot; RJ_ROWS rows a workgroup.
 template <int D> __global__ __launch_bounds__(RJ_THREADS) void k_share_join(AttnArgs a) {
-  using S = RowsShape<D, RW_PREFIX>;
+  using S = RowsShape<D>;
   constexpr int PER = S::BM / RJ_ROWS, MOST = 512;  // (parts of a block: the slots of the workspace at most)
   __shared__ float fac[RJ_ROWS][MOST];
   const unsigned id = blockIdx.x / PER, blocks = gridDim.x / PER;

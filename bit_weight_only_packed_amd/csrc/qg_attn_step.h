@@ -47,6 +47,9 @@ constexpr int ST_TK = 32;  // tokens of a tile
 // whose run holds many short sequences ends last (48 sequences of 3 to 24,577 tokens, 8
 // kv heads of 128, an (entry, kv head) counted as its tiles alone: 384 us; at 16: 109).
 constexpr int ST_COST = 16;
+// Tiles of what is left of an entry behind its shared tokens, up to which one workgroup takes all of it: 8 answers
+// of 1 to 300 own tokens 32.5 us without, 29.5 at 16 and 64; 64 of 9 to 1,500 116 without, 115 at 16, 118 at 64.
+constexpr int ST_SHORT = 16;
 // added to a weight's exponent, at most 0, for the matrix cores' sake
 template <bool BF> constexpr float ST_BIAS = BF ? 0.0f : AT_FP16_TOP;
 // and what that is more than the many-row kernel's, whose results of shared tokens are joined
@@ -241,7 +244,15 @@ void k_attn_step(AttnArgs a) {
     const int len = __builtin_amdgcn_readfirstlane(pre[j + 1]) - before, nt = len - ST_COST;
     const int seg = before * heads, head = (u - seg) / len;
     const int tile0 = seg + head * len + ST_COST;  // place of (entry, head)'s first tile
-    const int t0 = max(u - tile0, 0), t1 = min(nt, u1 - tile0);
+    int t0 = max(u - tile0, 0), t1 = min(nt, u1 - tile0);
+    ShareEntry shared{};
+    if constexpr (SH) {
+      shared = a.share[j];
+      shared.tokens = __builtin_amdgcn_readfirstlane(shared.tokens), shared.row = __builtin_amdgcn_readfirstlane(shared.row);
+      // what is left of an entry behind its shared tokens is short as a rule: then it is the workgroup's that
+      // has its first place, and no two need to meet for it
+      if (shared.tokens > 0 && nt <= ST_SHORT) t0 = u > tile0 - ST_COST ? nt : 0, t1 = nt;
+    }
     u = tile0 + nt;
     if (t0 >= t1) continue;  // the run ends before its first tile
     KvEntry e = list[j];
@@ -249,13 +260,8 @@ void k_attn_step(AttnArgs a) {
     e.row0 = __builtin_amdgcn_readfirstlane(e.row0), e.rows = __builtin_amdgcn_readfirstlane(e.rows);
     const int p0 = e.pos, p1 = p0 + e.rows - 1, nrows = e.rows * a.G;
     const TileRange<ST_TK> tr(p0, p1, a.window, a.sinks);
-    ShareEntry shared{};
     int cut = 0;  // tiles of shared tokens
-    if constexpr (SH) {
-      shared = a.share[j];
-      shared.tokens = __builtin_amdgcn_readfirstlane(shared.tokens), shared.row = __builtin_amdgcn_readfirstlane(shared.row);
-      cut = tr.before(shared.tokens / ST_TK);
-    }
+    if constexpr (SH) cut = tr.before(shared.tokens / ST_TK);
     const int32_t* table = a.c.tables + (int64_t)e.slot * a.c.max_pages;
 
     // the rows of this kv head: row r is new token r / G, q head head * G + r % G
