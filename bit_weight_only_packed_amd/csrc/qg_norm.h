@@ -4,8 +4,12 @@
 //   h = round(x + r),  y = h w / sqrt(mean h^2 + eps),  codes round(y / s), s = max |y| / top
 //
 // Bound.  HBM where rows are many: each operand is read once and each output written
-// once, and a row lives in registers between its sum and its outputs.  Where rows are few, the
-// call: one round trip to memory, one sum over the workgroup, one store.
+// once, and a row lives in registers between its sum and its outputs.  8,191 rows of 5,120 with the residual
+// (bf16): 53 us, 336 MB at 6.3 TB/s (some of the residual from the last-level cache); 2,047 rows of 17,408 to e4m3
+// with a scale for each 128: 37 us, 107 MB at 2.9 TB/s (80 registers a thread
+// with three chunks; with four, 100 of them and fewer waves, 55).
+// Where rows are few, the call: one round trip to memory, one sum over the workgroup, one store (one row of
+// 5,120: 3.2 us).
 #pragma once
 #include "qg_attn.h"
 #include "qg_step.h"
