@@ -135,8 +135,10 @@ class KVCache:
         self._dev = pool.get_device()
         self._dtype = pool.dtype
         self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        self._args = (_KvBatch(), _KvRows(), _KvRows(), _KvRows(), _KvRows())
+        self._args = (_KvBatch(), _KvRows(), _KvRows())
+        self._more = (_KvRows(), _KvRows())
         self._refs = tuple(ctypes.byref(x) for x in self._args)
+        self._more_refs = tuple(ctypes.byref(x) for x in self._more)
 
     @property
     def handle(self):
@@ -242,11 +244,11 @@ class KVCache:
         """Write the rows' keys and values, [rows][kv_heads][head_dim] each.  Which
         slots: see the class; one slot takes one entry of a call."""
         st = self._on(stream)
-        _, ka, va = self._args[:3]
+        _, ka, va = self._args
         rows, _ = self._rows(ka, "k", k, self.kv_heads)
         self._rows(va, "v", v, self.kv_heads, rows)
         held = self._batch(rows, seqs, row_start, max_rows, stream)
-        rb, rk, rv = self._refs[:3]
+        rb, rk, rv = self._refs
         self._call("append", layer, rb, rk, rv, st)
         del held
 
@@ -257,7 +259,7 @@ class KVCache:
         is returned (out may be q; q None: keys and values only).  rotary: a ``Rotary`` on
         the cache's GPU.  out of a row at a position before 0 (an idle slot's) is 0."""
         st = self._on(stream)
-        _, ka, va, qa, oa = self._args
+        (_, ka, va), (qa, oa) = self._args, self._more
         rows, _ = self._rows(ka, "k", k, self.kv_heads)
         self._rows(va, "v", v, self.kv_heads, rows)
         if rotary.turns.get_device() != self._dev:
@@ -272,7 +274,7 @@ class KVCache:
         elif out is not None:
             raise ValueError("out without q")
         held = self._batch(rows, seqs, row_start, max_rows, stream)
-        rb, rk, rv, rq, ro = self._refs
+        (rb, rk, rv), (rq, ro) = self._refs, self._more_refs
         self._call("append_rotary", layer, rb, rk, rv, rq, ro, heads, rotary._ref, st)
         del held
         return out
@@ -283,7 +285,18 @@ class KVCache:
         layer; returns out of the same shape.  scale: default head_dim ** -0.5.
         window: a row sees its last ``window`` tokens (0: all) and the first
         ``sinks`` of its slot.  Which slots the rows are of: see the class."""
-        return self._attend("attend", (), q, layer, seqs, row_start, max_rows, scale, window, sinks, out, stream)
+        st = self._on(stream)
+        _, qa, oa = self._args
+        rows, heads = self._rows(qa, "q", q)
+        if out is None:
+            with _on(stream):
+                out = self._torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        self._rows(oa, "out", out, heads, rows)
+        held = self._batch(rows, seqs, row_start, max_rows, stream)
+        rb, rq, ro = self._refs
+        self._call("attend", layer, rb, rq, ro, heads, self.head_dim ** -0.5 if scale is None else scale, window, sinks, st)
+        del held
+        return out
 
     def attend_shared(self, q, *, groups=None, least: int = None, layer: int = 0, seqs=None, row_start=None,
                       max_rows: int = None, scale: float = None, window: int = 0, sinks: int = 0, out=None, stream=None):
@@ -299,19 +312,16 @@ class KVCache:
         else:
             groups = self._index("groups", groups, None, stream)
             more = (groups.data_ptr(), groups.numel() - 1, -1 if least is None else least)
-        return self._attend("attend_shared", more, q, layer, seqs, row_start, max_rows, scale, window, sinks, out, stream)
-
-    def _attend(self, name, more, q, layer, seqs, row_start, max_rows, scale, window, sinks, out, stream):
         st = self._on(stream)
-        _, qa, oa = self._args[:3]
+        _, qa, oa = self._args
         rows, heads = self._rows(qa, "q", q)
         if out is None:
             with _on(stream):
                 out = self._torch.empty(q.shape, dtype=q.dtype, device=q.device)
         self._rows(oa, "out", out, heads, rows)
         held = self._batch(rows, seqs, row_start, max_rows, stream)
-        rb, rq, ro = self._refs[:3]
-        self._call(name, layer, rb, rq, ro, heads, self.head_dim ** -0.5 if scale is None else scale, window, sinks, *more, st)
+        rb, rq, ro = self._refs
+        self._call("attend_shared", layer, rb, rq, ro, heads, self.head_dim ** -0.5 if scale is None else scale, window, sinks, *more, st)
         del held
         return out
 
