@@ -61,20 +61,21 @@ def _lib():
         import torch
         from . import _check, lib
         _state = (torch, lib(), _check, {torch.float16: TYPE_F16, torch.bfloat16: TYPE_BF16},
-                  getattr(torch._C, "_cuda_getCurrentRawStream", None))
+                  getattr(torch._C, "_cuda_getCurrentRawStream", None),
+                  getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device))
     return _state
 
 
 def _call(fn, dev, stream, *args) -> None:
     """One call on a GPU's stream, with that GPU the current one."""
-    torch, _, check, _, raw = _state
+    torch, _, check, _, raw, current = _state
     if stream is not None:
         st = stream.cuda_stream
     elif raw is not None:
         st = raw(dev)
     else:
         st = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev:
+    if current() == dev:
         status = fn(*args, st)
     else:
         with torch.cuda.device(dev):
@@ -85,11 +86,10 @@ def _call(fn, dev, stream, *args) -> None:
 
 def _empty(shape, dtype, like, stream):
     """Memory that belongs to the stream the work runs on."""
-    torch = _state[0]
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
+    with _state[0].cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _count(name, n) -> None:
@@ -116,43 +116,42 @@ def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, quant=None, gr
     one fp32 scale for each ``group`` elements of a row (32, 64 or 128; 0: the row), max |y| / 127 or / 448.
     ``out`` (and ``scales``, contiguous [rows][groups]) may be given; out may be x.
     """
-    torch, L, _, types, _ = _lib()
-    if x.dim() != 2 or x.dtype not in types or not x.is_cuda:
-        raise ValueError(f"x must be float16 or bfloat16 [rows][n] on a GPU, not {x.dtype} {list(x.shape)} on {x.device}")
+    torch, L, _, types, *_ = _lib()
     shape, dtype, dev = x.shape, x.dtype, x.get_device()
+    if len(shape) != 2 or dtype not in types or dev < 0:
+        raise ValueError(f"x must be float16 or bfloat16 [rows][n] on a GPU, not {dtype} {list(shape)} on {x.device}")
     rows, n = shape
     _count("rows", rows)
-    d = _Norm()
-    d.x_stride = _matrix("x", x, shape, dtype, dev)
-    d.x, d.rows, d.n, d.dtype, d.group, d.eps = x.data_ptr(), rows, n, types[dtype], group, eps
+    w = r = s = None
+    r_stride = codes = 0
     if weight is not None:
         if weight.shape != (n,) or weight.dtype != dtype or weight.get_device() != dev or not weight.is_contiguous():
             raise ValueError(f"weight must be contiguous {dtype} [{n}] on {x.device}")
-        d.weight = weight.data_ptr()
+        w = weight.data_ptr()
     if residual is not None:
-        d.residual_stride = _matrix("residual", residual, shape, dtype, dev)
-        d.residual = residual.data_ptr()
+        r_stride = _matrix("residual", residual, shape, dtype, dev)
+        r = residual.data_ptr()
     if quant is None:
         kind = dtype
         if scales is not None:
             raise ValueError("scales are an output of quant")
     elif quant in (torch.int8, torch.float8_e4m3fn):
         kind = quant
-        d.codes = CODES_INT8 if quant == torch.int8 else CODES_E4M3
+        codes = CODES_INT8 if quant == torch.int8 else CODES_E4M3
         per = -(-n // group) if group > 0 else 1
         if scales is None:
             scales = _empty((rows, per), torch.float32, x, stream)
         elif scales.shape != (rows, per) or scales.dtype != torch.float32 or scales.get_device() != dev or not scales.is_contiguous():
             raise ValueError(f"scales must be contiguous float32 [{rows}][{per}] on {x.device}")
-        d.scales = scales.data_ptr()
+        s = scales.data_ptr()
     else:
         raise ValueError(f"quant must be None, torch.int8 or torch.float8_e4m3fn, not {quant}")
+    x_stride = _matrix("x", x, shape, dtype, dev)
     if out is None:
-        out = _empty(shape, kind, x, stream)
-        d.out_stride = n
+        out, out_stride = _empty(shape, kind, x, stream), n
     else:
-        d.out_stride = _matrix("out", out, shape, kind, dev)
-    d.out = out.data_ptr()
+        out_stride = _matrix("out", out, shape, kind, dev)
+    d = _Norm(x.data_ptr(), r, w, out.data_ptr(), s, x_stride, r_stride, out_stride, rows, n, types[dtype], codes, group, eps)
     _call(L.qgs_rms_norm, dev, stream, ctypes.byref(d))
     return out if quant is None else (out, scales)
 
@@ -223,7 +222,7 @@ class Rotary:
     def rotate(self, x, positions, out=None, stream=None):
         """x [rows][heads][head_dim] (fp16 or bf16) with row i turned to positions[i] (int32, on x's GPU); elements
         from ``dim`` on are copied.  Returns out, which may be x."""
-        torch, L, _, types, _ = _lib()
+        torch, L, _, types, *_ = _lib()
         if x.dim() != 3 or x.dtype not in types or not x.is_cuda:
             raise ValueError(f"x must be float16 or bfloat16 [rows][heads][head_dim] on a GPU, not {x.dtype} {list(x.shape)} on {x.device}")
         rows, heads, d = x.shape
@@ -257,7 +256,7 @@ def sample(logits, u, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, probs: 
     tokens' mass passes u times all of it.  NaN counts as -inf; a row of -inf alone gives -1.
     workspace: a uint8 tensor of at least sample_workspace(rows, vocab) bytes (default: made here).
     """
-    torch, L, _, types, _ = _lib()
+    torch, L, _, types, *_ = _lib()
     kind = types.get(logits.dtype, TYPE_F32 if logits.dtype == torch.float32 else None)
     if logits.dim() != 2 or kind is None or not logits.is_cuda:
         raise ValueError(f"logits must be float16, bfloat16 or float32 [rows][vocab] on a GPU, not {logits.dtype} "
@@ -303,7 +302,7 @@ def sample_workspace(rows: int, vocab: int) -> int:
     """Bytes of workspace that sample takes for so many rows and tokens."""
     got = _sizes.get((rows, vocab))
     if got is None:
-        _, L, check, _, _ = _lib()
+        _, L, check, *_ = _lib()
         n = ctypes.c_size_t()
         check(L.qgs_sample_workspace(rows, vocab, ctypes.byref(n)))
         if len(_sizes) > 256:
