@@ -30,8 +30,8 @@ template <bool BF> hipError_t by_chunks(NormArgs a, int codes, hipStream_t st) {
   while (a.team < chunks) a.team *= 2;
   if (a.team <= 32) go<BF, 1, true>(a, codes, NM_TEAMS / a.team, NM_TEAMS, st);
   else if (chunks <= 64) go<BF, 1, false>(a, codes, 1, threads(1), st);
-  else if (chunks <= 2048) go<BF, 2, false>(a, codes, 1, threads(2), st);
-  else if (chunks <= 3072) go<BF, 3, false>(a, codes, 1, threads(3), st);
+  else if (chunks <= 2 * 1024) go<BF, 2, false>(a, codes, 1, threads(2), st);
+  else if (chunks <= 3 * 1024) go<BF, 3, false>(a, codes, 1, threads(3), st);
   else go<BF, 4, false>(a, codes, 1, threads(4), st);
   return hipGetLastError();
 }

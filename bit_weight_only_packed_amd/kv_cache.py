@@ -66,6 +66,9 @@ class KVCache:
             kv.append(k, v, layer=layer)       # their keys and values
             out = kv.attend(q, layer=layer)    # attention of the new rows
 
+    (with rotary positions q = kv.append_rotated(q, k, v, rotary, layer=layer), and
+    kv.attend_shared where slots are long forks of one another).
+
     Rows of a call: ``seqs`` (int32 [n], default slots 0 .. n - 1) names the
     slots; with ``row_start`` (int32 [n + 1], with ``max_rows`` at least the
     largest count) entry j has rows row_start[j] .. row_start[j + 1] - 1, without

@@ -111,6 +111,14 @@ def test_sample_workspace(L):
     assert L.qgs_sample(None, 0x400000, need, None) == Q.QG_ERR_INVALID_ARG
 
 
+def test_cache_calls_without_a_cache(L):
+    from bit_weight_only_packed_amd import kv_cache as K
+    b, r = ctypes.byref(K._KvBatch(1, 1, 1, None, None)), ctypes.byref(K._KvRows(0x1000, 128, 128))
+    rot = ctypes.byref(B._Rotary(0x100000, 128, B.HALVES, 1.0))
+    refused(L, L.qgkv_append_rotary(None, 0, b, r, r, r, r, 8, rot, None), "handle")
+    refused(L, L.qgkv_attend_shared(None, 0, b, r, r, 8, 1.0, 0, 0, None, 1, -1, None), "handle")
+
+
 def test_binding_refuses_before_the_library():
     x = torch.zeros((2, 16), dtype=torch.float16)
     with pytest.raises(ValueError, match="GPU"):
