@@ -378,10 +378,13 @@ void k_attn_rows(AttnArgs a) {
   const bool live = rw < total, alive = r0 + wave * 32 < total;
   const int ri = live ? rw / a.G : 0;
   int pw0, pw1;  // first and last position of the wave's rows
+  bool counts = live;
   if constexpr (MODE == RW_PREFIX) {
-    // rows of many entries.  What comes of those that see nothing, or that max_rows leaves out and have no
-    // position, is not looked at: a position that masks nothing costs least.
+    // Rows of many entries.  What comes of those that see nothing, or that max_rows leaves out (-1), is not
+    // looked at: a position that masks nothing costs least, and a q of 0 raises no maximum, which would
+    // change the roundings of the wave's other rows.
     const int p = live ? a.share_pos[e.row0 + ri] : -1;
+    counts = p >= 0;
     r.pos = live ? ((unsigned)p < (unsigned)p1 ? p : p1) : -1;
     pw0 = live ? r.pos : 0x7FFFFFFF, pw1 = r.pos;
 #pragma unroll
@@ -397,7 +400,7 @@ void k_attn_rows(AttnArgs a) {
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) {
       r.Q[c] = *reinterpret_cast<const kv_u4*>(qp + 16 * c);
-      if (!live) r.Q[c] = kv_u4{0, 0, 0, 0};
+      if (!counts) r.Q[c] = kv_u4{0, 0, 0, 0};
     }
   }
 #pragma unroll

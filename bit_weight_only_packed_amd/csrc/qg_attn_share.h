@@ -53,7 +53,9 @@ __global__ __launch_bounds__(SP_T) void k_share_plan(ShareArgs a) {
         break;
       }
   const KvEntry e = entry[j];
-  for (int i = tid; i < e.rows; i += SP_T) a.pos[e.row0 + i] = e.pos + i;
+  // (-1: left out by max_rows; every row between a group's first and last has its position from this call)
+  const int all = kv_all_rows(a.b, e, j);
+  for (int i = tid; i < all; i += SP_T) a.pos[e.row0 + i] = i < e.rows ? e.pos + i : -1;
   __syncthreads();
   // -1: no constraint on the others (an entry that sees nothing)
   int tokens = -1;

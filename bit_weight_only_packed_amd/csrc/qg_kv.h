@@ -59,6 +59,10 @@ __device__ __forceinline__ KvEntry kv_entry(const KvDev& c, const KvBatchDev& b,
   e.rows = min(rows, b.max_rows);
   return e;
 }
+// the entry's rows with those that max_rows leaves out
+__device__ __forceinline__ int kv_all_rows(const KvBatchDev& b, const KvEntry& e, int j) {
+  return b.row_start ? min(max(b.row_start[j + 1], e.row0), b.rows) - e.row0 : e.rows;
+}
 
 // An entry of a page table, at an address that is the same for the whole wave, by a
 // scalar load: it neither takes a place among the vector loads in flight, which are

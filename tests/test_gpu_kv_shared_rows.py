@@ -1,0 +1,52 @@
+"""Attention of shared tokens beside rows that have no output: rows left out by max_rows and rows of idle slots leave
+the other rows' bits alone, whatever they hold and whatever calls went before."""
+from __future__ import annotations
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from _kv import rand  # noqa: E402
+from test_gpu_kv_shared import Forked, ints  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu_present():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D,G", [(64, 4), (128, 5), (256, 2)])
+def test_left_out_rows_leave_the_others_alone(dtype, D, G):
+    """Left-out rows of large scores, which would raise the running maximum of their wave; between the calls one that
+    gives the same rows of a call other positions."""
+    f = Forked([1500], [[30, 40, 35]], dtype, 16, 1, D, seed=16)
+    kv = f.gpu
+    q = rand((21, G, D), dtype, 12, 1.5)
+    live = torch.zeros(21, dtype=torch.bool, device="cuda")
+    live[[0, 1, 7, 8, 14, 15]] = True
+    q[~live] *= 20
+    kw = dict(row_start=ints(0, 7, 14, 21), max_rows=2)
+    first = kv.attend_shared(q, **kw)[live]
+    kv.attend_shared(rand((22, G, D), dtype, 1), seqs=ints(0, 1), row_start=ints(0, 11, 22), max_rows=11, window=20)
+    assert torch.equal(kv.attend_shared(q, **kw)[live], first)
+    for value in (0.0, 60000.0, float("nan"), float("inf")):
+        other = q.clone()
+        other[~live] = value
+        assert torch.equal(kv.attend_shared(other, **kw)[live], first), value
+
+
+def test_idle_rows_leave_the_others_alone():
+    f = Forked([1500], [[30, 40, 35, 9]], "f16", 16, 1, 64, seed=17)
+    kv = f.gpu
+    kv.trim(ints(1, 2))
+    q = rand((4, 8, 64), "f16", 3, 1.5)
+    first = kv.attend_shared(q)
+    assert (first[[1, 2]] == 0).all()
+    for value in (0.0, 60000.0, float("nan")):
+        other = q.clone()
+        other[[1, 2]] = value
+        got = kv.attend_shared(other)
+        assert torch.equal(got[[0, 3]], first[[0, 3]]) and (got[[1, 2]] == 0).all(), value
