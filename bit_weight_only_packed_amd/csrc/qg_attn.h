@@ -168,7 +168,7 @@ __device__ __forceinline__ void at_store(const AttnArgs& a, const KvEntry& e, in
 // the exponents of this kernel's weights have more than those of the many-row kernel
 // that made it, so that both mean the same.
 struct AtNoExtra {
-  static constexpr bool some = false;
+  static constexpr bool some = false, there = false;
   __device__ __forceinline__ at_f2 ml(int) const { return at_f2{0, 0}; }
   __device__ __forceinline__ at_f4 o(int, int) const { return at_f4{0, 0, 0, 0}; }
 };
@@ -206,11 +206,11 @@ template <int D> struct AtPrefix {
 // fac, tot, part: AT_JOIN_CAP floats of LDS each; n <= AT_JOIN_CAP.
 constexpr int AT_JOIN_CAP = 2720;  // (row, partial) pairs at a time; 4 floats of 512 threads fit as well
 //
-// extra: a partial of the rows' shared tokens comes to these, the last one of the order.
+// extra: a partial of the rows' shared tokens comes to these, the last one of the order (if there is one).
 template <bool BF, int D, int THREADS, class F, class X = AtNoExtra>
 __device__ __forceinline__ void at_join(const AttnArgs& a, __amdgpu_buffer_rsrc_t rs, const KvEntry& e, int head, int r0, int f0,
                                         int nrows, int ld, int own, float* fac, float* tot, float* part, F slot, X extra = X()) {
-  const int n = own + (X::some ? 1 : 0);
+  const int n = own + (X::some && extra.there ? 1 : 0);
   constexpr int NB = 16, NW = THREADS / 64;
   static_assert(4 * THREADS <= AT_JOIN_CAP, "part");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;

@@ -49,7 +49,7 @@ namespace qg {
 // the second for what a second workgroup of a CU brings over one (2 prompts of 1,500 rows
 // of 3,000 tokens, 8 q heads of 128 and one kv head: 67 us unshared, 76 at 23 tiles a part).
 constexpr int RW_MIN_TILES = 8, RW_LONG_TILES = 32;
-constexpr int RW_REST_TILES = 3;     // (of an entry's own tokens, which are few)
+constexpr int RW_REST_TILES = 3;     // (of an entry's own tokens behind shared ones, which are few)
 // parts of a block with so many shared tokens
 constexpr int RW_PREFIX_PART = 128, RW_PREFIX_LONG = 1024;
 __device__ __forceinline__ int rw_prefix_parts(int tokens, int splits, int splits1) {
@@ -303,7 +303,8 @@ template <int D, int MODE = RW_WHOLE> struct RowsBlock {
       shared = a.share[j];
       cut = tr.before(shared.tokens / S::KT);
     }
-    parts = max(min(a.splits, rw_parts(tr.n - cut, a.splits1, MODE == RW_REST ? RW_REST_TILES : RW_MIN_TILES)), 1);
+    // (an entry that shares nothing has the parts, and the bits, of a call without sharing)
+    parts = max(min(a.splits, rw_parts(tr.n - cut, a.splits1, MODE == RW_REST && shared.tokens > 0 ? RW_REST_TILES : RW_MIN_TILES)), 1);
   }
 };
 // a block of a group's rows with its shared tokens
@@ -531,7 +532,7 @@ void k_attn_rows(AttnArgs a) {
   r.l += __shfl_xor(r.l, 32);
   if (MODE != RW_PREFIX && parts == 1) {
     if (live) {
-      if constexpr (MODE == RW_REST) {
+      if constexpr (MODE == RW_REST) if (blk.shared.tokens > 0) {
         const AtPrefix<D> p(a, blk.shared, head, 0.0f);
         const at_f2 ml = p.ml(rw);
         const float m = r.m * a.scale_log2, M = at_safe(fmaxf(m, ml.x));
