@@ -115,14 +115,17 @@ __global__ __launch_bounds__(SP_T) void k_share_plan(ShareArgs a) {
   // blocks of the groups, one after another (few groups: one thread); none where all that sharing
   // would save is less than it costs
   if (tid == 0) {
-    int64_t read = 0;  // tokens that would be read without sharing
+    int64_t saved = 0;  // tokens less to read, in eighths
     for (int g = 0; g < a.ngroups; ++g) {
       int t = g_live[g] > 1 ? g_tokens[g] / SHARE_TILE * SHARE_TILE : 0;
       if (t < SHARE_MIN) t = 0;
       g_tokens[g] = t;
-      read += (a.window ? min((int64_t)t, (int64_t)a.window + a.sinks) : t) * g_live[g];
+      if (t == 0) continue;
+      const int64_t read = a.window ? min((int64_t)t, (int64_t)a.window + a.sinks) : t;
+      const int64_t waves = ((int64_t)(g_hi[g] - g_lo[g]) * a.G + 31) / 32;
+      saved += read * (8 * (g_live[g] + a.extra) - a.cost * waves);
     }
-    const bool pays = read >= a.least;
+    const bool pays = saved >= 8 * a.least;
     int base = 0;
     for (int g = 0; g < a.ngroups; ++g) {
       const int t = pays ? g_tokens[g] : 0;

@@ -155,7 +155,8 @@ struct ShareArgs {
   KvBatchDev b;
   const int32_t* groups;  // first entries of the groups and n (NULL: one group)
   int ngroups, G, blocks; // blocks: ShareBlocks that the call has room for
-  int64_t least;          // (entry, shared token) pairs below which nothing is shared
+  int64_t least;          // (entry, shared token) pairs below which nothing is shared, counted as in ShareRule
+  int extra, cost;
   int window, sinks;
   ShareEntry* share;
   ShareBlock* share_blocks;
@@ -166,15 +167,30 @@ struct ShareArgs {
 constexpr int SHARE_ROWS = 1 << 16;  // rows of a call that share tokens at most
 // shared tokens come in whole tiles of both kernels, and few of them are left to the entries
 constexpr int SHARE_TILE = 64, SHARE_MIN = 256;
-// Bytes of shared tokens, each counted once for every entry that reads it, from which on sharing
-// pays: what it costs is three launches and a second pass over the rows' results.  us of qgkv_attend /
-// with shared tokens, caches not warm, one row an entry (the entries' bytes together), and 8 rows an
-// entry for heads of 128, 4 for heads of 256:
-//   40 q, 8 kv heads of 128   8 x 8,192 tokens (273 MB) 36 / 46, 8 x 16,384 (542) 58 / 55, 64 x 4,096 (1,113) 89 / 70,
-//                             64 x 32,768 (8.7 GB) 1,254 / 134;  8 rows: 16 x 4,096 (278) 70 / 73, 32 x 4,096 (557) 95 / 96
-//   16 q, 2 kv heads of 256   8 x 16,384 (271) 54 / 83, 64 x 4,096 (557) 47 / 79; 4 rows: 32 x 4,096 (278) 97 / 99
-//   8 q, 8 kv heads of 64     8 x 16,384 (271) 31 / 41, 64 x 4,096 (557) 48 / 48
-constexpr int64_t SHARE_PAYS = 512 << 20;
+// Where sharing pays, when the caller sets no limit.  It saves its group's entries but one the reading of
+// the shared tokens, which the last-level cache serves at some 14 TB/s where entries read them nearly in
+// step and HBM at 4 where they are long; it costs three launches, partials, and the tokens' products with the
+// group's rows, in waves of 32 rows of a kv head.  So it is done where
+//   token bytes * sum over the groups of tokens * (entries + extra - cost / 8 * waves)  reaches  mib MiB,
+// with numbers for each head size and each kernel that attend would take, set from 385 measurements (heads of 64, 128 and 256; 1 to
+// 16 rows an entry; 2 to 128 entries of 2,048 to 131,072 tokens).  Of those sharing is taken where attend is
+// faster by 1 us at most (heads of 256: 22), attend where sharing is faster by 1 (many rows 20; heads of 256: 52).
+// us of attend / shared:
+//   40 q, 8 kv heads of 128   1 row: 8 x 16,384 tokens 60 / 63, 64 x 2,048 55 / 68, 64 x 4,096 76 / 73, 64 x 8,192 130 / 82,
+//                             2 x 131,072 262 / 180;  4 rows: 64 x 4,096 85 / 105, 64 x 8,192 135 / 125, 16 x 32,768 148 / 111;
+//                             8 rows: 16 x 16,384 142 / 115, 2 x 65,536 109 / 139
+//   16 q, 2 kv heads of 256   1 row: 64 x 4,096 57 / 89, 64 x 8,192 83 / 100, 16 x 32,768 157 / 111;  4 rows: 64 x 4,096 129 / 131,
+//                             16 x 32,768 199 / 174;  8 rows: 64 x 8,192 221 / 271
+//   8 q, 8 kv heads of 64     1 row: 8 x 16,384 42 / 48, 64 x 4,096 54 / 52, 16 x 16,384 60 / 49, 64 x 8,192 85 / 55
+// One limit of 512 MiB for all took sharing where it is slower by up to 40 us with one to 4 rows and 332 with 16.
+struct ShareRule {
+  int extra, cost;  // entries, eighths of an entry
+  int mib;
+};
+constexpr ShareRule share_rule(int D, bool few) {
+  if (few) return D == 64 ? ShareRule{2, 7, 480} : D == 128 ? ShareRule{3, 2, 1024} : ShareRule{2, 18, 544};
+  return D == 64 ? ShareRule{1, 1, 800} : D == 128 ? ShareRule{0, 3, 480} : ShareRule{1, 6, 320};
+}
 hipError_t launch_share_plan(const ShareArgs& a, hipStream_t st);
 
 // Rows of one kv head that the few-row kernel takes, (new rows) * (q heads per kv head).

@@ -387,12 +387,21 @@ qg_status qgkv_attend_shared(qg_kv_handle h, int32_t layer, const qg_kv_batch* b
   // without two entries in a group there is nothing to share; and calls of more rows than the
   // workspace has slots for are made of blocks that read the tokens many times either way
   const int64_t token = (int64_t)4 * a.c.kv_heads * h->d.head_dim;  // bytes of a token
-  if (least < 0) least = SHARE_PAYS;
+  ShareRule rule{0, 0, 0};
+  if (least < 0) {
+    rule = share_rule(h->d.head_dim, (int64_t)a.b.max_rows * a.G <= step_max_rows(h->d.head_dim));
+    least = (int64_t)rule.mib << 20;
+  }
   const int64_t seen = window ? std::min<int64_t>(a.c.cap, (int64_t)window + sinks) : a.c.cap;  // tokens of an entry at most
-  if (n_groups == a.b.n || a.b.rows > SHARE_ROWS || grid > kRowsSlots || a.b.n * seen < least / token)
+  // what an entry can bring at most, in eighths: it has a row at least, and without row_start all of its rows
+  const int64_t each = std::max<int64_t>(0, 8 - (int64_t)rule.cost * (b->row_start ? 1 : a.b.max_rows) * a.G / 32);
+  if (n_groups == a.b.n || a.b.rows > SHARE_ROWS || grid > kRowsSlots ||
+      seen * (a.b.n * each + 8 * (int64_t)n_groups * rule.extra) < 8 * (least / token))
     return attend(h, a, false, st);
   ShareArgs p = h->share;
   p.least = least / token;
+  p.extra = rule.extra;
+  p.cost = rule.cost;
   p.window = window;
   p.sinks = sinks;
   p.c = a.c;

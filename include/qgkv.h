@@ -188,9 +188,10 @@ qg_status qgkv_attend(qg_kv_handle h, int32_t layer, const qg_kv_batch* b, const
  * of their rows, in whole multiples of 64 tokens, 256 at least; entries that see nothing are left
  * aside.
  *   least  bytes of keys and values from which on it is done: of the shared tokens, each counted once for every
- *          entry that reads it, over all groups.  Below that the call costs less as
- *          qgkv_attend, which it then is but for some 11 us that finding out takes (none where
- *          n slots as long as their tables would hold less).  Negative: the measured 512 MiB; 0: always.
+ *          entry that reads it, over all groups.  0: always.  Negative: where it was measured to pay, which
+ *          goes by the head size, the entries, their rows and the bytes of the shared tokens.  Otherwise
+ *          the call is qgkv_attend, bit for bit, but for some 11 us that finding out takes (none where n
+ *          slots as long as their tables would hold too little).
  * Calls of very many rows (more than 512 / kv_heads blocks of 128 (row, q head of a kv head) pairs) are
  * qgkv_attend too.  The split of tokens depends on the group, so a row's bits may differ from
  * qgkv_attend's. */
