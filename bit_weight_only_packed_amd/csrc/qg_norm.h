@@ -131,8 +131,7 @@ template <bool BF, int C, int CODES, bool TEAM> __global__ __launch_bounds__(TEA
     for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(nm_at<BF>(h[c], i), nm_at<BF>(h[c], i), ss);
   ss = sum(ss);
   const float n = (float)a.n;
-  float rs = 1.0f / sqrtf(ss / n + a.eps);
-  int e = 0;  // the row is taken times 2^-e
+  float rs = 1.0f / sqrtf(ss / n + a.eps), rs2 = 1.0f;  // (rs2 is 1 but where one factor would lose bits)
   if (__builtin_expect(!(ss < __builtin_inff()), 0)) {
     // squares that overflow fp32 (bf16 values past 2^63)
     float top = 0.0f;
@@ -145,7 +144,7 @@ template <bool BF, int C, int CODES, bool TEAM> __global__ __launch_bounds__(TEA
       }
     top = most(top);
     if (top < __builtin_inff()) {  // (NaN and infinities stay as the formula has them)
-      e = ilogbf(top);
+      const int e = ilogbf(top);
       ss = 0.0f;
 #pragma unroll
       for (int c = 0; c < C; ++c)
@@ -155,23 +154,22 @@ template <bool BF, int C, int CODES, bool TEAM> __global__ __launch_bounds__(TEA
           ss = __builtin_fmaf(v, v, ss);
         }
       ss = sum(ss);
-      rs = 1.0f / sqrtf(ss / n + ldexpf(a.eps, -2 * e));
+      // The factor of the row as it is, in halves: h * 2^-e would have lost the small elements' bits.
+      rs = ldexpf(1.0f / sqrtf(ss / n + ldexpf(a.eps, -2 * e)), -(e / 2));
+      rs2 = ldexpf(1.0f, -(e - e / 2));
     }
   }
   const auto normed = [&](float (&y)[8], int c) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = nm_at<BF>(h[c], i);
-    if (__builtin_expect(e != 0, 0)) {
+    for (int i = 0; i < 8; ++i) y[i] = nm_at<BF>(h[c], i) * rs;
+    if (__builtin_expect(rs2 != 1.0f, 0)) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = ldexpf(y[i], -e);
+      for (int i = 0; i < 8; ++i) y[i] *= rs2;
     }
     if (a.weight) {
       const kv_u4 w = nm_load(a.weight + place(c), a.n - place(c));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = y[i] * rs * nm_at<BF>(w, i);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] *= rs;
+      for (int i = 0; i < 8; ++i) y[i] *= nm_at<BF>(w, i);
     }
   };
   if constexpr (CODES == QGS_SAME) {
