@@ -69,15 +69,19 @@ template <bool MAX> __device__ __forceinline__ float nm_team(float x, int T) {
   return x;
 }
 
+template <int CODES> constexpr float nm_top = CODES == QGS_INT8 ? 127.0f : 448.0f;
+
 // codes of 8 values: v / s rounded to nearest even.  |v| / s is at most the type's largest but
-// for the rounding of s, which the rounding of the code takes away.
+// for the rounding of s, which the rounding of the code takes away where s has its 24 bits.  (max / top may
+// have none: of 176 units of 2^-149 it is one, and |v| / s 176.  So there it is held to the largest.)
 template <int CODES> __device__ __forceinline__ kv_u2 nm_codes(const float (&v)[8], float s) {
   kv_u2 w = {0, 0};
   if (!(s > 0.0f)) return w;  // zeros, or a NaN scale
+  constexpr float TOP = nm_top<CODES>;
   float c[8];
   if (__builtin_expect(s < 0x1p-100f, 0)) {  // 1 / s may overflow
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = v[i] / s;
+    for (int i = 0; i < 8; ++i) c[i] = fminf(fmaxf(v[i] / s, -TOP), TOP);
   } else {
     const float r = 1.0f / s;
 #pragma unroll
@@ -184,7 +188,7 @@ template <bool BF, int C, int CODES, bool TEAM> __global__ __launch_bounds__(TEA
       nm_store(out + place(c), w, a.n - place(c));
     }
   } else {
-    constexpr float TOP = CODES == QGS_INT8 ? 127.0f : 448.0f;
+    constexpr float TOP = nm_top<CODES>;
     uint8_t* out = reinterpret_cast<uint8_t*>(a.out) + row * a.out_stride;
     // the largest magnitudes; a NaN counts as infinity
     const auto largest = [](const float (&v)[8], float m) {

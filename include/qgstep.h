@@ -33,8 +33,9 @@ enum { QGS_MAX_NORM = 32768, QGS_MAX_VOCAB = 1 << 20 };
  * codes QGS_SAME: out is y, of x's type.  QGS_INT8, QGS_E4M3: for each `group` elements
  * of a row (0: the whole row; 32, 64 or 128, the last may be short) a scale
  * s = max |y| / 127 (int8) or / 448 (e4m3: 4 exponent and 3 mantissa bits, no infinity),
- * fp32, and out holds y / s rounded to nearest even; a group of zeros has scale 0, one
- * that holds a NaN or infinity scale NaN, and both have codes 0.
+ * fp32, and out holds y / s rounded to nearest even, held to 127 or 448 (which it passes only where s
+ * is too small for fp32's 24 bits); a group of zeros has scale 0 (so has one whose s is below fp32's
+ * smallest number), one that holds a NaN or infinity scale NaN, and both have codes 0.
  * Rows may lie at any strides (elements) and need no alignment past their
  * type's; rows of one operand do not overlap.  out may be x (same pointer and
  * stride, QGS_SAME); no other operands share memory. */

@@ -11,6 +11,7 @@ from _kv import UNIT, np64  # noqa: E402
 from oracle import step_oracle as SO  # noqa: E402
 import bit_weight_only_packed_amd as Q  # noqa: E402
 
+CODES = {"int8": (torch.int8, 127.0), "e4m3": (torch.float8_e4m3fn, 448.0)}
 TINY = 2.0 ** -149  # fp32's smallest number
 
 
@@ -33,3 +34,33 @@ def test_small_elements_beside_large_ones(n, exp):
     ref = SO.rms_norm(np64(x), np64(w))
     # the output's rounding, the arithmetic of the mean and root, and half of fp32's smallest number times the weight
     assert (np.abs(np64(y) - ref) <= np.abs(ref) * (UNIT["bf16"] + 40 * 2.0 ** -24) + TINY / 2 * 2.0 ** 60).all()
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("low", [0, 3])
+def test_codes_whose_scale_has_few_bits(kind, low):
+    """A row with one large element and a group near 2^-140 (sqrt(96) 2^-70 times 8 m, 780 to 7,800 of the smallest
+    numbers, or an eighth of that): max / top is a handful of them, and y / scale may pass the type's largest, where
+    the code stays at it and keeps its sign."""
+    code, top = CODES[kind]
+    m = torch.arange(20, 200, 0.5, dtype=torch.float64) * 2.0 ** (-80 - low)
+    x = torch.zeros((m.numel(), 96), dtype=torch.float64)
+    x[:, 0] = 2.0 ** 70
+    x[:, 32], x[:, 33], x[:, 34], x[:, 40] = m * 8, -m * 8, m, -m * 4
+    x[:, 64], x[:, 65] = m * 32, -m * 32
+    x = x.to(torch.bfloat16).cuda()
+    codes, scales = Q.rms_norm(x, quant=code, group=32)
+    y = SO.rms_norm(np64(x))
+    c, s = np64(codes.float()), np64(scales)
+    assert (s[:, 1] < 8 * TINY).any() and (s[:, 1] > 0).any()
+    want = SO.group_scales(y, top, 32)
+    # y is fp32's, a product of roundings of 2^-23 of it and then to a multiple of 2^-149; so is the scale
+    assert (np.abs(s - want) <= want * 2.0 ** -21 + 1.5 * TINY).all()
+    wide = np.repeat(s, 32, 1)
+    step = 1.0 if kind == "int8" else np.exp2(np.maximum(np.floor(np.log2(np.maximum(np.abs(c), 2.0 ** -6))), -6) - 3)
+    held = np.clip(y, -top * wide, top * wide)
+    keep = wide > 0
+    assert (np.abs(c) <= top).all() and (c[~keep] == 0).all()
+    assert (np.abs(c * wide - held) <= wide * step / 2 * (1 + 2.0 ** -10) + np.abs(y) * 2.0 ** -20 + TINY)[keep].all()
+    big = keep & (np.abs(y) > 40 * TINY) & (np.abs(y) > wide)
+    assert big.any() and (np.sign(c) == np.sign(y))[big].all()
