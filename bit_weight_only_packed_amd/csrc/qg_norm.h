@@ -135,20 +135,27 @@ template <bool BF, int C, int CODES, bool TEAM> __global__ __launch_bounds__(TEA
     for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(nm_at<BF>(h[c], i), nm_at<BF>(h[c], i), ss);
   ss = sum(ss);
   const float n = (float)a.n;
-  float rs = 1.0f / sqrtf(ss / n + a.eps), rs2 = 1.0f;  // (rs2 is 1 but where one factor would lose bits)
-  if (__builtin_expect(!(ss < __builtin_inff()), 0)) {
-    // squares that overflow fp32 (bf16 values past 2^63)
-    float top = 0.0f;
+  const float mean = ss / n + a.eps;
+  float rs = 1.0f / sqrtf(mean), rs2 = 1.0f;  // (rs2 is 1 but where one factor would lose bits)
+  if (__builtin_expect(!(ss < __builtin_inff()) | (mean < 0x1p-100f), 0)) {
+    // squares that overflow fp32 (bf16 values past 2^63), or lose bits that count (with an eps as small as they are): the
+    // row's sum again, times 2^-2e
+    int e = -60;
+    bool again = true;
+    if (!(ss < __builtin_inff())) {
+      float top = 0.0f;
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+      for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float v = fabsf(nm_at<BF>(h[c], i));
-        top = fmaxf(top, v == v ? v : __builtin_inff());
-      }
-    top = most(top);
-    if (top < __builtin_inff()) {  // (NaN and infinities stay as the formula has them)
-      const int e = ilogbf(top);
+        for (int i = 0; i < 8; ++i) {
+          const float v = fabsf(nm_at<BF>(h[c], i));
+          top = fmaxf(top, v == v ? v : __builtin_inff());
+        }
+      top = most(top);
+      again = top < __builtin_inff();  // (NaN and infinities stay as the formula has them)
+      e = again ? ilogbf(top) : 0;
+    }
+    if (again) {
       ss = 0.0f;
 #pragma unroll
       for (int c = 0; c < C; ++c)

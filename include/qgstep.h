@@ -28,7 +28,7 @@ enum { QGS_MAX_NORM = 32768, QGS_MAX_VOCAB = 1 << 20 };
 /* Root-mean-square norm of rows of n elements.
  *   h = x + residual, rounded once to the type and stored in residual (NULL: h = x)
  *   y = h * weight / sqrt(mean(h^2) + eps)              (weight NULL: 1)
- * The mean is of the stored h, in fp32 (scaled where squares would overflow); h / sqrt(..) is fp32's, with
+ * The mean is of the stored h, in fp32 (scaled where squares would overflow or vanish); h / sqrt(..) is fp32's, with
  * the fewer bits of its numbers below 2^-126 there, and y, its product with weight, is rounded once.
  * codes QGS_SAME: out is y, of x's type.  QGS_INT8, QGS_E4M3: for each `group` elements
  * of a row (0: the whole row; 32, 64 or 128, the last may be short) a scale

@@ -36,6 +36,20 @@ def test_small_elements_beside_large_ones(n, exp):
     assert (np.abs(np64(y) - ref) <= np.abs(ref) * (UNIT["bf16"] + 40 * 2.0 ** -24) + TINY / 2 * 2.0 ** 60).all()
 
 
+@pytest.mark.parametrize("eps", [2.0 ** -149, 1e-44, 1e-40, 1e-36, 2.0 ** -101, 2.0 ** -99, 1e-20])
+@pytest.mark.parametrize("n", [40, 1000, 5120])
+def test_squares_too_small_for_fp32(eps, n):
+    """Rows of 2^-130 to 2^-40 with an eps no larger than their squares, which fp32 rounds away."""
+    g = torch.Generator().manual_seed(n)
+    x = torch.randn((19, n), generator=g, dtype=torch.float64) * torch.exp2(torch.arange(-130, -35, 5, dtype=torch.float64))[:, None]
+    x[3] = 0
+    x = x.to(torch.bfloat16).cuda()
+    ref = SO.rms_norm(np64(x), eps=float(np.float32(eps)))
+    y = np64(Q.rms_norm(x, eps=eps))
+    # the output's rounding, the arithmetic of the sum, root and products, half of bf16's smallest number
+    assert (np.abs(y - ref) <= np.abs(ref) * (UNIT["bf16"] + 40 * 2.0 ** -24) + 2.0 ** -134).all()
+
+
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
 @pytest.mark.parametrize("low", [0, 3])
 def test_codes_whose_scale_has_few_bits(kind, low):
