@@ -79,13 +79,20 @@ template <int CODES> __device__ __forceinline__ kv_u2 nm_codes(const float (&v)[
   if (!(s > 0.0f)) return w;  // zeros, or a NaN scale
   constexpr float TOP = nm_top<CODES>;
   float c[8];
-  if (__builtin_expect(s < 0x1p-100f, 0)) {  // 1 / s may overflow
+  if (__builtin_expect(s < 0x1p-80f, 0)) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) c[i] = fminf(fmaxf(v[i] / s, -TOP), TOP);
   } else {
-    const float r = 1.0f / s;
+    // The quotient as fp32 division rounds it: 1 / s in two parts gives it to one unit, and one step by the
+    // remainder brings it there (Markstein's theorem; the remainder is exact for quotients of 2^-11 and more, s
+    // being 2^-80 at least, and what is smaller has a code of 0 either way).  Against v r alone, which is 1.5 units
+    // off: 33 us and 32 (2,047 rows of 17,408 to e4m3).
+    const float r = 1.0f / s, r2 = __builtin_fmaf(-r, s, 1.0f) * r;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = v[i] * r;
+    for (int i = 0; i < 8; ++i) {
+      const float q = __builtin_fmaf(v[i], r, v[i] * r2);
+      c[i] = __builtin_fmaf(__builtin_fmaf(-q, s, v[i]), r, q);
+    }
   }
   if constexpr (CODES == QGS_INT8) {
 #pragma unroll

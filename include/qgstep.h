@@ -33,7 +33,7 @@ enum { QGS_MAX_NORM = 32768, QGS_MAX_VOCAB = 1 << 20 };
  * codes QGS_SAME: out is y, of x's type.  QGS_INT8, QGS_E4M3: for each `group` elements
  * of a row (0: the whole row; 32, 64 or 128, the last may be short) a scale
  * s = max |y| / 127 (int8) or / 448 (e4m3: 4 exponent and 3 mantissa bits, no infinity),
- * fp32, and out holds y / s rounded to nearest even, held to 127 or 448 (which it passes only where s
+ * fp32, and out holds y / s (of fp32 y, in fp32) rounded to nearest even, held to 127 or 448 (which it passes only where s
  * is too small for fp32's 24 bits); a group of zeros has scale 0 (so has one whose s is below fp32's
  * smallest number), one that holds a NaN or infinity scale NaN, and both have codes 0.
  * Rows may lie at any strides (elements) and need no alignment past their

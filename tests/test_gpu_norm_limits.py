@@ -7,7 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from _kv import UNIT, np64  # noqa: E402
+from _kv import DT, UNIT, np64  # noqa: E402
 from oracle import step_oracle as SO  # noqa: E402
 import bit_weight_only_packed_amd as Q  # noqa: E402
 
@@ -78,3 +78,31 @@ def test_codes_whose_scale_has_few_bits(kind, low):
     assert (np.abs(c * wide - held) <= wide * step / 2 * (1 + 2.0 ** -10) + np.abs(y) * 2.0 ** -20 + TINY)[keep].all()
     big = keep & (np.abs(y) > 40 * TINY) & (np.abs(y) > wide)
     assert big.any() and (np.sign(c) == np.sign(y))[big].all()
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("group", [32, 128])
+def test_codes_are_the_quotients_nearest(kind, dtype, group):
+    """Rows of ones have a norm of exactly 1 and y = weight, so every code is known: fp32's max / top and y / scale, rounded
+    to nearest even, ties among them (multiples of half a step of a largest value that the type's divides)."""
+    code, top = CODES[kind]
+    n = 32768
+    x = torch.ones((1, n), dtype=DT[dtype], device="cuda")
+    for seed in range(24):
+        g = torch.Generator().manual_seed(seed)
+        w = torch.randn(n, generator=g)
+        if seed % 2:  # multiples of 1 / 2 in groups whose largest is 127 / 2 (or 448 / 7) times a small whole number
+            m = torch.randint(1, 8, (n // group, 1), generator=g)
+            big = m * (63.5 if kind == "int8" else 64.0)
+            w = (torch.randint(-120, 121, (n // group, group), generator=g) * m / 4).clamp(-big, big)
+            w[:, :1] = big
+            w = w.reshape(-1)
+        w = w.to(DT[dtype])
+        codes, scales = Q.rms_norm(x, w.cuda(), eps=1e-30, quant=code, group=group)
+        y = w.float().reshape(-1, group)
+        s = y.abs().amax(1, keepdim=True) / torch.tensor(top)
+        assert torch.equal(scales.cpu().reshape(-1, 1), s)
+        want = y / s
+        want = torch.round(want).to(torch.int8) if kind == "int8" else want.to(code)
+        assert torch.equal(codes.cpu().float(), want.reshape(1, n).float()), seed
