@@ -1,4 +1,6 @@
 // k_sample.hip -- launchers of the sampling kernels (qg_sample.h).
+#include <algorithm>
+
 #include "qg_sample.h"
 
 namespace qg {
@@ -6,10 +8,10 @@ namespace qg {
 namespace {
 
 template <int TY> hipError_t go(const SampleArgs& a, hipStream_t st) {
-  for (int at = 0; at < a.rows; at += SAMPLE_ROWS) {
-    const unsigned rows = (unsigned)(a.rows - at < SAMPLE_ROWS ? a.rows - at : SAMPLE_ROWS);
+  for (int64_t at = 0; at < a.rows; at += SAMPLE_ROWS) {  // (at may pass 2^31 at the end)
+    const unsigned rows = (unsigned)std::min<int64_t>(a.rows - at, SAMPLE_ROWS);
     SampleArgs b = a;
-    b.logits = reinterpret_cast<const char*>(a.logits) + (int64_t)at * a.stride * (TY == QGS_F32 ? 4 : 2);
+    b.logits = reinterpret_cast<const char*>(a.logits) + at * a.stride * (TY == QGS_F32 ? 4 : 2);
     b.u += at, b.tokens += at;
     if (b.probs) b.probs += at;
     if (b.temperature) b.temperature += at;
@@ -51,7 +53,7 @@ void sample_parts(int rows, int vocab, int* parts, int* len) {
 //   32 rows   16,001   49 / 39, 20 / 18, 59 / 41     32,003  51 / 58, 20 / 29, 56 / 55
 //   128 rows  32,003   68 / 57, 28 / 29, 67 / 57     65,537  104 / 90, 48 / 53, 90 / 100
 //   256 rows  65,537   132 / 92, 68 / 57, 106 / 103  131,071 156 / 167, 107 / 106, 138 / 199
-bool sample_whole(int rows, int vocab) { return vocab <= 16384 || (vocab <= 65536 && vocab <= 256 * rows); }
+bool sample_whole(int rows, int vocab) { return vocab <= 16384 || (vocab <= 65536 && vocab <= 256 * (int64_t)rows); }
 
 hipError_t launch_sample(const SampleArgs& a, int type, hipStream_t st) {
   if (type == QGS_F16) return go<QGS_F16>(a, st);
