@@ -116,16 +116,23 @@ __device__ __forceinline__ void sm_table(double* tab) {
 struct SmScale {
   float top, per_bucket;
   double rate;         // log2(e) / temperature
+  // Temperatures so large that logits whose difference passes fp32 have weights, or so small that
+  // per_bucket does: buckets in fp64, for all of the row.
+  bool wide;
   const double* tab;
   __device__ __forceinline__ SmScale(float top_, float heat, const double* tab_) : top(top_), tab(tab_) {
     rate = 1.4426950408889634 / (double)heat;
     per_bucket = (float)(rate * (SM_BUCKETS / 44.0));
+    wide = !(per_bucket >= 0x1p-117f && per_bucket < __builtin_inff());
   }
   // Monotone in l: a rounded difference, times a constant, cut off.  SM_BUCKETS: a weight of 0.
   __device__ __forceinline__ int bucket(float l) const {
     if (l == top) return 0;
-    if (l == -__builtin_inff()) return SM_BUCKETS;
-    const float x = (top - l) * per_bucket;
+    float x = (top - l) * per_bucket;  // (infinite where l is -inf)
+    if (__builtin_expect(wide, 0)) {
+      if (l == -__builtin_inff() || top == __builtin_inff()) return SM_BUCKETS;
+      x = (float)(((double)top - (double)l) * (rate * (SM_BUCKETS / 44.0)));
+    }
     return x < (float)SM_BUCKETS ? (int)x : SM_BUCKETS;
   }
   // The weight of a logit in a bucket, in units of 2^-SM_BITS, before its rounding: 2^e = 2^(n / 128) 2^f
