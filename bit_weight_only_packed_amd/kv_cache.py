@@ -314,6 +314,8 @@ class KVCache:
             more = (None, 1, -1 if least is None else least)
         else:
             groups = self._index("groups", groups, None, stream)
+            if groups.numel() == 0:
+                raise ValueError("groups is empty: it holds the entries at which groups begin, and n")
             more = (groups.data_ptr(), groups.numel() - 1, -1 if least is None else least)
         st = self._on(stream)
         _, qa, oa = self._args

@@ -50,3 +50,13 @@ def test_idle_rows_leave_the_others_alone():
         other[[1, 2]] = value
         got = kv.attend_shared(other)
         assert torch.equal(got[[0, 3]], first[[0, 3]]) and (got[[1, 2]] == 0).all(), value
+
+
+def test_groups_that_hold_nothing_are_refused():
+    """Not taken for no groups at all, which is one of all entries."""
+    f = Forked([640], [[2, 9, 5]], "f16", 16, 1, 64, seed=18)
+    q = rand((3, 4, 64), "f16", 4)
+    for groups in ([], torch.empty(0, dtype=torch.int32, device="cuda")):
+        with pytest.raises(ValueError, match="groups"):
+            f.gpu.attend_shared(q, groups=groups)
+    assert f.gpu.attend_shared(q, groups=[0, 3]).shape == q.shape
