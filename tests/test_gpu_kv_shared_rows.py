@@ -2,13 +2,16 @@
 the other rows' bits alone, whatever they hold and whatever calls went before."""
 from __future__ import annotations
 
+from types import SimpleNamespace
+
 import pytest
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from _kv import rand  # noqa: E402
-from test_gpu_kv_shared import Forked, ints  # noqa: E402
+from _kv import UNIT, check_out, np64, rand  # noqa: E402
+from oracle import kv_oracle as KO  # noqa: E402
+from test_gpu_kv_shared import Always, Forked, ints  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -60,3 +63,34 @@ def test_groups_that_hold_nothing_are_refused():
         with pytest.raises(ValueError, match="groups"):
             f.gpu.attend_shared(q, groups=groups)
     assert f.gpu.attend_shared(q, groups=[0, 3]).shape == q.shape
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+def test_more_entries_than_the_plan_has_threads(rows):
+    """700 entries in two groups and some idle ones: a thread of the plan has several."""
+    n = 700
+    kv = Always(40 + 2 * n, 16, 1, 64, max_seqs=n + 1, max_pages=24)
+    kv.extend([0] * n + [320])
+    kv.append(rand((320, 1, 64), "f16", 1), rand((320, 1, 64), "f16", 2), seqs=[n])
+    kv.fork([n] * n, list(range(n)))
+    grow = torch.randint(rows, 9, (n + 1,), generator=torch.Generator().manual_seed(3), dtype=torch.int32)
+    grow[n] = 0
+    kv.extend(grow.cuda())
+    total = int(grow.sum())
+    start = torch.zeros(n + 1, dtype=torch.int32)
+    start[1:] = grow[:n].cumsum(0)
+    kv.append(rand((total, 1, 64), "f16", 4), rand((total, 1, 64), "f16", 5), seqs=list(range(n)), row_start=start.cuda(), max_rows=8)
+    kv.trim([5, 300, 699])
+    kv.check()
+    q = rand((n * rows, 2, 64), "f16", 6, 1.5)
+    seqs = torch.arange(n, dtype=torch.int32, device="cuda")
+    got = kv.attend_shared(q, seqs=seqs, groups=[0, 333, n])
+    plain = kv.attend(q, seqs=seqs)
+    assert not torch.equal(got, plain)
+    # both within 2 u of the definition in the root mean square, and some of them against it
+    err = (got.double() - plain.double()).square().mean().sqrt()
+    assert err <= 4 * UNIT["f16"] * plain.double().square().mean().sqrt()
+    ref = KO.Cache(np64(kv.pool), kv.tables.cpu().numpy(), kv.lens.cpu().numpy(), kv.refs.cpu().numpy())
+    for s in (0, 5, 255, 256, 332, 333, 511, 512, 699):
+        mine = slice(s * rows, (s + 1) * rows)
+        check_out(got[mine], ref.attend(0, [s], [rows], np64(q[mine]), 0.125), "f16", q[mine], SimpleNamespace(ref=ref), 0, [s], [rows], 0.125)
