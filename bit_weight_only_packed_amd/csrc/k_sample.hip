@@ -35,7 +35,8 @@ template <int TY> hipError_t go(const SampleArgs& a, hipStream_t st) {
 
 }  // namespace
 
-// A part is 2,048 tokens at least, one load of a thread; some 4,096 parts in all, 64 of a row at most.
+// Parts of some 2,048 tokens, one load of a thread (33 parts of 2,000 or fewer for a row of 66,000), or more where there
+// would be more than 64 of a row or some 4,096 in all.
 // us with 1,024 / 2,048 / 4,096 / 8,192 parts: 128 rows of 100,003 98 / 91 / 86 / 90, of 131,071 without limits
 // 69 / 61 / 59 / 67, 250 rows of 131,000 with top-k and top-p 147 / 138 / 149 / 177.
 void sample_parts(int rows, int vocab, int* parts, int* len) {

@@ -15,8 +15,8 @@
 //   k_attn_step, _rows  (SH, RW_REST) the other tokens, joined with that result
 //
 // Measured: one row each of 64 answers to 32,768 tokens, 9 to 1,500 tokens of their own, bf16, 40 q and 8 kv heads
-// of 128: 116 us (208 MB that it cannot do without, 43 GFLOP), as qgkv_attend 1,260.  The plan 9.4 us (some eight
-// dependent round trips), the shared tokens 69 (320 rows in three blocks of 128: 51 GFLOP computed, 750 TFLOP/s, what
+// of 128: 115 us (208 MB that it cannot do without, 43 GFLOP), as qgkv_attend 1,260.  The plan 9.4 us (some eight
+// dependent round trips), the shared tokens 71 (320 rows in three blocks of 128: 51 GFLOP computed, 720 TFLOP/s, what
 // the many-row kernel reaches on long windows; read from HBM once), their join 9, the rest 32 (76 MB; two or three
 // entries' beginnings and ends in each workgroup).
 #pragma once

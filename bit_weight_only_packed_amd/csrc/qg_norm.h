@@ -6,8 +6,9 @@
 // Bound.  HBM where rows are many: each operand is read once and each output written
 // once, and a row lives in registers between its sum and its outputs.  8,191 rows of 5,120 with the residual
 // (bf16): 53 us, 336 MB at 6.3 TB/s (some of the residual from the last-level cache); 2,047 rows of 17,408 to e4m3
-// with a scale for each 128: 37 us, 107 MB at 2.9 TB/s (80 registers a thread
-// with three chunks; with four, 100 of them and fewer waves, 55).
+// with a scale for each 128: 39 us, 107 MB at 2.8 TB/s.  There a row is a block of 12 waves, of which a CU holds
+// two (77 registers a thread: 6 waves a SIMD), and nothing of a block's is on its way while it sums its row
+// (with four chunks a thread, 97 registers, 55 us).
 // Where rows are few, the call: one round trip to memory, one sum over the workgroup, one store (one row of
 // 5,120: 3.2 us).
 #pragma once
@@ -86,7 +87,7 @@ template <int CODES> __device__ __forceinline__ kv_u2 nm_codes(const float (&v)[
     // The quotient as fp32 division rounds it: 1 / s in two parts gives it to one unit, and one step by the
     // remainder brings it there (Markstein's theorem; the remainder is exact for quotients of 2^-11 and more, s
     // being 2^-80 at least, and what is smaller has a code of 0 either way).  Against v r alone, which is 1.5 units
-    // off: 33 us and 32 (2,047 rows of 17,408 to e4m3).
+    // off: 33 us and 32 (2,047 rows of 17,408 to e4m3, from the last-level cache).
     const float r = 1.0f / s, r2 = __builtin_fmaf(-r, s, 1.0f) * r;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -109,7 +110,7 @@ template <int CODES> __device__ __forceinline__ kv_u2 nm_codes(const float (&v)[
 
 // Thread t of a row holds its chunks t, t + T, ... of 8 elements, as the 16-bit values that
 // they are.  A row is a workgroup's, or, where it is short (TEAM: the heads of q and k), a.team lanes'
-// of a wave: 60,000 rows of 128 elements 15.1 us, with a wave each 27.9.
+// of a wave: 60,000 rows of 128 elements with the residual (61 MB) 15.1 us, with a wave each 27.9.
 template <bool BF, int C, int CODES, bool TEAM> __global__ __launch_bounds__(TEAM ? NM_TEAMS : 1024) void k_rms_norm(NormArgs a) {
   __shared__ float lds[16];
   const int T = TEAM ? a.team : (int)blockDim.x, tid = TEAM ? (int)threadIdx.x & (T - 1) : (int)threadIdx.x;

@@ -5,7 +5,7 @@
 //   index up to which the kept mass passes u * (all of it).
 //
 // Which token comes out hangs on comparisons of sums, so the sums are exact: a weight is
-// fp64 (exp2, off by some 2^-52 of itself), rounded to a multiple of 2^-43, and weights are added as
+// fp64 (a table and a series, off by 2^-49 of itself at most), rounded to a multiple of 2^-43, and weights are added as
 // 64-bit integers.  Integer sums do not depend on their order, so they may meet by atomics.
 //
 // The order is never made whole.  A row's logits fall into SM_BUCKETS buckets by their distance
@@ -23,8 +23,8 @@
 //                  then the part that holds the picked one
 // Bound: the chain of dependent round trips (three arrivals of the parts among them) where rows are few, the
 // LDS additions and fp64 weights of every token where they are many; reading the logits is a small part.  One
-// row of 131,071 (top-k 50, top-p 0.95): 3.1 + 12.0 + 15.2 + 3.9 us; 128 rows of 100,003 with settings of every
-// kind: 9 + 24 + 32 + 22 us.  Rows that are short go whole to a workgroup each (k_sample_row), one launch.
+// row of 131,071 (top-k 50, top-p 0.95): 3.1 + 11.4 + 15.0 + 3.9 us; 128 rows of 100,003 with settings of every
+// kind: 9 + 23 + 33 + 23 us.  Rows that are short go whole to a workgroup each (k_sample_row), one launch.
 #pragma once
 #include "qg_attn.h"
 #include "qg_step.h"
@@ -136,7 +136,7 @@ struct SmScale {
     return x < (float)SM_BUCKETS ? (int)x : SM_BUCKETS;
   }
   // The weight of a logit in a bucket, in units of 2^-SM_BITS, before its rounding: 2^e = 2^(n / 128) 2^f
-  // with |f| <= 2^-8, and 2^f by its series to f^4 (the next term is below 2^-49): 15 instructions, where
+  // with |f| <= 2^-8, and 2^f by its series to f^4 (the next term is at most 2^-49.5): 15 instructions, where
   // exp2 takes some 40 (one row of 131,071 by one workgroup: 91 us against 108).
   __device__ __forceinline__ double scaled(float l) const {
     if (l == top) return (double)(1ull << SM_BITS);  // (infinities among them)

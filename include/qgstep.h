@@ -97,9 +97,9 @@ qg_status qgs_rotate(const qgs_rows* d, const qgs_rotary* rotary, void* stream);
  * never picked, and a row of nothing else gives token -1 and prob 0.  (top_k <= 0, top_p
  * >= 1 or NaN, min_p <= 0 or NaN: no such limit.  u is held to [0, 1).)
  *
- * Weights are computed in fp64 and held as multiples of 2^-43 (2^-44 of the largest is
- * the most that one is off, and tokens below that are not picked); their sums are exact,
- * so results depend on nothing but the row. */
+ * Weights are computed in fp64 and held as multiples of 2^-43 (2^-44 of the largest and 2^-49 of
+ * itself is the most that one is off, and tokens below 2^-44 are not picked); their sums are
+ * exact, so results depend on nothing but the row. */
 typedef struct {
   const void* logits;
   int64_t stride;           /* elements from a row to the next */
